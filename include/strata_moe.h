@@ -36,6 +36,7 @@
  *     (T * K + 15 * E) * max(H, I) * 2 bytes < 2^31 (and x below 2 GiB), which
  *     at H = 2560, K = 10, E = 512 allows up to about 41,000 tokens; longer
  *     prompts run as several chunks (the pages' prompt path is chunked too).
+ *     (strata_moe_decode, for a decode batch, takes at most 64 tokens.)
  *   - Thread safety: calls may come from several host threads; calls that
  *     share the library-owned workspace of one device (the default when no
  *     workspace was set) must not overlap on different streams.
@@ -327,6 +328,96 @@ int strata_moe_ring_destroy(strata_moe_ring* ring);
  * host layout other than the one above, or blobs that are not pinned. */
 int strata_moe_prefill_streamed(const float* x, const float* router_w, const strata_moe_experts* experts,
                                 strata_moe_ring* ring, int64_t T, int32_t K, float* out, void* stream);
+
+/* ------------------------------------- low-rank adapters of many requests */
+
+/* The adapters that the requests of a call may carry, beside a projection
+ * that all of them share (y = x W): adapter a adds
+ *   scale[a] * B_a (A_a x)
+ * to the rows of its requests.
+ *   a:     [n_adapter][rank][in_dim]   row-major, of the type `dtype`
+ *   b:     [n_adapter][out_dim][rank]
+ *   scale: [n_adapter] fp32, or NULL for 1
+ *   ranks: [n_adapter] int32, or NULL: adapter a uses the first ranks[a] rows
+ *          of A_a and columns of B_a (clamped to [0, rank]; the rest is not
+ *          read into any result, so it may hold anything); NULL means rank.
+ * Sizes: 1 <= n_adapter <= 65536, 1 <= rank <= 256, in_dim and out_dim in
+ * [1, 65536].  a and b are aligned to their element.  Products are exact or
+ * rounded to fp32, and every sum is held in fp32. */
+typedef struct strata_moe_adapters {
+    int32_t n_adapter;
+    int32_t rank;
+    int32_t in_dim;
+    int32_t out_dim;
+    int32_t dtype; /* STRATA_MOE_ADAPTER_F32, _F16 or _BF16 */
+    const void* a;
+    const void* b;
+    const float* scale;
+    const int32_t* ranks;
+} strata_moe_adapters;
+
+#define STRATA_MOE_ADAPTER_F32 1
+#define STRATA_MOE_ADAPTER_F16 2
+#define STRATA_MOE_ADAPTER_BF16 3
+
+/* Device workspace of a strata_moe_adapt call of T tokens.  Errors: EINVAL
+ * for sizes outside the limits above or T outside [0, 2^24], EUNSUPPORTED for
+ * an unknown dtype. */
+int strata_moe_adapt_workspace_bytes(int64_t T, const strata_moe_adapters* adapters, size_t* bytes);
+
+/* out[t] = y[t] + scale_a B_a (A_a x[t]) with a = ids[t]; out[t] = y[t] where
+ * ids[t] is outside [0, n_adapter) (a request without an adapter: -1).
+ *   x   [T] rows of in_dim fp32, x_stride floats apart
+ *   ids [T] int32; rows of one request next to each other share the reads of
+ *       its adapter, any order is right
+ *   y   [T] rows of out_dim fp32, y_stride apart: the shared projection's output
+ *   out [T] rows of out_dim fp32, out_stride apart; may be y itself (the same
+ *       pointer and stride), and must not overlap x or y otherwise
+ * Strides are at least the row's width (y and out are only read or written
+ * within it); all rows are 4-byte aligned.  The shared projection may be any:
+ * the layer itself (after strata_moe_prefill, y = its output), the router, or
+ * one outside this library.  workspace: caller-owned, 256-byte aligned,
+ * strata_moe_adapt_workspace_bytes() bytes, uninitialised; calls in flight
+ * together (and graphs that may replay together) each need their own.  The
+ * call only enqueues kernels, so it can be captured.  Repeated calls give the
+ * same bits.  Errors: EINVAL for sizes, NULL pointers, alignment, strides or
+ * overlap, ENOMEM for a workspace that is too small. */
+int strata_moe_adapt(const float* x, int64_t x_stride, const int32_t* ids, const strata_moe_adapters* adapters,
+                     int64_t T, const float* y, int64_t y_stride, float* out, int64_t out_stride, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------- the layer for a few tokens */
+
+#define STRATA_MOE_DECODE_MAX_TOKENS 64
+
+/* Device workspace of a strata_moe_decode call of T tokens (adapters may be
+ * NULL).  Errors: those of strata_moe_decode's size checks. */
+int strata_moe_decode_workspace_bytes(int64_t T, int32_t K, const strata_moe_experts* experts,
+                                      const strata_moe_adapters* adapters, size_t* bytes);
+
+/* The layer of strata_moe_prefill for 0 <= T <= STRATA_MOE_DECODE_MAX_TOKENS
+ * tokens (a decode batch, a window of drafted tokens): the same definition
+ * (routing of the exact logits, int8 rounding of x and H, the 2-bit experts,
+ * the optional router bias and shared expert) in kernels for few rows.  The
+ * sums over H and I are held in fp64 here, so the H codes are those of exact
+ * sums; strata_moe_prefill's may differ from them at rounding ties, and its
+ * output with them (by up to about 1e-4 of the largest output).
+ *   adapters, adapter_ids [T] int32: NULL, or the requests' adapters beside
+ *   the whole layer (in_dim = out_dim = hidden), added to out as
+ *   strata_moe_adapt does.
+ * Unlike strata_moe_prefill the call takes its workspace from the caller
+ * (256-byte aligned, strata_moe_decode_workspace_bytes() bytes,
+ * uninitialised), so calls on different streams may overlap if each has its
+ * own; graphs that may replay together need one each, too.  It only enqueues
+ * kernels (no allocation, no wait), so it can be captured, and repeated calls
+ * give the same bits.  experts->flags and router_prepared are checked but
+ * not used; strata_moe_timing does not see these calls.  x, out and
+ * shared_gate are 16-byte aligned; out must not overlap x.  Errors: those of
+ * strata_moe_prefill, plus EINVAL for T above the limit or adapters of other
+ * widths and ENOMEM for a workspace that is too small. */
+int strata_moe_decode(const float* x, const float* router_w, const strata_moe_experts* experts, int64_t T, int32_t K,
+                      const strata_moe_adapters* adapters, const int32_t* adapter_ids, float* out, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* ----------------------------------------------------------------- timing */
 

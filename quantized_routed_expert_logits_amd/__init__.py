@@ -57,6 +57,11 @@ class DebugStruct(ctypes.Structure):
     _fields_ = [(name, _P) for name in ("ids", "p", "offsets", "src", "slot", "qx", "sx", "qh", "sh")]
 
 
+class AdaptersStruct(ctypes.Structure):
+    _fields_ = [("n_adapter", _i32), ("rank", _i32), ("in_dim", _i32), ("out_dim", _i32), ("dtype", _i32),
+                ("a", _P), ("b", _P), ("scale", _P), ("ranks", _P)]
+
+
 def _sig(name, args, res=ctypes.c_int):
     f = getattr(_lib, name)
     f.argtypes = args
@@ -86,6 +91,13 @@ _sig("strata_moe_ring_bytes", [_i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)
 _sig("strata_moe_ring_create", [_i32, _i32, _i32, _P, ctypes.c_size_t, _P, ctypes.POINTER(_P)])
 _sig("strata_moe_ring_destroy", [_P])
 _sig("strata_moe_prefill_streamed", [_P, _P, ctypes.POINTER(ExpertsStruct), _P, _i64, _i32, _P, _P])
+_sig("strata_moe_adapt_workspace_bytes", [_i64, ctypes.POINTER(AdaptersStruct), ctypes.POINTER(ctypes.c_size_t)])
+_sig("strata_moe_adapt", [_P, _i64, _P, ctypes.POINTER(AdaptersStruct), _i64, _P, _i64, _P, _i64, _P,
+                          ctypes.c_size_t, _P])
+_sig("strata_moe_decode_workspace_bytes", [_i64, _i32, ctypes.POINTER(ExpertsStruct), ctypes.POINTER(AdaptersStruct),
+                                           ctypes.POINTER(ctypes.c_size_t)])
+_sig("strata_moe_decode", [_P, _P, ctypes.POINTER(ExpertsStruct), _i64, _i32, ctypes.POINTER(AdaptersStruct), _P, _P,
+                           _P, ctypes.c_size_t, _P])
 _sig("strata_moe_timing", [ctypes.c_int, _i32])
 _sig("strata_moe_timing_kinds", [])
 _sig("strata_moe_timing_name", [ctypes.c_int], ctypes.c_char_p)
@@ -99,9 +111,12 @@ EXPORTED = [
     "strata_moe_quantize", "strata_moe_gate_up", "strata_moe_down", "strata_moe_timing",
     "strata_moe_timing_kinds", "strata_moe_timing_name", "strata_moe_timing_read",
     "strata_moe_ring_bytes", "strata_moe_ring_create", "strata_moe_ring_destroy", "strata_moe_prefill_streamed",
-    "strata_moe_prefill_noalloc",
+    "strata_moe_prefill_noalloc", "strata_moe_adapt_workspace_bytes", "strata_moe_adapt",
+    "strata_moe_decode_workspace_bytes", "strata_moe_decode",
 ]
 NOALLOC_SCRATCH_BYTES = 512 << 20  # STRATA_MOE_NOALLOC_SCRATCH_BYTES
+DECODE_MAX_TOKENS = 64             # STRATA_MOE_DECODE_MAX_TOKENS
+ADAPTER_DTYPES = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}  # STRATA_MOE_ADAPTER_*
 
 
 def library() -> ctypes.CDLL:
@@ -476,6 +491,132 @@ def strata_moe_prefill_debug(x, router_w, experts: Experts, K: int, out, stream=
                                          ctypes.byref(dbg), _stream(stream)), "strata_moe_prefill_debug")
     d["out"] = out
     return d
+
+
+# ------------------------------------------- adapters and the few-token layer
+class Adapters:
+    """Low-rank adapters of many requests beside a projection they share:
+    adapter n adds scale[n] * b[n] @ (a[n] @ x[t]) to the rows of its requests.
+
+    a [n][rank][in_dim] and b [n][out_dim][rank] of one dtype (float32,
+    float16 or bfloat16); scale [n] float32 or None (1); ranks [n] int32 or
+    None: adapter n uses its first ranks[n] rows of a and columns of b."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor | None = None,
+                 ranks: torch.Tensor | None = None):
+        if not isinstance(a, torch.Tensor) or not isinstance(b, torch.Tensor) or a.dim() != 3 or b.dim() != 3:
+            raise ValueError("a must be [n][rank][in_dim] and b [n][out_dim][rank]")
+        if a.dtype not in ADAPTER_DTYPES:
+            raise TypeError(f"adapters must be one of {sorted(str(d) for d in ADAPTER_DTYPES)}, got {a.dtype}")
+        n, rank, in_dim = a.shape
+        _expect(b, "b", (n, b.shape[1], rank), a.dtype)
+        if scale is not None:
+            _expect(scale, "scale", (n,), torch.float32)
+        if ranks is not None:
+            _expect(ranks, "ranks", (n,), torch.int32)
+        for name, t in (("a", a), ("b", b), ("scale", scale), ("ranks", ranks)):
+            if t is not None and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t is not None and t.device != a.device:
+                raise ValueError("arguments are on different devices")
+        self.a, self.b, self.scale, self.ranks = a, b, scale, ranks
+        self.n_adapter, self.rank, self.in_dim, self.out_dim = n, rank, in_dim, b.shape[1]
+        self.struct = AdaptersStruct(n, rank, in_dim, self.out_dim, ADAPTER_DTYPES[a.dtype], a.data_ptr(), b.data_ptr(),
+                                     None if scale is None else scale.data_ptr(),
+                                     None if ranks is None else ranks.data_ptr())
+
+
+def strata_moe_adapt_workspace_bytes(T: int, adapters: Adapters) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.strata_moe_adapt_workspace_bytes(T, ctypes.byref(adapters.struct), ctypes.byref(b)),
+           "strata_moe_adapt_workspace_bytes")
+    return b.value
+
+
+def _rows(t, name: str, T: int, width: int):
+    """A [T][width] fp32 tensor with contiguous rows -> its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    _dtype(t, torch.float32, name)
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != width:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, width)}")
+    if T <= 1:
+        if width > 1 and t.stride(1) != 1 and T == 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return width
+    if (width > 1 and t.stride(1) != 1) or t.stride(0) < width:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(0)
+
+
+def _with_workspace(call, device, workspace, nbytes, stream):
+    """call(workspace pointer, its bytes, stream) with the tensors' device
+    current and the given workspace, or one allocated on the stream."""
+    with torch.cuda.device(device):
+        if workspace is None:
+            s = torch.cuda.current_stream(device) if stream is None else stream
+            with torch.cuda.stream(s):
+                workspace = torch.empty(max(nbytes(), 1), dtype=torch.uint8, device=device)
+        elif workspace.device != device:
+            raise ValueError("the workspace is on another device")
+        return call(_ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def strata_moe_adapt(x: torch.Tensor, ids: torch.Tensor, adapters: Adapters, y: torch.Tensor, out: torch.Tensor,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = y[t] + the adapter ids[t]'s rows of x[t] (ids[t] < 0: y[t]).  x, y and out may have padded rows;
+    out may be y.  workspace: strata_moe_adapt_workspace_bytes() bytes for this call alone, or None to allocate it."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D [T][in_dim] tensor")
+    if not isinstance(adapters, Adapters):
+        raise TypeError("adapters must be an Adapters object")
+    T = x.shape[0]
+    xs, ys, os_ = (_rows(t, n, T, w) for t, n, w in ((x, "x", adapters.in_dim), (y, "y", adapters.out_dim),
+                                                     (out, "out", adapters.out_dim)))
+    _expect(ids, "ids", (T,), torch.int32)
+    _one_device(x=x, ids=ids, y=y, out=out, a=adapters.a)
+    _ptr(ids)
+
+    def call(ws, nbytes, st):
+        _check(_lib.strata_moe_adapt(x.data_ptr(), xs, ids.data_ptr(), ctypes.byref(adapters.struct), T, y.data_ptr(),
+                                     ys, out.data_ptr(), os_, ws, nbytes, st), "strata_moe_adapt")
+        return out
+
+    return _with_workspace(call, x.device, workspace, lambda: strata_moe_adapt_workspace_bytes(T, adapters), stream)
+
+
+def strata_moe_decode_workspace_bytes(T: int, K: int, experts: Experts, adapters: Adapters | None = None) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.strata_moe_decode_workspace_bytes(T, K, ctypes.byref(experts.struct),
+                                                  None if adapters is None else ctypes.byref(adapters.struct),
+                                                  ctypes.byref(b)), "strata_moe_decode_workspace_bytes")
+    return b.value
+
+
+def strata_moe_decode(x: torch.Tensor, router_w: torch.Tensor, experts: Experts, K: int, out: torch.Tensor,
+                      adapters: Adapters | None = None, adapter_ids: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The layer for at most DECODE_MAX_TOKENS tokens, with the requests' adapters beside it if given.  workspace:
+    strata_moe_decode_workspace_bytes() bytes for this call alone, or None to allocate it."""
+    if getattr(experts, "streamed", False):
+        raise TypeError("the few-token layer reads resident experts: use Experts")
+    T = _check_layer_args(x, router_w, experts, out)
+    if (adapters is None) != (adapter_ids is None):
+        raise ValueError("adapters and adapter_ids come together")
+    if adapters is not None:
+        if not isinstance(adapters, Adapters):
+            raise TypeError("adapters must be an Adapters object")
+        _expect(adapter_ids, "adapter_ids", (T,), torch.int32)
+        _one_device(x=x, adapter_ids=adapter_ids, a=adapters.a)
+
+    def call(ws, nbytes, st):
+        _check(_lib.strata_moe_decode(_ptr(x), _ptr(router_w), ctypes.byref(experts.struct), T, K,
+                                      None if adapters is None else ctypes.byref(adapters.struct), _ptr(adapter_ids),
+                                      _ptr(out), ws, nbytes, st), "strata_moe_decode")
+        return out
+
+    return _with_workspace(call, x.device, workspace,
+                           lambda: strata_moe_decode_workspace_bytes(T, K, experts, adapters), stream)
 
 
 # -------------------------------------------------------------- single steps

@@ -12,6 +12,7 @@
 // then adds every token's K rows in k order (deterministic).
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -70,14 +71,20 @@ int hip_fail(hipError_t e, const char* what) {
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // ----------------------------------------------------------------- device
+// Devices already found to be gfx950 (the properties of a device do not
+// change, and reading them costs more than a small call's launches).
+std::atomic<bool> g_supported[64];
+
 int check_device() {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) return fail(STRATA_MOE_EUNSUPPORTED, "no HIP device");
+    if (dev >= 0 && dev < 64 && g_supported[dev].load(std::memory_order_relaxed)) return 0;
     hipDeviceProp_t prop;
     if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return fail(STRATA_MOE_EUNSUPPORTED, "no HIP device");
     if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
         return fail(STRATA_MOE_EUNSUPPORTED, "device %d is %s; this library is built for gfx950 only", dev,
                     prop.gcnArchName);
+    if (dev >= 0 && dev < 64) g_supported[dev].store(true, std::memory_order_relaxed);
     return 0;
 }
 
@@ -652,6 +659,87 @@ int run_layer(const float* x, const float* wr, const strata_moe_experts* ex, int
     return 0;
 }
 
+// ------------------------------------------- adapters and few-token calls
+int check_adapters(const strata_moe_adapters* ad) {
+    if (!ad) return fail(STRATA_MOE_EINVAL, "adapters is NULL");
+    if (ad->n_adapter < 1 || ad->n_adapter > 65536)
+        return fail(STRATA_MOE_EINVAL, "n_adapter %d outside [1, 65536]", ad->n_adapter);
+    if (ad->rank < 1 || ad->rank > kAdapterMaxRank)
+        return fail(STRATA_MOE_EINVAL, "rank %d outside [1, %d]", ad->rank, kAdapterMaxRank);
+    if (ad->in_dim < 1 || ad->in_dim > 65536 || ad->out_dim < 1 || ad->out_dim > 65536)
+        return fail(STRATA_MOE_EINVAL, "in_dim %d or out_dim %d outside [1, 65536]", ad->in_dim, ad->out_dim);
+    if (ad->dtype != STRATA_MOE_ADAPTER_F32 && ad->dtype != STRATA_MOE_ADAPTER_F16 &&
+        ad->dtype != STRATA_MOE_ADAPTER_BF16)
+        return fail(STRATA_MOE_EUNSUPPORTED, "unknown adapter dtype %d", ad->dtype);
+    return 0;
+}
+
+int check_adapter_pointers(const strata_moe_adapters* ad) {
+    const size_t el = ad->dtype == STRATA_MOE_ADAPTER_F32 ? 4 : 2;
+    if (!ad->a || !ad->b) return fail(STRATA_MOE_EINVAL, "adapter matrix pointer is NULL");
+    if (!aligned(ad->a, el) || !aligned(ad->b, el) || (ad->scale && !aligned(ad->scale, 4)) ||
+        (ad->ranks && !aligned(ad->ranks, 4)))
+        return fail(STRATA_MOE_EINVAL, "adapter arrays must be aligned to their elements");
+    return 0;
+}
+
+constexpr int64_t kAdaptMaxTokens = (int64_t)1 << 24;
+
+int check_adapt_tokens(int64_t T) {
+    if (T < 0 || T > kAdaptMaxTokens)
+        return fail(STRATA_MOE_EINVAL, "T = %lld outside [0, %lld]", (long long)T, (long long)kAdaptMaxTokens);
+    return 0;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+    if (!ws || !aligned(ws, 256)) return fail(STRATA_MOE_EINVAL, "the workspace must be 256-byte aligned device memory");
+    if (have < need) return fail(STRATA_MOE_ENOMEM, "workspace of %zu bytes given, %zu needed", have, need);
+    return 0;
+}
+
+// Bytes from the first to past the last element of T rows `stride` apart.
+uintptr_t row_span(int64_t T, int64_t stride, int64_t width) { return (uintptr_t)(((T - 1) * stride + width) * 4); }
+
+bool overlap(const void* a, uintptr_t an, const void* b, uintptr_t bn) {
+    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+    return pa < pb + bn && pb < pa + an;
+}
+
+AdaptLaunch adapt_launch(const strata_moe_adapters* ad, const int32_t* ids, int64_t T, char* ws) {
+    AdaptLaunch l{};
+    l.ids = ids;
+    l.a = ad->a;
+    l.b = ad->b;
+    l.scale = ad->scale;
+    l.ranks = ad->ranks;
+    l.n_adapter = ad->n_adapter;
+    l.rank = ad->rank;
+    l.in_dim = ad->in_dim;
+    l.out_dim = ad->out_dim;
+    l.dtype = ad->dtype;
+    l.T = T;
+    l.workspace = ws;
+    return l;
+}
+
+// The size checks of a few-token call, and its workspace: the layer's, then
+// the adapters'.
+int decode_sizes(int64_t T, int32_t K, const strata_moe_experts* ex, const strata_moe_adapters* ad, size_t* layer,
+                 size_t* adapters) {
+    TRY(check_layer(T, K, ex));
+    if (T > kDecodeMaxTokens)
+        return fail(STRATA_MOE_EINVAL, "T = %lld above the few-token limit of %d", (long long)T, kDecodeMaxTokens);
+    if (ad) {
+        TRY(check_adapters(ad));
+        if (ad->in_dim != ex->hidden || ad->out_dim != ex->hidden)
+            return fail(STRATA_MOE_EINVAL, "adapters of %d -> %d beside a layer of %d", ad->in_dim, ad->out_dim,
+                        ex->hidden);
+    }
+    *layer = decode_workspace((int32_t)T, ex->hidden, ex->n_expert, K, ex->ffn, ex->shared_gate != nullptr);
+    *adapters = ad ? adapt_workspace(T, ad->rank) : 0;
+    return 0;
+}
+
 // The scratch of strata_moe_prefill_noalloc: one array per GPU the library
 // runs on, loaded with the code object and held until the process ends.  Its
 // device address comes from hipGetSymbolAddress once per device (the array's
@@ -1127,6 +1215,109 @@ int strata_moe_down(const int8_t* qh, const float* sh, const int32_t* offsets, c
         HIP_TRY(launch_gemv(l, cl, n, E, all, st), "GEMV launch");
     }
     HIP_TRY(launch_combine(dm, slot, T, K, H, out, st), "combine launch");
+    return 0;
+}
+
+int strata_moe_adapt_workspace_bytes(int64_t T, const strata_moe_adapters* adapters, size_t* bytes) {
+    g_err.clear();
+    if (!bytes) return fail(STRATA_MOE_EINVAL, "bytes is NULL");
+    TRY(check_adapters(adapters));
+    TRY(check_adapt_tokens(T));
+    *bytes = adapt_workspace(T, adapters->rank);
+    return 0;
+}
+
+int strata_moe_adapt(const float* x, int64_t x_stride, const int32_t* ids, const strata_moe_adapters* adapters,
+                     int64_t T, const float* y, int64_t y_stride, float* out, int64_t out_stride, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    size_t need = 0;
+    TRY(strata_moe_adapt_workspace_bytes(T, adapters, &need));
+    const int64_t max_stride = (int64_t)1 << 32;
+    if (x_stride < adapters->in_dim || y_stride < adapters->out_dim || out_stride < adapters->out_dim ||
+        x_stride > max_stride || y_stride > max_stride || out_stride > max_stride)
+        return fail(STRATA_MOE_EINVAL, "row strides (%lld, %lld, %lld) below the widths (%d, %d) or above 2^32",
+                    (long long)x_stride, (long long)y_stride, (long long)out_stride, adapters->in_dim,
+                    adapters->out_dim);
+    if (T == 0) return 0;
+    if (!x || !ids || !y || !out) return fail(STRATA_MOE_EINVAL, "null x / ids / y / out");
+    if (!aligned(x, 4) || !aligned(ids, 4) || !aligned(y, 4) || !aligned(out, 4))
+        return fail(STRATA_MOE_EINVAL, "x, ids, y and out must be 4-byte aligned");
+    TRY(check_adapter_pointers(adapters));
+    const uintptr_t nx = row_span(T, x_stride, adapters->in_dim), ny = row_span(T, y_stride, adapters->out_dim),
+                    no = row_span(T, out_stride, adapters->out_dim);
+    if (overlap(out, no, x, nx)) return fail(STRATA_MOE_EINVAL, "out overlaps x");
+    if (!(out == y && out_stride == y_stride) && overlap(out, no, y, ny))
+        return fail(STRATA_MOE_EINVAL, "out overlaps y without being y");
+    TRY(check_workspace(workspace, workspace_bytes, need));
+    TRY(check_device());
+    AdaptLaunch l = adapt_launch(adapters, ids, T, (char*)workspace);
+    l.x = x;
+    l.x_stride = x_stride;
+    l.y = y;
+    l.y_stride = y_stride;
+    l.out = out;
+    l.out_stride = out_stride;
+    HIP_TRY(launch_adapt(l, (hipStream_t)stream), "adapter launch");
+    return 0;
+}
+
+int strata_moe_decode_workspace_bytes(int64_t T, int32_t K, const strata_moe_experts* experts,
+                                      const strata_moe_adapters* adapters, size_t* bytes) {
+    g_err.clear();
+    if (!bytes) return fail(STRATA_MOE_EINVAL, "bytes is NULL");
+    size_t layer = 0, ad = 0;
+    TRY(decode_sizes(T, K, experts, adapters, &layer, &ad));
+    *bytes = layer + ad;
+    return 0;
+}
+
+int strata_moe_decode(const float* x, const float* router_w, const strata_moe_experts* experts, int64_t T, int32_t K,
+                      const strata_moe_adapters* adapters, const int32_t* adapter_ids, float* out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    size_t layer = 0, ad = 0;
+    TRY(decode_sizes(T, K, experts, adapters, &layer, &ad));
+    if (T == 0) return 0;
+    if (!x || !router_w || !out) return fail(STRATA_MOE_EINVAL, "null x / router_w / out");
+    if (!aligned(x, 16) || !aligned(out, 16)) return fail(STRATA_MOE_EINVAL, "x and out must be 16-byte aligned");
+    TRY(check_no_overlap(x, out, T * experts->hidden * 4));
+    if (adapters) {
+        TRY(check_adapter_pointers(adapters));
+        if (!adapter_ids || !aligned(adapter_ids, 4))
+            return fail(STRATA_MOE_EINVAL, "adapters need adapter_ids (4-byte aligned)");
+    } else if (adapter_ids) {
+        return fail(STRATA_MOE_EINVAL, "adapter_ids without adapters");
+    }
+    TRY(check_workspace(workspace, workspace_bytes, layer + ad));
+    TRY(check_device());
+    DecodeLaunch l{};
+    l.x = x;
+    l.router_w = router_w;
+    l.bias = experts->router_bias;
+    l.shared_gate = experts->shared_gate;
+    l.gate_up = (const uint8_t*)experts->gate_up;
+    l.gate_up_stride = experts->gate_up_stride;
+    l.down = (const uint8_t*)experts->down;
+    l.down_stride = experts->down_stride;
+    l.T = (int32_t)T;
+    l.H = experts->hidden;
+    l.E = experts->n_expert;
+    l.K = K;
+    l.I = experts->ffn;
+    l.sym = experts->format == STRATA_MOE_Q2_SYM ? 1 : 0;
+    l.out = out;
+    l.workspace = (char*)workspace;
+    HIP_TRY(launch_decode(l, (hipStream_t)stream), "few-token layer launch");
+    if (adapters) {
+        AdaptLaunch al = adapt_launch(adapters, adapter_ids, T, (char*)workspace + layer);
+        al.x = x;
+        al.x_stride = experts->hidden;
+        al.y = out;
+        al.y_stride = experts->hidden;
+        al.out = out;
+        al.out_stride = experts->hidden;
+        HIP_TRY(launch_adapt(al, (hipStream_t)stream), "adapter launch");
+    }
     return 0;
 }
 

@@ -1,0 +1,270 @@
+"""The layer for a few tokens (strata_moe_decode) against the CPU oracle.
+
+The H codes of this path are those of exact sums, so an output differs from
+the oracle's only by: the routing weight's rounding to fp32, the weighted
+row's, and at most Kg - 1 fp32 additions of the combine, each at most 2^-24
+of the sum of absolute terms.  With one more for the second-order terms:
+    |dy[t, j]| <= (Kg + 2) 2^-24 sum_k p[t,k] |D[t,k,j]|.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synthetic as S
+from layers import canonical_expert, getter, gpu_experts, rel_err, shared_args
+
+
+@pytest.fixture(scope="module")
+def qm():
+    import quantized_routed_expert_logits_amd as qm
+    return qm
+
+
+def _t(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _bound(s, ref):
+    """(Kg + 2) 2^-24 sum p |D| from an oracle.layer result."""
+    rows = np.abs(ref["D"])[ref["slot"]].reshape(s.T, s.K, s.H)
+    b = np.einsum("tk,tkh->th", ref["p"], rows)
+    kg = s.K
+    if ref["shared"] is not None:
+        b = b + ref["shared"]["g"][:, None] * np.abs(ref["shared"]["D"])
+        kg += 1
+    return (kg + 2) * 2.0 ** -24 * b
+
+
+def _check(s, y, ref):
+    err = np.abs(y.cpu().numpy().astype(np.float64) - ref["y"])
+    assert np.all(err <= _bound(s, ref) + 1e-300), f"worst {np.max(err / (_bound(s, ref) + 1e-300)):.2f} of the bound"
+
+
+def _oracle(s, x, wr, bias=None):
+    return oracle.layer(x, wr, bias, getter(s), s.E, s.K, fmt=s.fmt, shared=shared_args(s))
+
+
+SIZES = [
+    S.custom(T=1, H=128, E=1, K=1, I=64),                                 # the smallest layer
+    S.custom(T=1, H=256, E=16, K=2, I=128),
+    S.custom(T=64, H=256, E=16, K=2, I=128),                              # 8 rows an expert
+    S.custom(T=64, H=128, E=2, K=2, I=64, shared=True),                   # every expert gets every row
+    S.custom(T=63, H=384, E=70, K=5, I=192, fmt="q2_0"),                  # odd counts, a partial group of experts
+    S.custom(T=7, H=640, E=65, K=16, I=320, shared=False),
+    S.custom(T=13, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),
+    S.custom(T=33, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),
+    S.custom(T=40, H=256, E=31, K=15, I=64, skewed=True, shared=True),    # n = 640 pairs, hot experts
+    S.custom(T=5, H=1280, E=12, K=3, I=448),
+    S.custom(T=3, H=4096, E=3, K=1, I=64),                                # the widest hidden size
+    S.custom(T=2, H=128, E=3, K=2, I=4096),                               # the widest FFN
+    S.custom(T=64, H=128, E=1024, K=16, I=64),                            # the most experts and pairs
+    S.custom(T=64, H=128, E=1023, K=15, I=64, shared=True),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("s", SIZES, ids=lambda s: s.name)
+def test_layer_against_the_oracle(qm, s):
+    x, wr, bias = S.activations(s), S.router_weight(s), S.router_bias(s)
+    y = qm.strata_moe_decode(_t(x), _t(wr), gpu_experts(s), s.K, torch.full((s.T, s.H), float("nan"), device="cuda"))
+    _check(s, y, _oracle(s, x, wr, bias))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 2, 4, 9, 17, 32, 64])
+def test_production_layer_sampled(qm, T):
+    s = S.custom(T=T, H=2560, E=512, K=10, I=1024)
+    x, wr = S.activations(s), S.router_weight(s)
+    ex = gpu_experts(S.shape("window_32"))
+    y = qm.strata_moe_decode(_t(x), _t(wr), ex, s.K, torch.empty((T, s.H), device="cuda")).cpu().numpy()
+    tokens = sorted({0, T // 2, T - 1})
+    ref = oracle.layer_tokens(x, wr, None, getter(s), s.K, tokens)
+    bound = (s.K + 2) * 2.0 ** -24 * np.einsum("tk,tkh->th", ref["p"], np.abs(ref["D"]))
+    assert np.all(np.abs(y[tokens] - ref["y"]) <= bound)
+    # the prompt path's layer on the same tokens: other H codes at rounding ties only
+    yp = qm.strata_moe_prefill(_t(x), _t(wr), ex, s.K, torch.empty((T, s.H), device="cuda")).cpu().numpy()
+    assert rel_err(y, yp) <= 2e-3
+
+
+@pytest.mark.gpu
+def test_every_token_to_the_same_experts(qm):
+    s = S.custom(T=64, H=256, E=16, K=2, I=128)
+    x, wr = S.activations(s), S.router_weight(s)
+    bias = np.zeros(s.E, np.float32)
+    bias[[3, 11]] = 1e4
+    y = qm.strata_moe_decode(_t(x), _t(wr), gpu_experts(s).with_router_bias(_t(bias)), s.K,
+                             torch.empty((s.T, s.H), device="cuda"))
+    _check(s, y, _oracle(s, x, wr, bias))
+
+
+@pytest.mark.gpu
+def test_equal_logits_zero_rows_and_tiny_values(qm):
+    s = S.custom(T=5, H=256, E=16, K=2, I=128)
+    x, wr = S.activations(s), np.zeros((s.H, s.E), np.float32)   # every logit equal: the first K experts
+    x[1] = 0.0                                                   # every code zero
+    x[2] *= np.float32(1e-30)
+    x[3, 32:64] = np.float32(1e-41)                              # a subnormal block
+    x[4, :32] = np.float32(np.arange(32) - 15.5)                 # quotients on a rounding tie
+    x[4, 0] = 127.0
+    y = qm.strata_moe_decode(_t(x), _t(wr), gpu_experts(s), s.K, torch.empty((s.T, s.H), device="cuda"))
+    ref = _oracle(s, x, wr)
+    assert np.all(ref["ids"] == [0, 1])
+    err = np.abs(y.cpu().numpy() - ref["y"])
+    assert np.all(err <= _bound(s, ref) + 2.0 ** -148)  # an fp32 subnormal's own spacing
+    assert np.all(y[1].cpu().numpy() == 0)
+
+
+@pytest.mark.gpu
+def test_a_token_that_is_not_finite_leaves_the_others(qm):
+    s = S.custom(T=9, H=256, E=16, K=2, I=128, shared=True)
+    x, wr = S.activations(s), S.router_weight(s)
+    ex = gpu_experts(s)
+    good = qm.strata_moe_decode(_t(x), _t(wr), ex, s.K, torch.empty((s.T, s.H), device="cuda"))
+    x[4, 7], x[6, 3] = np.nan, np.inf
+    y = qm.strata_moe_decode(_t(x), _t(wr), ex, s.K, torch.empty((s.T, s.H), device="cuda"))
+    keep = [t for t in range(s.T) if t not in (4, 6)]
+    assert torch.equal(y[keep], good[keep])
+
+
+@pytest.mark.gpu
+def test_workspace_contents_and_bounds(qm):
+    """An uninitialised workspace of just the bytes asked for, an output with
+    guard rows behind it, the same bits every time."""
+    s = S.custom(T=33, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True)
+    x, wr, ex = _t(S.activations(s)), _t(S.router_weight(s)), gpu_experts(s)
+    need = qm.strata_moe_decode_workspace_bytes(s.T, s.K, ex)
+    ref = None
+    for fill in (0x00, 0xff, 0x7f):
+        ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+        buf = torch.full((s.T + 2, s.H), 7.0, device="cuda")
+        y = qm.strata_moe_decode(x, wr, ex, s.K, buf[:s.T], workspace=ws[:need])
+        assert torch.all(buf[s.T:] == 7.0) and torch.all(ws[need:] == fill)
+        ref = y.clone() if ref is None else ref
+        assert torch.equal(y, ref)
+    with pytest.raises(qm.StrataMoeError) as ei:
+        qm.strata_moe_decode(x, wr, ex, s.K, torch.empty_like(x), workspace=ws[:need - 256])
+    assert ei.value.code == qm.ENOMEM
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once(qm):
+    shapes = [S.custom(T=64, H=256, E=16, K=2, I=128), S.custom(T=33, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True)]
+    ins = [(_t(S.activations(s)), _t(S.router_weight(s)), gpu_experts(s)) for s in shapes]
+    refs = [qm.strata_moe_decode(x, wr, ex, s.K, torch.empty_like(x)) for s, (x, wr, ex) in zip(shapes, ins)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.full_like(x, float("nan")) for _ in range(20)] for x, _, _ in ins]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for j, (s, (x, wr, ex)) in enumerate(zip(shapes, ins)):
+            qm.strata_moe_decode(x, wr, ex, s.K, outs[j][i], stream=streams[j])
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(o, refs[j]) for o in outs[j])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("s", [S.custom(T=1, H=256, E=16, K=2, I=128),
+                               S.custom(T=33, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True)], ids=lambda s: s.name)
+def test_captured_and_replayed(qm, s):
+    x, wr, ex = _t(S.activations(s)), _t(S.router_weight(s)), gpu_experts(s)
+    out = torch.empty_like(x)
+    qm.strata_moe_decode(x, wr, ex, s.K, out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qm.strata_moe_decode(x, wr, ex, s.K, out)
+    for i in range(4):  # new inputs in the captured buffers, eager calls in between
+        x.copy_(_t(S.activations(s, seed=i + 1)))
+        ref = qm.strata_moe_decode(x, wr, ex, s.K, torch.empty_like(x))
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+
+
+@pytest.mark.gpu
+def test_adapters_beside_the_layer(qm):
+    """With adapters the call is the layer, then the adapters on its output;
+    a prompt through strata_moe_prefill and strata_moe_adapt agrees."""
+    s = S.custom(T=19, H=256, E=16, K=2, I=128, shared=True)
+    x, wr, ex = _t(S.activations(s)), _t(S.router_weight(s)), gpu_experts(s)
+    rng = torch.Generator().manual_seed(3)
+    ad = qm.Adapters(torch.randn((4, 8, s.H), generator=rng).cuda().bfloat16() / 16,
+                     torch.randn((4, s.H, 8), generator=rng).cuda().bfloat16(),
+                     scale=torch.rand(4, generator=rng).cuda())
+    ids = torch.randint(-1, 4, (s.T,), generator=rng, dtype=torch.int32).cuda()
+    y = qm.strata_moe_decode(x, wr, ex, s.K, torch.empty_like(x), adapters=ad, adapter_ids=ids)
+    plain = qm.strata_moe_decode(x, wr, ex, s.K, torch.empty_like(x))
+    assert torch.equal(y, qm.strata_moe_adapt(x, ids, ad, plain, torch.empty_like(x)))
+    assert torch.equal(y[ids < 0], plain[ids < 0]) and not torch.equal(y, plain)
+    p = qm.strata_moe_prefill(x, wr, ex, s.K, torch.empty_like(x))
+    qm.strata_moe_adapt(x, ids, ad, p, p)
+    assert rel_err(y.cpu().numpy(), p.cpu().numpy()) <= 2e-3
+
+
+# -------------------------------------------------------- refusals (no GPU)
+def _struct(qm, E=16, H=256, I=128, fmt=1):
+    gu, dn = qm.strata_moe_packed_bytes(H, I)
+    return qm.ExpertsStruct(E, H, I, fmt, 1 << 20, gu, 1 << 30, dn, None)
+
+
+def _call(qm, st, T=4, K=2, x=1 << 16, out=1 << 24, ws=1 << 28, nbytes=1 << 40, ad=None, ids=None, wr=64):
+    p = ctypes.c_void_p
+    return qm.library().strata_moe_decode(p(x), p(wr), None if st is None else ctypes.byref(st), T, K,
+                                          None if ad is None else ctypes.byref(ad), p(ids) if ids else None, p(out),
+                                          p(ws) if ws else None, nbytes, None)
+
+
+def test_refusals_on_the_host(qm):
+    st = _struct(qm)
+    for kw in (dict(T=-1), dict(T=65), dict(K=0), dict(K=17), dict(x=None), dict(out=None), dict(wr=None),
+               dict(x=(1 << 16) + 4), dict(out=(1 << 24) + 8), dict(ws=None), dict(ws=(1 << 28) + 64),
+               dict(out=1 << 16), dict(out=(1 << 16) + 2048), dict(ids=64)):
+        assert _call(qm, st, **kw) == qm.EINVAL, kw
+        assert qm.strata_moe_last_error() != ""
+    assert _call(qm, None) == qm.EINVAL
+    assert _call(qm, st, nbytes=4096) == qm.ENOMEM
+    assert _call(qm, _struct(qm, fmt=7)) == qm.EUNSUPPORTED
+    assert _call(qm, _struct(qm, E=2), K=3) == qm.EINVAL
+    assert _call(qm, st, T=0, x=None, out=None, wr=None, ws=None, nbytes=0) == 0
+    ad = qm.AdaptersStruct(2, 8, 256, 256, 1, 256, 256, None, None)
+    assert _call(qm, st, ad=ad) == qm.EINVAL                                          # no adapter_ids
+    for bad in (qm.AdaptersStruct(2, 8, 256, 128, 1, 256, 256, None, None),          # other widths
+                qm.AdaptersStruct(2, 8, 128, 256, 1, 256, 256, None, None),
+                qm.AdaptersStruct(2, 8, 256, 256, 1, None, 256, None, None),
+                qm.AdaptersStruct(2, 0, 256, 256, 1, 256, 256, None, None)):
+        assert _call(qm, st, ad=bad, ids=64) == qm.EINVAL
+
+
+def test_workspace_size_query(qm):
+    b = ctypes.c_size_t()
+    lib, st = qm.library(), _struct(qm)
+    assert lib.strata_moe_decode_workspace_bytes(64, 2, ctypes.byref(st), None, ctypes.byref(b)) == 0
+    plain = b.value
+    assert plain % 256 == 0 and plain > 0
+    ad = qm.AdaptersStruct(2, 8, 256, 256, 3, 256, 256, None, None)
+    assert lib.strata_moe_decode_workspace_bytes(64, 2, ctypes.byref(st), ctypes.byref(ad), ctypes.byref(b)) == 0
+    assert b.value >= plain + 64 * 8 * 4
+    assert lib.strata_moe_decode_workspace_bytes(65, 2, ctypes.byref(st), None, ctypes.byref(b)) == qm.EINVAL
+    assert lib.strata_moe_decode_workspace_bytes(64, 2, ctypes.byref(st), None, None) == qm.EINVAL
+
+
+def test_binding_refusals(qm):
+    E, H, I, T = 8, 256, 128, 4
+    ex = qm.Experts(E, H, I, device="cpu")
+    x, wr, out = torch.zeros((T, H)), torch.zeros((H, E)), torch.zeros((T, H))
+    ad = qm.Adapters(torch.zeros((2, 4, H)), torch.zeros((2, H, 4)))
+    with pytest.raises(TypeError):
+        qm.strata_moe_decode(x, wr, ex, 2, out)                       # CPU tensors
+    with pytest.raises(ValueError):
+        qm.strata_moe_decode(torch.zeros((T, H + 1)), wr, ex, 2, out)
+    with pytest.raises(TypeError):
+        qm.strata_moe_decode(x.double(), wr, ex, 2, out)
+    with pytest.raises((TypeError, ValueError)):
+        qm.strata_moe_decode(x, wr, ex, 2, out, adapters=ad)
+    assert qm.DECODE_MAX_TOKENS == 64

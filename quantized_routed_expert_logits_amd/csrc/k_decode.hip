@@ -21,20 +21,29 @@ namespace strata_moe {
 
 namespace {
 
-constexpr int kRouterSlices = 16;  // ranges of the router's reduction
+constexpr int kRouterSlices = 8;   // ranges of the router's reduction
 constexpr int kThreads = 512;      // 8 waves
 constexpr int kWavesD = kThreads / 64;
-constexpr int kPassRows = 8;       // rows per pass over a chunk's weights
+constexpr int kChunkTokens = 8;    // rows of a chunk at most
+constexpr int kPairTokens = 4;     // calls of at most this many tokens keep every pair on its own
 constexpr int kResident = 512;     // workgroups of the expert kernel that run at once, about
 // Polls before a wait gives up (seconds).  A wait ends by itself unless the
 // caller let two calls share a workspace; then the results are lost, not the GPU.
 constexpr int kMaxPolls = 1 << 21;
 
-// A chunk is the rows of one expert.  Both words are nonzero once written.
+// A chunk is up to 8 rows of one expert.  head and mask are nonzero once
+// written.  What is polled, counted and drawn has a line of its own (next to
+// each other the counters' additions queued behind the polls).
 struct Chunk {
     uint64_t head;  // expert << 32 | first row << 16 | rows
     uint64_t mask;  // the tokens, ascending row by row
+    int32_t pad0[28];
+    int32_t gu_done;  // gate/up workgroups finished
+    int32_t pad1[31];
+    int32_t ticket;   // workgroups that started: gate/up first, then down
+    int32_t pad2[31];
 };
+static_assert(sizeof(Chunk) == 384, "three lines");
 
 struct DecodeArgs {
     const float* x;
@@ -48,7 +57,9 @@ struct DecodeArgs {
     int32_t T, H, E, K, I, shared;
     int32_t Kg, Eg;        // pairs per token, experts (with the shared one)
     int32_t n;             // T * Kg
-    int32_t cap;           // most chunks: min(n, Eg)
+    int32_t cap;           // most chunks
+    int32_t split;         // waves that share a slab's reduction: 1, 2, 4 or 8
+    int32_t gw, dw;        // workgroups per chunk: gate/up, down
     float* out;
     double* part;          // [slices][T][Eg] partial logits (column E: the shared gate's dot product)
     int8_t* qx;            // [T][H]
@@ -65,15 +76,13 @@ struct DecodeArgs {
     int32_t* topk_next;    // tokens whose top-K is taken
     int32_t* topk_done;
     int32_t* nchunks;      // the chunk count plus one
-    int32_t* ticket;       // [cap] slabs taken of a chunk: gate/up first, then down
-    int32_t* gu_done;      // [cap] gate/up slabs finished
     int32_t* dn_done;      // [T][H / 128] weighted rows finished
     Chunk* chunks;         // [cap]
 };
 
 // What workgroups of one launch hand to each other goes through agent-scope
 // accesses: they pass the L2s, which differ between the XCDs.  The writer
-// waits for its stores (publish), then one thread counts them.
+// waits for its stores, then one thread counts them.
 template <typename V>
 __device__ __forceinline__ V peek(const V* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -85,9 +94,11 @@ __device__ __forceinline__ void poke(V* p, V v) {
 __device__ __forceinline__ int bump(int32_t* p) {
     return __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// The wave's stores are done.
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // Every wave's stores are done once the workgroup is past this.
 __device__ __forceinline__ void publish() {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    stores_done();
     __syncthreads();
 }
 
@@ -184,15 +195,15 @@ struct TopkLds {
     int e[kMaxExperts];
     int rank[kMaxExperts];
     double best[kMaxTopK], w[kMaxTopK];
-    int id[kMaxTopK];
     int count;
+    int id[kMaxTopK];    // the result: experts in rank order,
+    float p[kMaxTopK];   // their weights; the shared expert's behind them
 };
 
 __device__ void topk_token(const DecodeArgs& g, int t, TopkLds& l) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const double ninf = -__builtin_huge_val();
     if (threadIdx.x == 0) l.count = 0;
-    for (int i = threadIdx.x; i < kMaxExperts; i += kThreads) l.rank[i] = 0;
     __syncthreads();
     for (int c = wave; c * 64 < g.E; c += kWavesD) {
         const int e = c * 64 + lane;
@@ -223,6 +234,7 @@ __device__ void topk_token(const DecodeArgs& g, int t, TopkLds& l) {
             const int at = base + __popcll(kept & ((1ull << lane) - 1));
             l.v[at] = v;
             l.e[at] = e;
+            l.rank[at] = 0;
         }
     }
     __syncthreads();
@@ -233,7 +245,7 @@ __device__ void topk_token(const DecodeArgs& g, int t, TopkLds& l) {
         const int e = l.e[i], part = threadIdx.x >> 7;
         int r = 0;
 #pragma unroll 8
-        for (int j = part; j < n; j += 4) r += (l.v[j] > v || (l.v[j] == v && l.e[j] < e)) ? 1 : 0;
+        for (int j = part; j < n; j += 4) r += (int)(l.v[j] > v) | ((int)(l.v[j] == v) & (int)(l.e[j] < e));
         if (r) atomicAdd(&l.rank[i], r);
     }
     __syncthreads();
@@ -243,20 +255,20 @@ __device__ void topk_token(const DecodeArgs& g, int t, TopkLds& l) {
             l.id[l.rank[i]] = l.e[i];
         }
     __syncthreads();
-    if ((int)threadIdx.x < g.K) l.w[threadIdx.x] = exp(l.best[threadIdx.x] - l.best[0]);
-    __syncthreads();
-    if ((int)threadIdx.x < g.K) {
+    if (wave == 0) {
+        double w = lane < g.K ? exp(l.best[lane] - l.best[0]) : 0.0;
         double z = 0.0;
-        for (int k = 0; k < g.K; ++k) z += l.w[k];
-        poke(&g.ids[t * g.Kg + threadIdx.x], l.id[threadIdx.x]);
-        poke(&g.p[t * g.Kg + threadIdx.x], (float)(l.w[threadIdx.x] / z));
+        for (int k = 0; k < g.K; ++k) z += __shfl(w, k);
+        if (lane < g.K) l.p[lane] = (float)(w / z);
+    } else if (wave == 1 && g.shared) {
+        double v = lane < kRouterSlices ? g.part[((int64_t)lane * g.T + t) * g.Eg + g.E] : 0.0;
+        for (int o = 1; o < kRouterSlices; o <<= 1) v += __shfl_xor(v, o);
+        if (lane == 0) {
+            l.id[g.K] = g.E;
+            l.p[g.K] = (float)(1.0 / (1.0 + exp(-v)));
+        }
     }
-    if (g.shared && threadIdx.x == 64) {
-        double v = 0.0;
-        for (int s = 0; s < kRouterSlices; ++s) v += g.part[((int64_t)s * g.T + t) * g.Eg + g.E];
-        poke(&g.ids[t * g.Kg + g.K], g.E);
-        poke(&g.p[t * g.Kg + g.K], (float)(1.0 / (1.0 + exp(-v))));
-    }
+    __syncthreads();
 }
 
 // ---------------------------------------------------------------- grouping
@@ -272,15 +284,24 @@ struct GroupLds {
 __device__ void group_pairs(const DecodeArgs& g, GroupLds& l) {
     for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) l.mask[e] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < g.n; i += kThreads)
-        atomicOr((unsigned long long*)&l.mask[peek(&g.ids[i]) & (kMaxExperts - 1)], 1ull << (i / g.Kg));
+    constexpr int kPer = (kDecodeMaxTokens * (kMaxTopK + 1) + kThreads - 1) / kThreads;
+    int id[kPer];  // pairs threadIdx.x + j kThreads
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        id[j] = i < g.n ? peek(&g.ids[i]) & (kMaxExperts - 1) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        if (id[j] >= 0) atomicOr((unsigned long long*)&l.mask[id[j]], 1ull << ((threadIdx.x + j * kThreads) / g.Kg));
     __syncthreads();
-    // exclusive scan of (rows, hit experts) over the experts, packed in one
-    // int: two experts a thread
+    // exclusive scan of (rows, chunks) over the experts, packed in one int:
+    // two experts a thread
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int e0 = 2 * threadIdx.x;
     const int c0 = __popcll(l.mask[e0]), c1 = __popcll(l.mask[e0 + 1]);
-    const int mine = (c0 | (c0 > 0 ? 1 << 16 : 0)) + (c1 | (c1 > 0 ? 1 << 16 : 0));
+    auto packed = [](int c) { return c | (c + kChunkTokens - 1) / kChunkTokens << 16; };
+    const int mine = packed(c0) + packed(c1);
     int s = mine;
     for (int o = 1; o < 64; o <<= 1) {
         const int v = __shfl_up(s, o);
@@ -290,31 +311,39 @@ __device__ void group_pairs(const DecodeArgs& g, GroupLds& l) {
     __syncthreads();
     int at = s - mine;
     for (int w = 0; w < wave; ++w) at += l.wsum[w];
+    // the shared expert, the last one, has every token: its chunks go first
+    const int first = g.shared ? (g.T + kChunkTokens - 1) / kChunkTokens : 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int e = e0 + j, c = j ? c1 : c0;
         l.row0[e] = at & 0xffff;
-        if (c > 0) {
-            // the shared expert's chunk has every token: it goes first
-            const int ci = g.shared ? (e == g.E ? 0 : (at >> 16) + 1) : at >> 16;
-            poke(&g.chunks[ci].head, ((uint64_t)e << 32) | ((uint64_t)(at & 0xffff) << 16) | (uint64_t)c);
-            poke(&g.chunks[ci].mask, l.mask[e]);
-            at += c | (1 << 16);
+        uint64_t left = l.mask[e];
+        for (int r = 0; r < c; r += kChunkTokens) {
+            uint64_t rest = left;
+            for (int k = 0; k < kChunkTokens; ++k) rest &= rest - 1;  // without the lowest 8 tokens
+            const int ci = (g.shared && e == g.E ? 0 : first + (at >> 16)) + r / kChunkTokens;
+            const int rows = c - r < kChunkTokens ? c - r : kChunkTokens;
+            poke(&g.chunks[ci].head, ((uint64_t)e << 32) | ((uint64_t)((at & 0xffff) + r) << 16) | (uint64_t)rows);
+            poke(&g.chunks[ci].mask, left ^ rest);
+            left = rest;
         }
+        at += packed(c);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < g.n; i += kThreads) {
-        const int e = peek(&g.ids[i]) & (kMaxExperts - 1), t = i / g.Kg;
-        poke(&g.row_pair[l.row0[e] + __popcll(l.mask[e] & ((1ull << t) - 1))], i);
-    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        if (id[j] >= 0) {
+            const int i = threadIdx.x + j * kThreads;
+            poke(&g.row_pair[l.row0[id[j]] + __popcll(l.mask[id[j]] & ((1ull << (i / g.Kg)) - 1))], i);
+        }
     publish();
     if (threadIdx.x == kThreads - 1) poke(g.nchunks, (at >> 16) + 1);
 }
 
 // ----------------------------------------------------------------- experts
-// The products of one slab (128 weight rows) with up to 8 activation rows
-// on the int8 matrix unit.  A record's dword p holds, per lane (row r = lane
-// % 16, codes k = 8 (lane / 16) ..), the 16 codes of its rows in fragments A =
+// The products of one slab (128 weight rows) with up to 8 activation rows on
+// the int8 matrix unit.  A record's dword p holds, per lane (row r = lane %
+// 16, codes k = 8 (lane / 16) ..), the 16 codes of its rows in fragments A =
 // 2p and B = 2p + 1, two bits each; shifted and masked it is 4 dwords of
 // bytes A_k B_k A_k+1 B_k+1: 16 bytes, one operand of the 16x16x64 product.
 // Against activations spread to a_k 0 a_k+1 0 that is fragment A's block sum,
@@ -324,22 +353,9 @@ __device__ void group_pairs(const DecodeArgs& g, GroupLds& l) {
 // product's initial value.
 // The activations are the product's rows and the weights its columns: a lane
 // gets, for its own weight row, the four activation rows 4 (lane / 16) + i.
-// Row j of the pass sits in product row 4 (j % 4) + j / 4, so up to 4 NI rows
-// need only the results i < NI.
-// The thread's index, opaque to the compiler: what is computed from it stays
-// inside the pass that needs it (hoisted out of the loop over passes it took
-// some 40 registers through every pass).
-__device__ __forceinline__ int pass_thread() {
-    int t = threadIdx.x;
-    asm volatile("" : "+v"(t));
-    return t;
-}
-
+// Row j of the chunk sits in product row 4 (j % 4) + j / 4, so up to 4 NI rows
+// need only the results i < NI: lane (r, kg) has rows kg + 4 i.
 typedef int v4i __attribute__((ext_vector_type(4)));
-
-struct Block {
-    uint4 c, d;  // a lane's 16 code bytes, its row's 8 fp16 scales
-};
 
 template <bool kSym>
 __device__ __forceinline__ v4i code_bytes(uint32_t w) {
@@ -350,331 +366,399 @@ __device__ __forceinline__ v4i code_bytes(uint32_t w) {
                (int)((w >> 6) & 0x03030303u)};
 }
 
-// The activations of a pass in LDS: code rows `stride` bytes apart, then
-// (scale, code sum) of row j and block b at [b * rows + j].
-__device__ __forceinline__ int act_stride(int Kd) { return Kd + 8; }
+// What a wave works on: blocks [b0, b0 + nb) of one slab against its chunk's
+// rows, with the other waves of its split on the rest of the blocks.
+struct Work {
+    int e, row0, rows, c;
+    const int* tok;  // [rows] tokens (LDS)
+    int slab, part, b0, nb;
+    int slab0, nslab;  // the workgroup's slabs
+};
 
-// One pass: `rows` activation rows of a Kd-long reduction against the slab at
-// rec0.  stage(codes, scales) fills the LDS once the first blocks' loads are
-// out.  Returns in lds tot[4 NI][128] doubles: row j, fragment order f * 16 + r.
-template <bool kSym, int NI, typename Stage>
-__device__ void slab_pass(const uint8_t* rec0, int Kd, char* lds, Stage stage) {
-    constexpr int R = 4 * NI;
-    constexpr int kDepth = NI == 1 ? 5 : 4;  // blocks in flight per wave, as the registers allow
-    const int nblk = Kd / kBlock;
-    const int tid = pass_thread();
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r16 = lane & 15, kg = lane >> 4;
-    const int per = (nblk + kWavesD - 1) / kWavesD;
-    const int b0 = wave * per, nb = b0 + per <= nblk ? per : (b0 < nblk ? nblk - b0 : 0);
-    auto load = [&](int b, Block& r) {
-        const int bb = b < nb ? b0 + b : (nb > 0 ? b0 + nb - 1 : 0);  // past the run: a block that is never used
-        const uint8_t* rec = rec0 + (int64_t)bb * kRecordBytes;
-        r.c = *reinterpret_cast<const uint4*>(rec + lane * 16);
-        r.d = *reinterpret_cast<const uint4*>(rec + kRecordCodeBytes + r16 * 16);
-    };
-    Block ring[kDepth];
-#pragma unroll
-    for (int j = 0; j < kDepth; ++j) load(j, ring[j]);
-    __builtin_amdgcn_sched_barrier(0);
-    uint8_t* qa = (uint8_t*)lds;
-    int2* sa = (int2*)(lds + R * act_stride(Kd));
-    stage(qa, sa, tid);
-    __syncthreads();
-    const int slot = r16 >> 2 | (r16 & 3) << 2;  // product row m holds row m / 4 + 4 (m % 4)
-    const uint8_t* qrow = qa + (slot < R ? slot : 0) * act_stride(Kd) + 8 * kg;
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+
+template <int NI>
+struct Block {
+    v4u c, d;    // a lane's 16 code bytes, its weight row's 8 fp16 scales
+    v2u q;       // its 8 activation codes
+    v2u s[NI];   // scale (fp32), code sum of its activation rows
+};
+
+constexpr int kBufferWord3 = 0x00020000;  // buffer descriptor word 3 for raw dword loads on gfx9 (gfx950)
+constexpr int kAgentLoad = 16;            // a buffer load's sc1 bit: past the L2, as peek()
+
+// p and bytes are the same on every lane (and so in scalar registers).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int bytes) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uintptr_t)p >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(((uintptr_t)hi << 32) | lo), (short)0,
+                                             __builtin_amdgcn_readfirstlane(bytes), kBufferWord3);
+}
+
+// One block's products and scaling.
+template <bool kSym, int NI>
+__device__ __forceinline__ void block_sums(const Block<NI>& r, double (&acc)[8][NI]) {
     constexpr int zp = kSym ? -3 : -1;
-    double acc[8][NI];
+    double sc[NI];
+    v4i z{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        sc[i] = (double)__builtin_bit_cast(float, r.s[i][0]);
+        z[i] = __mul24((int)r.s[i][1], zp);  // |sum| <= 32 * 127: a full-rate 24-bit multiply
+    }
+    const v4i aA{(int)__builtin_amdgcn_perm(0u, r.q[0], 0x0c010c00u), (int)__builtin_amdgcn_perm(0u, r.q[0], 0x0c030c02u),
+                 (int)__builtin_amdgcn_perm(0u, r.q[1], 0x0c010c00u), (int)__builtin_amdgcn_perm(0u, r.q[1], 0x0c030c02u)};
+    const v4i aB{(int)((uint32_t)aA[0] << 8), (int)((uint32_t)aA[1] << 8), (int)((uint32_t)aA[2] << 8),
+                 (int)((uint32_t)aA[3] << 8)};
+    // the products of dword p + 1 run beside the scaling of dword p
+    v4i cw = code_bytes<kSym>(r.c[0]);
+    v4i pa = __builtin_amdgcn_mfma_i32_16x16x64_i8(aA, cw, z, 0, 0, 0);
+    v4i pb = __builtin_amdgcn_mfma_i32_16x16x64_i8(aB, cw, z, 0, 0, 0);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        v4i na, nb;
+        if (p < 3) {
+            cw = code_bytes<kSym>(r.c[p + 1]);
+            na = __builtin_amdgcn_mfma_i32_16x16x64_i8(aA, cw, z, 0, 0, 0);
+            nb = __builtin_amdgcn_mfma_i32_16x16x64_i8(aB, cw, z, 0, 0, 0);
+        }
+        const float da = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.d[p] & 0xffffu));
+        const float db = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.d[p] >> 16));
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            acc[2 * p][i] = fma((double)((float)pa[i] * da), sc[i], acc[2 * p][i]);
+            acc[2 * p + 1][i] = fma((double)((float)pb[i] * db), sc[i], acc[2 * p + 1][i]);
+        }
+        // the results that no row uses stay allocated until here: a register
+        // that a running product still writes cannot be taken without a stall
+        asm volatile("" ::"v"(pa), "v"(pb));
+        if (p < 3) pa = na, pb = nb;
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// acc[f][i]: the sums of weight row f * 16 + r and activation row kg + 4 i
+// over the wave's blocks.  act / scl with the lane's byte offsets qo / so[i]:
+// its code row's 8 codes of the first block, its rows' scales.  ready() is
+// called once the first blocks' weights are on their way and before the
+// activations are read; kAgent: they come from other workgroups.
+template <bool kSym, int NI, bool kAgent, typename Ready>
+__device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, __amdgpu_buffer_rsrc_t act, int qo,
+                                          __amdgpu_buffer_rsrc_t scl, const int (&so)[NI], double (&acc)[8][NI],
+                                          Ready ready) {
+    constexpr int kDepth = 4;  // blocks in flight
+    constexpr int aux = kAgent ? kAgentLoad : 0;
+    const int lane = threadIdx.x & 63, r16 = lane & 15;
+    const int last = w.nb > 0 ? w.nb - 1 : 0;  // past the run: its last block again, never used
+    const __amdgpu_buffer_rsrc_t rr = buffer_of(rec, (last + 1) * kRecordBytes);
+    auto load_w = [&](int b, Block<NI>& r) {
+        const int at = (b < last ? b : last) * kRecordBytes;
+        r.c = __builtin_amdgcn_raw_buffer_load_b128(rr, lane * 16, at, 0);
+        r.d = __builtin_amdgcn_raw_buffer_load_b128(rr, kRecordCodeBytes + r16 * 16, at, 0);
+    };
+    auto load_a = [&](int b, Block<NI>& r) {
+        b = b < last ? b : last;
+        r.q = __builtin_amdgcn_raw_buffer_load_b64(act, qo, b * kBlock, aux);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) r.s[i] = __builtin_amdgcn_raw_buffer_load_b64(scl, so[i], b * 8, aux);
+    };
+    Block<NI> ring[kDepth];
+#pragma unroll
+    for (int j = 0; j < kDepth; ++j) load_w(j, ring[j]);
+    __builtin_amdgcn_sched_barrier(0);
+    ready();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < kDepth; ++j) {
+        load_a(j, ring[j]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int f = 0; f < 8; ++f)
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[f][i] = 0.0;
-    for (int b = 0; b < nb; b += kDepth) {
+    // whole turns of the ring have no branches inside (each block's wait
+    // counts the loads behind it), the rest of the run loads nothing more
+    int b = 0;
+    for (; b + kDepth <= w.nb; b += kDepth) {
 #pragma unroll
         for (int j = 0; j < kDepth; ++j) {
-            if (b + j < nb) {
-                const Block r = ring[j];
-                const int blk = b0 + b + j;
-                const uint2 q = *reinterpret_cast<const uint2*>(qrow + blk * kBlock);
-                double s[NI];
-                v4i z{0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int2 v = sa[blk * R + kg + 4 * i];
-                    s[i] = (double)__builtin_bit_cast(float, v.x);
-                    z[i] = zp * v.y;
-                }
-                v4i aA, aB;
-                aA[0] = (int)__builtin_amdgcn_perm(0u, q.x, 0x0c010c00u);
-                aA[1] = (int)__builtin_amdgcn_perm(0u, q.x, 0x0c030c02u);
-                aA[2] = (int)__builtin_amdgcn_perm(0u, q.y, 0x0c010c00u);
-                aA[3] = (int)__builtin_amdgcn_perm(0u, q.y, 0x0c030c02u);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) aB[i] = (int)((uint32_t)aA[i] << 8);
-                const uint32_t c[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
-                const uint32_t d[4] = {r.d.x, r.d.y, r.d.z, r.d.w};
-                // the products of dword p + 1 run beside the scaling of dword p
-                v4i w = code_bytes<kSym>(c[0]);
-                v4i pa = __builtin_amdgcn_mfma_i32_16x16x64_i8(aA, w, z, 0, 0, 0);
-                v4i pb = __builtin_amdgcn_mfma_i32_16x16x64_i8(aB, w, z, 0, 0, 0);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    v4i na, nb;
-                    if (p < 3) {
-                        w = code_bytes<kSym>(c[p + 1]);
-                        na = __builtin_amdgcn_mfma_i32_16x16x64_i8(aA, w, z, 0, 0, 0);
-                        nb = __builtin_amdgcn_mfma_i32_16x16x64_i8(aB, w, z, 0, 0, 0);
-                    }
-                    const float da = (float)__builtin_bit_cast(_Float16, (uint16_t)(d[p] & 0xffffu));
-                    const float db = (float)__builtin_bit_cast(_Float16, (uint16_t)(d[p] >> 16));
-#pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        acc[2 * p][i] = fma((double)((float)pa[i] * da), s[i], acc[2 * p][i]);
-                        acc[2 * p + 1][i] = fma((double)((float)pb[i] * db), s[i], acc[2 * p + 1][i]);
-                    }
-                    if (p < 3) pa = na, pb = nb;
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                // no block's work moves into another's: the ring is what is in
-                // flight, and the registers hold one block's products
-                load(b + j + kDepth, ring[j]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            block_sums<kSym, NI>(ring[j], acc);
+            load_w(b + j + kDepth, ring[j]);
+            load_a(b + j + kDepth, ring[j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // the waves' sums, halved three times: the upper half of the waves hands
-    // its sums to the lower (a fixed order)
-    double* red = (double*)lds;
 #pragma unroll
-    for (int half = kWavesD / 2; half >= 1; half /= 2) {
-        __syncthreads();  // the activations, or the last round's sums, are read
-        if (wave >= half && wave < 2 * half)
+    for (int j = 0; j < kDepth - 1; ++j)
+        if (b + j < w.nb) block_sums<kSym, NI>(ring[j], acc);
+}
+
+// Every wave's sums to LDS: [wave][4 NI][128], row j of the chunk, fragment
+// order f * 16 + r.  The waves of a slab are next to each other.
+template <int NI>
+__device__ __forceinline__ void share_sums(const Work& w, const double (&acc)[8][NI], double* lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, kg = lane >> 4;
 #pragma unroll
-            for (int f = 0; f < 8; ++f)
+    for (int i = 0; i < NI; ++i)
+        if (kg + 4 * i < w.rows)
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    red[((wave - half) * R + kg + 4 * i) * 128 + f * 16 + r16] = acc[f][i];
-        __syncthreads();
-        if (wave < half)
-#pragma unroll
-            for (int f = 0; f < 8; ++f)
-#pragma unroll
-                for (int i = 0; i < NI; ++i) acc[f][i] += red[(wave * R + kg + 4 * i) * 128 + f * 16 + r16];
-    }
-    __syncthreads();
-    constexpr double unit = kSym ? 0.5 : 1.0;  // the symmetric map's codes are 2 (q - 1.5)
-    if (wave == 0)
-#pragma unroll
-        for (int f = 0; f < 8; ++f)
-#pragma unroll
-            for (int i = 0; i < NI; ++i) red[(kg + 4 * i) * 128 + f * 16 + r16] = unit * acc[f][i];
+            for (int f = 0; f < 8; ++f) lds[(wave * 4 * NI + kg + 4 * i) * 128 + f * 16 + r16] = acc[f][i];
     __syncthreads();
 }
 
-// What the whole workgroup knows about its piece of work.
-struct Piece {
-    int e, row0, rows, slab, c;
-    const int* tok;  // [rows] tokens (LDS)
-};
-
-// Gate/up of rows [r, r + rows) of a chunk: h = silu(G) U rounded to int8,
-// half a wave per row and block of 32.
+// Sum `at` (row j, fragment order) of the workgroup's slab s, its waves in order.
 template <bool kSym, int NI>
-__device__ void gate_up_pass(const DecodeArgs& g, const Piece& w, int r, int rows, char* lds) {
+__device__ __forceinline__ double slab_sum(const DecodeArgs& g, const double* lds, int s, int j, int at) {
+    constexpr double unit = kSym ? 0.5 : 1.0;  // the symmetric map's codes are 2 (q - 1.5)
+    double v = 0.0;
+    for (int o = 0; o < g.split; ++o) v += lds[((s * g.split + o) * 4 * NI + j) * 128 + at];
+    return unit * v;
+}
+
+// Gate/up of the workgroup's slabs: h = silu(G) U, rounded to int8.  Slab
+// columns 0..63 are gate rows, 64..127 the up rows of the same H values; half
+// a wave takes a block of 32.
+template <bool kSym, int NI>
+__device__ void gate_up_slabs(const DecodeArgs& g, const Work& w, double* lds) {
     const int nblk = g.H / kBlock;
-    const uint8_t* rec = g.gate_up + (int64_t)w.e * g.gate_up_stride + (int64_t)w.slab * nblk * kRecordBytes;
-    slab_pass<kSym, NI>(rec, g.H, lds, [&](uint8_t* qa, int2* sa, int tid) {
-        for (int i = tid; i < rows * (g.H / 8); i += kThreads) {
-            const int j = i / (g.H / 8), k = i % (g.H / 8);
-            *reinterpret_cast<uint2*>(qa + j * act_stride(g.H) + 8 * k) =
-                reinterpret_cast<const uint2*>(g.qx + (int64_t)w.tok[r + j] * g.H)[k];
-        }
-        for (int i = tid; i < rows * nblk; i += kThreads) {
-            const int j = i / nblk, k = i % nblk;
-            sa[k * 4 * NI + j] = g.sx[(int64_t)w.tok[r + j] * nblk + k];
-        }
-    });
-    const double* tot = (const double*)lds;
-    const int tid = pass_thread();
-    const int half = tid >> 5, l = tid & 31;
-    for (int i = half; i < 2 * rows; i += kThreads / 32) {
-        const int j = i >> 1, col = (i & 1) * 32 + l;
-        const double gt = tot[j * 128 + col], up = tot[j * 128 + 64 + col];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
+    const int mine = (r16 >> 2) + 4 * (r16 & 3);  // the row in product row r16
+    const int qo = w.tok[mine < w.rows ? mine : 0] * g.H + w.b0 * kBlock + 8 * kg;
+    int so[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) so[i] = (w.tok[kg + 4 * i < w.rows ? kg + 4 * i : 0] * nblk + w.b0) * 8;
+    const uint8_t* rec = g.gate_up + (int64_t)w.e * g.gate_up_stride + ((int64_t)w.slab * nblk + w.b0) * kRecordBytes;
+    double acc[8][NI];
+    slab_sums<kSym, NI, false>(w, rec, buffer_of(g.qx, g.T * g.H), qo, buffer_of(g.sx, g.T * nblk * 8), so, acc, [] {});
+    share_sums<NI>(w, acc, lds);
+    const int l = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < 2 * w.nslab * w.rows; i += kThreads / 32) {
+        const int hb = i & 1, s = (i >> 1) % w.nslab, j = (i >> 1) / w.nslab;
+        const double gt = slab_sum<kSym, NI>(g, lds, s, j, 32 * hb + l);
+        const double up = slab_sum<kSym, NI>(g, lds, s, j, 64 + 32 * hb + l);
         const float h = (float)(gt / (1.0 + exp(-gt)) * up);
         float m = fabsf(h);
-        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 32));
-        const float s = m / 127.0f;
-        const int q = s != 0.0f ? (int)round_half_away(h / s) : 0;
-        int sum = q;
-        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor(sum, o, 32);
-        uint32_t word = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) word |= (uint32_t)(__shfl(q, (l & 7) * 4 + k, 32) & 0xff) << (8 * k);
-        const int64_t row = w.row0 + r + j;
-        if (l < 8) poke(reinterpret_cast<uint32_t*>(g.qh + row * g.I + 64 * w.slab + 32 * (i & 1)) + l, word);
-        if (l == 8)
-            poke(reinterpret_cast<uint64_t*>(g.sh + row * (g.I / kBlock) + 2 * w.slab + (i & 1)),
-                 (uint64_t)__builtin_bit_cast(uint32_t, s) | (uint64_t)(uint32_t)sum << 32);
-    }
-}
-
-// Down of rows [r, r + rows): the weighted rows, and for every token whose
-// last row this is the sum of its rows, k ascending.
-template <bool kSym, int NI>
-__device__ void down_pass(const DecodeArgs& g, const Piece& w, int r, int rows, char* lds, int* flags) {
-    const int nblk = g.I / kBlock, nslab = g.H / kSlabRows;
-    const uint8_t* rec = g.down + (int64_t)w.e * g.down_stride + (int64_t)w.slab * nblk * kRecordBytes;
-    slab_pass<kSym, NI>(rec, g.I, lds, [&](uint8_t* qa, int2* sa, int tid) {
-        if (r == 0) {  // the chunk's H rows are finished
-            if (tid == 0)
-                for (int n = 0; n < kMaxPolls && peek(&g.gu_done[w.c]) < g.I / 64; ++n) __builtin_amdgcn_s_sleep(1);
-            __syncthreads();
-        }
-        for (int i = tid; i < rows * (g.I / 8); i += kThreads) {
-            const int j = i / (g.I / 8), k = i % (g.I / 8);
-            *reinterpret_cast<uint64_t*>(qa + j * act_stride(g.I) + 8 * k) =
-                peek(reinterpret_cast<const uint64_t*>(g.qh + (int64_t)(w.row0 + r + j) * g.I) + k);
-        }
-        for (int i = tid; i < rows * nblk; i += kThreads) {
-            const int j = i / nblk, k = i % nblk;
-            reinterpret_cast<uint64_t*>(sa)[k * 4 * NI + j] =
-                peek(reinterpret_cast<const uint64_t*>(g.sh + (int64_t)(w.row0 + r + j) * nblk) + k);
-        }
-    });
-    const double* tot = (const double*)lds;
-    const int tid = pass_thread();
-    for (int i = tid; i < rows * 128; i += kThreads) {
-        const int pair = peek(&g.row_pair[w.row0 + r + i / 128]);
-        poke(&g.dm[(int64_t)pair * g.H + 128 * w.slab + i % 128], (float)((double)peek(&g.p[pair]) * tot[i]));
+        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+        const float sc = m / 127.0f;
+        const int code = sc != 0.0f ? (int)round_half_away(h / sc) : 0;
+        int sum = code;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor(sum, o);
+        uint32_t word = (uint32_t)(code & 0xff) << (8 * (l & 3));
+        word |= __shfl_xor(word, 1);
+        word |= __shfl_xor(word, 2);
+        const int64_t row = w.row0 + j;
+        const int blk = 2 * (w.slab0 + s) + hb;
+        if ((l & 3) == 0) poke(reinterpret_cast<uint32_t*>(g.qh + row * g.I + 32 * blk + l), word);
+        if (l == 1)
+            poke(reinterpret_cast<uint64_t*>(g.sh + row * (g.I / kBlock) + blk),
+                 (uint64_t)__builtin_bit_cast(uint32_t, sc) | (uint64_t)(uint32_t)sum << 32);
     }
     publish();
-    if (tid < rows)
-        flags[tid] = bump(&g.dn_done[w.tok[r + tid] * nslab + w.slab]) == g.Kg - 1;
-    __syncthreads();
-    for (int i = tid; i < rows * 128; i += kThreads) {
-        if (!flags[i / 128]) continue;
-        const int64_t t = w.tok[r + i / 128];
-        const int col = 128 * w.slab + i % 128;
-        double s = 0.0;
-        for (int k = 0; k < g.Kg; ++k) s += (double)peek(&g.dm[(t * g.Kg + k) * g.H + col]);
-        g.out[t * g.H + col] = (float)s;
-    }
-    __syncthreads();
+    if (threadIdx.x == 0) bump(&g.chunks[w.c].gu_done);
 }
 
-template <bool kSym, bool kWide>
-__device__ void expert_piece(const DecodeArgs& g, const Piece& w, bool gate_up, char* lds, int* flags) {
-    for (int r = 0; r < w.rows; r += kPassRows) {
-        const int rows = w.rows - r < kPassRows ? w.rows - r : kPassRows;
-        if (gate_up) {
-            if (kWide && rows > 4)
-                gate_up_pass<kSym, 2>(g, w, r, rows, lds);
-            else
-                gate_up_pass<kSym, 1>(g, w, r, rows, lds);
-            __syncthreads();
-        } else {
-            if (kWide && rows > 4)
-                down_pass<kSym, 2>(g, w, r, rows, lds, flags);
-            else
-                down_pass<kSym, 1>(g, w, r, rows, lds, flags);
+// Down of the workgroup's slabs: the weighted rows, and for every token and
+// slab whose last row this is the sum of the rows, k ascending.
+struct Rows {
+    int pair[kChunkTokens];
+    float weight[kChunkTokens];
+    int last[kChunkTokens * kWavesD];  // [slab][row]
+};
+
+template <bool kSym, int NI>
+__device__ void down_slabs(const DecodeArgs& g, const Work& w, double* lds, Rows& rows, bool known) {
+    const int nblk = g.I / kBlock, nslab = g.H / kSlabRows;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
+    const int mine = (r16 >> 2) + 4 * (r16 & 3);
+    const int qo = (w.row0 + (mine < w.rows ? mine : 0)) * g.I + w.b0 * kBlock + 8 * kg;
+    int so[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) so[i] = ((w.row0 + (kg + 4 * i < w.rows ? kg + 4 * i : 0)) * nblk + w.b0) * 8;
+    const uint8_t* rec = g.down + (int64_t)w.e * g.down_stride + ((int64_t)w.slab * nblk + w.b0) * kRecordBytes;
+    double acc[8][NI];
+    slab_sums<kSym, NI, true>(w, rec, buffer_of(g.qh, g.n * g.I), qo, buffer_of(g.sh, g.n * nblk * 8), so, acc, [&] {
+        // the rows' pairs and weights, then the chunk's H rows
+        if (!known && (int)threadIdx.x < w.rows) {
+            const int pair = peek(&g.row_pair[w.row0 + threadIdx.x]);
+            rows.pair[threadIdx.x] = pair;
+            rows.weight[threadIdx.x] = peek(&g.p[pair]);
         }
+        if (threadIdx.x == 0)
+            for (int n = 0; n < kMaxPolls && peek(&g.chunks[w.c].gu_done) < g.gw; ++n) __builtin_amdgcn_s_sleep(2);
+        __syncthreads();
+    });
+    share_sums<NI>(w, acc, lds);
+    for (int i = threadIdx.x; i < w.nslab * w.rows * 128; i += kThreads) {
+        const int at = i & 127, s = (i >> 7) % w.nslab, j = (i >> 7) / w.nslab;
+        poke(&g.dm[(int64_t)rows.pair[j] * g.H + 128 * (w.slab0 + s) + at],
+             (float)((double)rows.weight[j] * slab_sum<kSym, NI>(g, lds, s, j, at)));
+    }
+    publish();
+    if ((int)threadIdx.x < w.nslab * w.rows) {
+        const int s = threadIdx.x % w.nslab, j = threadIdx.x / w.nslab;
+        rows.last[threadIdx.x] = bump(&g.dn_done[w.tok[j] * nslab + w.slab0 + s]) == g.Kg - 1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < w.nslab * w.rows * 64; i += kThreads) {
+        if (!rows.last[i >> 6]) continue;
+        const int s = (i >> 6) % w.nslab;
+        const int64_t t = w.tok[(i >> 6) / w.nslab];
+        const uint64_t* row = reinterpret_cast<const uint64_t*>(g.dm + t * g.Kg * g.H + 128 * (w.slab0 + s)) + (i & 63);
+        double s0 = 0.0, s1 = 0.0;
+#pragma unroll 4
+        for (int k = 0; k < g.Kg; ++k) {
+            const uint64_t v = peek(row + (int64_t)k * g.H / 2);
+            s0 += (double)__builtin_bit_cast(float, (uint32_t)v);
+            s1 += (double)__builtin_bit_cast(float, (uint32_t)(v >> 32));
+        }
+        reinterpret_cast<float2*>(g.out + t * g.H + 128 * (w.slab0 + s))[i & 63] = make_float2((float)s0, (float)s1);
     }
 }
 
 // Everything after the router in one launch.  Workgroup id -> chunk is fixed
-// (chunk_of); what the workgroup does for its chunk is the next slab in the
-// order gate/up 0 .. I/64 - 1, down 0 .. H/128 - 1, by the chunk's ticket.  A
-// workgroup that waits for the H rows of its chunk thus knows that their
-// slabs are all in the hands of workgroups that run, and those wait for
-// nothing but the top-K, which any waiting workgroup takes on itself while
-// there are tokens left: every wait ends whatever order the workgroups start
-// in and whatever else runs on the GPU.
+// (chunk_of); what the workgroup does for its chunk is its next group of
+// slabs, gate/up before down, by the chunk's ticket.  A workgroup that waits
+// for the H rows of its chunk thus knows that their slabs are all in the hands
+// of workgroups that run, and those wait for nothing but the top-K, which any
+// waiting workgroup takes on itself while there are tokens left: every wait
+// ends whatever order the workgroups start in and whatever else runs on the
+// GPU.
+// Up to kPairTokens tokens a chunk is one pair and every workgroup finds its
+// expert by the token's top-K itself: the experts that two tokens share are
+// few there, and the hand-offs of the grouping cost more than the top-K.
 __device__ int chunk_of(const DecodeArgs& g, int id) {
-    const int gu = g.I / 64, dn = g.H / kSlabRows;
     // gate/up runs `lag` chunks ahead of down, more than run at once
-    int lag = kResident / gu + 1;
+    int lag = kResident / g.gw + 1;
     if (lag > g.cap) lag = g.cap;
-    if (id < lag * gu) return id / gu;
-    id -= lag * gu;
-    const int whole = (g.cap - lag) * (gu + dn);
-    if (id < whole) return id % (gu + dn) < gu ? lag + id / (gu + dn) : id / (gu + dn);
-    return g.cap - lag + (id - whole) / dn;
+    if (id < lag * g.gw) return id / g.gw;
+    id -= lag * g.gw;
+    const int both = g.gw + g.dw, whole = (g.cap - lag) * both;
+    if (id < whole) return id % both < g.gw ? lag + id / both : id / both;
+    return g.cap - lag + (id - whole) / g.dw;
 }
 
-template <bool kSym, bool kWide>
+template <bool kSym, bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4) decode_experts_kernel(DecodeArgs g) {
     extern __shared__ double lds[];
     __shared__ int todo[4];      // what thread 0 found
     __shared__ uint64_t chunk[2];
-    __shared__ int tok[kDecodeMaxTokens];
-    __shared__ int flags[kPassRows];
+    __shared__ int tok[kChunkTokens];
+    __shared__ Rows rows;
     const int c = chunk_of(g, blockIdx.x);
     int ticket = 0;
-    if (threadIdx.x == 0) ticket = bump(&g.ticket[c]);
-    for (;;) {
-        if (threadIdx.x == 0) {
-            int what = 3;  // give up
-            for (int n = 0; n < kMaxPolls; ++n) {
-                const uint64_t head = peek(&g.chunks[c].head), mask = peek(&g.chunks[c].mask);
-                const int nch = peek(g.nchunks);
-                if (nch > 0 && c >= nch - 1) break;
-                if (nch > 0 && head != 0 && mask != 0) {
-                    chunk[0] = head, chunk[1] = mask;
-                    what = 0;
-                    break;
-                }
-                if (nch == 0 && peek(g.topk_next) < g.T) {
-                    const int t = bump(g.topk_next);
-                    if (t < g.T) {
-                        todo[1] = t;
-                        what = 1;
-                        break;
-                    }
-                }
-                __builtin_amdgcn_s_sleep(1);
-            }
-            todo[0] = what;
-        }
-        __syncthreads();
-        const int what = todo[0];
-        if (what == 3) return;
-        if (what == 0) break;
-        topk_token(g, todo[1], *(TopkLds*)lds);
-        publish();
-        if (threadIdx.x == 0) todo[2] = bump(g.topk_done) == g.T - 1;
-        __syncthreads();
-        if (todo[2]) group_pairs(g, *(GroupLds*)lds);
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) todo[3] = ticket;
-    if (threadIdx.x < 64) {
-        const uint64_t mask = chunk[1];
-        if (mask >> threadIdx.x & 1) tok[__popcll(mask & ((1ull << threadIdx.x) - 1))] = threadIdx.x;
-    }
-    __syncthreads();
-    const int gu = g.I / 64;
-    const int tk = __builtin_amdgcn_readfirstlane(todo[3]);
-    Piece w;
-    w.e = __builtin_amdgcn_readfirstlane((int)(chunk[0] >> 32));
-    w.row0 = __builtin_amdgcn_readfirstlane((int)(chunk[0] >> 16 & 0xffff));
-    w.rows = __builtin_amdgcn_readfirstlane((int)(chunk[0] & 0xffff));
+    if (threadIdx.x == 0) ticket = bump(&g.chunks[c].ticket);
+    Work w;
     w.c = c;
     w.tok = tok;
-    w.slab = tk < gu ? tk : tk - gu;
-    expert_piece<kSym, kWide>(g, w, tk < gu, (char*)lds, flags);
-    if (tk < gu) {
-        publish();
-        if (threadIdx.x == 0) bump(&g.gu_done[c]);
+    if constexpr (kPairs) {
+        TopkLds& l = *(TopkLds*)lds;
+        const int t = c / g.Kg, k = c % g.Kg;
+        topk_token(g, t, l);
+        w.e = __builtin_amdgcn_readfirstlane(l.id[k]);
+        w.row0 = c;
+        w.rows = 1;
+        if (threadIdx.x == 0) {
+            todo[3] = ticket;
+            tok[0] = t;
+            rows.pair[0] = c;
+            rows.weight[0] = l.p[k];
+        }
+    } else {
+        for (;;) {
+            if (threadIdx.x == 0) {
+                int what = 3;  // give up
+                for (int n = 0; n < kMaxPolls; ++n) {
+                    const uint64_t head = peek(&g.chunks[c].head), mask = peek(&g.chunks[c].mask);
+                    const int nch = peek(g.nchunks);
+                    if (nch > 0 && c >= nch - 1) break;
+                    if (nch > 0 && head != 0 && mask != 0) {
+                        chunk[0] = head, chunk[1] = mask;
+                        what = 0;
+                        break;
+                    }
+                    if (nch == 0 && peek(g.topk_next) < g.T) {
+                        const int t = bump(g.topk_next);
+                        if (t < g.T) {
+                            todo[1] = t;
+                            what = 1;
+                            break;
+                        }
+                    }
+                    __builtin_amdgcn_s_sleep(1);
+                }
+                todo[0] = what;
+                todo[3] = ticket;
+            }
+            __syncthreads();
+            const int what = __builtin_amdgcn_readfirstlane(todo[0]);
+            if (what == 3) return;
+            if (what == 0) break;
+            TopkLds& l = *(TopkLds*)lds;
+            const int t = todo[1];
+            topk_token(g, t, l);
+            if ((int)threadIdx.x < g.Kg) {
+                poke(&g.ids[t * g.Kg + threadIdx.x], l.id[threadIdx.x]);
+                poke(&g.p[t * g.Kg + threadIdx.x], l.p[threadIdx.x]);
+            }
+            publish();
+            if (threadIdx.x == 0) todo[2] = bump(g.topk_done) == g.T - 1;
+            __syncthreads();
+            if (todo[2]) group_pairs(g, *(GroupLds*)lds);
+            __syncthreads();
+        }
+        w.e = __builtin_amdgcn_readfirstlane((int)(chunk[0] >> 32));
+        w.row0 = __builtin_amdgcn_readfirstlane((int)(chunk[0] >> 16 & 0xffff));
+        w.rows = __builtin_amdgcn_readfirstlane((int)(chunk[0] & 0xffff));
+        if (threadIdx.x < 64) {
+            const uint64_t mask = chunk[1];
+            if (mask >> threadIdx.x & 1) tok[__popcll(mask & ((1ull << threadIdx.x) - 1))] = threadIdx.x;
+        }
     }
+    __syncthreads();
+    const int tk = __builtin_amdgcn_readfirstlane(todo[3]);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool gate_up = tk < g.gw;
+    const int slabs = gate_up ? g.I / 64 : g.H / kSlabRows, per = kWavesD / g.split;
+    w.slab0 = (gate_up ? tk : tk - g.gw) * per;
+    w.nslab = slabs - w.slab0 < per ? slabs - w.slab0 : per;
+    w.slab = w.slab0 + wave / g.split;
+    w.part = wave % g.split;
+    const int nblk = (gate_up ? g.H : g.I) / kBlock, run = (nblk + g.split - 1) / g.split;
+    w.b0 = w.part * run;
+    w.nb = w.b0 + run <= nblk ? run : nblk - w.b0;
+    // a wave without blocks or a slab still meets the others' barriers
+    if (w.nb <= 0) w.nb = 0, w.b0 = 0;
+    if (w.slab >= slabs) w.nb = 0, w.slab = w.slab0;
+    if (gate_up) {
+        if (!kPairs && w.rows > 4)
+            gate_up_slabs<kSym, 2>(g, w, lds);
+        else
+            gate_up_slabs<kSym, 1>(g, w, lds);
+    } else {
+        if (!kPairs && w.rows > 4)
+            down_slabs<kSym, 2>(g, w, lds, rows, false);
+        else
+            down_slabs<kSym, 1>(g, w, lds, rows, kPairs);
+    }
+}
+
+// Most chunks of n pairs: one for every expert hit, and one more for every 8
+// rows of an expert.
+int64_t chunk_cap(int64_t n, int64_t Eg, int32_t T) {
+    return T <= kPairTokens || n < Eg + n / kChunkTokens ? n : Eg + n / kChunkTokens;
 }
 
 // The workspace of one call.
 struct Plan {
-    size_t part, qx, sx, ids, p, row_pair, qh, sh, dm, words, ticket, gu_done, dn_done, chunks, total;
+    size_t part, qx, sx, ids, p, row_pair, qh, sh, dm, words, dn_done, chunks, total;
 };
 
 Plan plan(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I, bool shared) {
-    const int64_t Eg = E + shared, n = (int64_t)T * (K + shared), cap = n < Eg ? n : Eg;
+    const int64_t Eg = E + shared, n = (int64_t)T * (K + shared), cap = chunk_cap(n, Eg, T);
     size_t off = 0;
     auto take = [&](int64_t bytes) {
         const size_t at = off;
@@ -692,20 +776,10 @@ Plan plan(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I, bool shared) {
     o.sh = take(n * (I / kBlock) * 8);
     o.dm = take(n * H * 4);
     o.words = take(3 * 256);
-    o.ticket = take(cap * 4);
-    o.gu_done = take(cap * 4);
     o.dn_done = take((int64_t)T * (H / kSlabRows) * 4);
-    o.chunks = take(cap * 16);
+    o.chunks = take(cap * (int64_t)sizeof(Chunk));
     o.total = off;
     return o;
-}
-
-// LDS of a pass of up to `rows` rows: the activations (codes, and 8 bytes a
-// block), then half the waves' sums of 4 NI rows in the same place.
-size_t pass_lds(int Kd, int rows) {
-    const size_t R = rows <= 4 ? 4 : kPassRows;
-    const size_t act = R * (Kd + 8) + R * (Kd / kBlock) * 8, sums = (size_t)(kWavesD / 2) * R * 128 * 8;
-    return act > sums ? act : sums;
 }
 
 template <int TT>
@@ -744,7 +818,7 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     g.out = l.out;
     const Plan o = plan(l.T, l.H, l.E, l.K, l.I, g.shared);
     char* ws = l.workspace;
-    g.cap = g.n < g.Eg ? g.n : g.Eg;
+    g.cap = (int32_t)chunk_cap(g.n, g.Eg, g.T);
     g.part = (double*)(ws + o.part);
     g.qx = (int8_t*)(ws + o.qx);
     g.sx = (int2*)(ws + o.sx);
@@ -759,22 +833,27 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     g.topk_next = (int32_t*)(ws + o.words);
     g.topk_done = (int32_t*)(ws + o.words + 256);
     g.nchunks = (int32_t*)(ws + o.words + 512);
-    g.ticket = (int32_t*)(ws + o.ticket);
-    g.gu_done = (int32_t*)(ws + o.gu_done);
     g.dn_done = (int32_t*)(ws + o.dn_done);
     g.chunks = (Chunk*)(ws + o.chunks);
     hipError_t e = g.T == 1 ? launch_router_tt<1>(g, st) : g.T <= 4 ? launch_router_tt<4>(g, st) : launch_router_tt<8>(g, st);
     if (e != hipSuccess) return e;
-    // a chunk has at most T rows
+    // The waves of a slab: all 8 while the slabs are few (their latency counts),
+    // fewer as the workgroups fill the chip anyway.
+    const int gu = g.I / 64, dn = g.H / kSlabRows;
+    g.split = 8;
+    while (g.split > 2 && (int64_t)g.cap * (gu + dn) * g.split / kWavesD > 2 * kResident) g.split /= 2;
+    const int per = kWavesD / g.split;
+    g.gw = (gu + per - 1) / per;
+    g.dw = (dn + per - 1) / per;
     size_t lds = sizeof(TopkLds) > sizeof(GroupLds) ? sizeof(TopkLds) : sizeof(GroupLds);
-    for (const size_t need : {pass_lds(g.H, g.T), pass_lds(g.I, g.T)})
-        if (need > lds) lds = need;
-    const dim3 grid(g.cap * (g.I / 64 + g.H / kSlabRows));
+    const size_t sums = (size_t)kWavesD * (g.T <= kPairTokens ? 4 : 8) * 128 * 8;
+    if (sums > lds) lds = sums;
+    const dim3 grid(g.cap * (g.gw + g.dw));
     void (*kernel)(DecodeArgs);
-    if (g.T <= 4)  // every pass is a narrow one
-        kernel = l.sym ? decode_experts_kernel<true, false> : decode_experts_kernel<false, false>;
-    else
+    if (g.T <= kPairTokens)
         kernel = l.sym ? decode_experts_kernel<true, true> : decode_experts_kernel<false, true>;
+    else
+        kernel = l.sym ? decode_experts_kernel<true, false> : decode_experts_kernel<false, false>;
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), lds, st, g);
     return hipGetLastError();
 }

@@ -327,7 +327,7 @@ struct AdaptLaunch {
     int64_t out_stride;
     char* workspace;
 };
-size_t adapt_workspace(int64_t T, int32_t rank);
+size_t adapt_workspace(int64_t T, int32_t rank, int32_t in_dim);
 hipError_t launch_adapt(const AdaptLaunch& l, hipStream_t st);
 
 hipError_t launch_pack(const uint8_t* codes, const uint16_t* scales, int32_t nexp, int32_t M, int32_t Kd,

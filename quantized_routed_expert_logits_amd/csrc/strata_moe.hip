@@ -736,7 +736,7 @@ int decode_sizes(int64_t T, int32_t K, const strata_moe_experts* ex, const strat
                         ex->hidden);
     }
     *layer = decode_workspace((int32_t)T, ex->hidden, ex->n_expert, K, ex->ffn, ex->shared_gate != nullptr);
-    *adapters = ad ? adapt_workspace(T, ad->rank) : 0;
+    *adapters = ad ? adapt_workspace(T, ad->rank, ad->in_dim) : 0;
     return 0;
 }
 
@@ -1223,7 +1223,7 @@ int strata_moe_adapt_workspace_bytes(int64_t T, const strata_moe_adapters* adapt
     if (!bytes) return fail(STRATA_MOE_EINVAL, "bytes is NULL");
     TRY(check_adapters(adapters));
     TRY(check_adapt_tokens(T));
-    *bytes = adapt_workspace(T, adapters->rank);
+    *bytes = adapt_workspace(T, adapters->rank, adapters->in_dim);
     return 0;
 }
 

@@ -12,12 +12,27 @@
 // either way) and is never stored, so no value of one request reaches
 // another's row.
 //
-// The products run on the fp32 matrix unit (16x16x4): the activations and
-// sums are fp32 and an fp16 or bf16 weight widens exactly, so one kernel
-// serves the three types and nothing is rounded but the sums.  A lane's
-// operand is one value of k; it loads 8 consecutive values of k (16 bytes of a
-// 16-bit weight: a wave's load is whole 64-byte pieces of 16 rows) and feeds
-// them to 8 products, which only permutes k, for both operands alike.
+// Products.  The activations and sums are fp32.  fp32 and fp16 weights run on
+// the fp32 matrix unit (16x16x4; an fp16 weight widens exactly).  bf16 weights
+// run on the bf16 unit (16x16x32): a fp32 activation is the sum of three bf16
+// values, exactly (its 24 bits are cut into 8 + 8 + 8 from the top), so three
+// products give what one fp32 product gives, in 3/16 of its time.  The parts
+// below the first have accumulators of their own: their additions round at
+// 2^-8 of the first's.  (Below 2^-110 the lowest part is subnormal and may
+// count as zero; an infinite input or weight may give NaN in its row where
+// the definition has an infinity.)  fp16 weights do not split as cheaply: each
+// is two bf16 values, and cutting 64 rows of them costs more vector
+// instructions than the fp32 products they replace.
+//
+// A lane's operand is row lane % 16 and a run of consecutive values of k (8,
+// or 4 in the expand of ranks up to 16).  The fp32 unit takes the run one
+// value a product, which only permutes k, for both operands alike.
+//
+// Loads and stores go row by row, 4 or 16 neighbouring lanes to a row, and
+// cross to the products' layout (neighbouring lanes in different rows)
+// through LDS that belongs to the wave alone.  Loaded in the products' layout,
+// every lane's 16 bytes were an access of their own: 50 us against 23 for the
+// shrink of 8192 tokens at rank 64 with a quarter of the loads.
 #include "internal.h"
 
 namespace strata_moe {
@@ -28,7 +43,7 @@ constexpr int kTile = 16;         // tokens of a tile
 constexpr int kShrinkWaves = 8;   // waves that split a workgroup's part of the reduction over in
 constexpr int kRowTiles = 4;      // 16-row tiles of A per shrink workgroup: 64 ranks
 constexpr int kExpandWaves = 4;
-constexpr int kExpandCols = 32;   // outputs of a wave at a time
+constexpr int kExpandCols = 64;   // outputs of a wave at a time
 constexpr int kMaxSplit = 16;     // shrink workgroups that share a reduction
 constexpr int kPad = 4;           // floats between the LDS rows of v (spreads the banks)
 // Calls of up to this many tokens give every group of a tile workgroups of its
@@ -36,6 +51,11 @@ constexpr int kPad = 4;           // floats between the LDS rows of v (spreads t
 // ones have tiles enough to fill the chip.
 constexpr int kSpreadTokens = 256;
 constexpr int kFill = 512;        // workgroups that fill the chip
+// From this many tiles on every XCD takes a run of neighbouring tiles: prompts
+// share adapters with their neighbours, and an L2 then holds two or three of
+// them instead of all (8192 tokens, 16 adapters of rank 64, the shrink: 52 us
+// dealt round robin, 35 with a single adapter).
+constexpr int kDealTiles = 64;
 
 struct AdaptArgs {
     const float* x;
@@ -47,18 +67,21 @@ struct AdaptArgs {
     const float* scale;    // or null: 1
     const int32_t* ranks;  // or null: rank
     float* v;              // [split][T][vs]: the parts of A x
-    int64_t T, total;      // tokens of the launch, of the call
-    int64_t xs, ys, os;
+    int64_t T, xs, ys, os;
     int32_t L, rank, in, out_dim;
     int32_t vs;            // rank rounded up to 16
     int32_t ls;            // floats of an LDS row of v: rank rounded up to 32, and the pad
     int32_t split;         // parts of the reduction over in
     int32_t spread;        // groups of a tile that run side by side
     int32_t turns;         // expand: turns of kExpandCols outputs per wave
+    int32_t tiles;
+    int32_t deal;          // tiles are dealt to the XCDs in runs of this many, or 0
     int32_t copy;          // out is not y: rows without an adapter are copied
 };
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));  // at any float
 
 __device__ __forceinline__ v4f load4(const float* p) { return *reinterpret_cast<const v4f_any*>(p); }
@@ -119,6 +142,12 @@ __device__ __forceinline__ int adapter_rank(const AdaptArgs& g, int a) {
     return r < 0 ? 0 : (r > g.rank ? g.rank : r);
 }
 
+// The workgroup's tile, or -1.  Workgroups go to the 8 XCDs in turn.
+__device__ __forceinline__ int tile_of(const AdaptArgs& g, int id) {
+    const int tile = g.deal > 0 ? (id & 7) * g.deal + (id >> 3) : id;
+    return tile < g.tiles && (g.deal == 0 || (id >> 3) < g.deal) ? tile : -1;
+}
+
 // Calls f(adapter or -1, the group's lanes as a 16-bit mask) for every group
 // of the tile that is this workgroup's (the same on every wave).
 template <typename F>
@@ -139,30 +168,112 @@ __device__ __forceinline__ void for_groups(const AdaptArgs& g, int64_t t0, int s
     }
 }
 
+// A panel is 16 rows of 4 runs.  Loaded, lane l has run l % 4 of row l / 4;
+// crossed, lane l has run l / 16 of row l % 16.  buf: 64 runs of the wave's LDS.
+template <typename W, int P>
+__device__ __forceinline__ void cross_out(const Run<W, P>& f, char* buf) {
+    *reinterpret_cast<Run<W, P>*>(buf + (threadIdx.x & 63) * sizeof(f)) = f;
+}
+template <typename W, int P>
+__device__ __forceinline__ void cross_in(Run<W, P>& f, const char* buf) {
+    const int lane = threadIdx.x & 63;
+    f = *reinterpret_cast<const Run<W, P>*>(buf + ((lane & 15) * 4 + (lane >> 4)) * sizeof(f));
+}
+
+// acc += w x over a run of k, for N tiles of weights (the product's rows) and
+// 16 activations (its columns).  lo: the bf16 parts below the first.
+template <typename W, int P, int N>
+struct Products {
+    Run<float, P> x;
+    __device__ __forceinline__ void set(const Run<float, P>& v) { x = v; }
+    template <int M>
+    __device__ __forceinline__ void add(const Run<W, P> (&w)[N], v4f (&acc)[M], v4f (&)[M]) const {
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[i].get(j), x.get(j), acc[i], 0, 0, 0);
+    }
+};
+
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+
+template <int P, int N>
+struct Products<Bf16, P, N> {
+    uint32_t x[3][P / 2];  // the three parts, two values a dword
+    __device__ __forceinline__ void set(const Run<float, P>& v) {
+        constexpr uint32_t kTop = 0xffff0000u, kTops = 0x07060302u;  // both upper halves
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            float a = v.get(j), b = v.get(j + 1);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const uint32_t ab = __builtin_bit_cast(uint32_t, a), bb = __builtin_bit_cast(uint32_t, b);
+                x[p][j / 2] = __builtin_amdgcn_perm(bb, ab, kTops);
+                if (p < 2) {
+                    a -= __builtin_bit_cast(float, ab & kTop);
+                    b -= __builtin_bit_cast(float, bb & kTop);
+                }
+            }
+        }
+    }
+    template <int M>
+    __device__ __forceinline__ void add(const Run<Bf16, P> (&w)[N], v4f (&acc)[M], v4f (&lo)[M]) const {
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v4f& s = p == 0 ? acc[i] : lo[i];
+                if constexpr (P == 8)
+                    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(v8b, w[i].r),
+                        __builtin_bit_cast(v8b, v4u{x[p][0], x[p][1], x[p][2], x[p][3]}), s, 0, 0, 0);
+                else
+                    s = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+                        __builtin_bit_cast(v4i16, w[i].r), __builtin_bit_cast(v4i16, v2u{x[p][0], x[p][1]}), s, 0, 0, 0);
+            }
+    }
+};
+
 // Products of steps [s0, s1) of 32 values of k: RT tiles of 16 A rows against
-// the tile's tokens.  a[i], x: the lane's rows (rows and tokens outside the
-// group repeat one of it: the loads need no branch, and what comes of them is
-// not stored).
+// the tile's tokens.  al[i], xl: the rows that the lane loads, a[i], x: those
+// of its operands (rows and tokens outside the group repeat one of it: the
+// loads need no branch, and what comes of them is not stored).
 template <typename W, int RT>
-__device__ __forceinline__ void shrink_steps(const AdaptArgs& g, const W* const (&a)[kRowTiles], const float* x, int s0,
-                                             int s1, v4f (&acc)[kRowTiles]) {
+__device__ __forceinline__ void shrink_steps(const AdaptArgs& g, const W* const (&al)[kRowTiles], const float* xl,
+                                             const W* const (&a)[kRowTiles], const float* x, int s0, int s1,
+                                             v4f (&acc)[kRowTiles], v4f (&lo)[kRowTiles], char* buf) {
     constexpr int kDepth = RT == 1 ? 4 : RT == 2 ? 3 : 2;  // steps in flight
-    const int k0 = 8 * ((threadIdx.x & 63) >> 4);
+    constexpr int kPanel = 64 * 8 * (int)sizeof(W);
+    const int lane = threadIdx.x & 63;
     const int whole = g.in / 32 < s1 ? g.in / 32 : s1;
-    Run<float, 8> xr[kDepth];
+    Run<float, 4> xr[kDepth][2];  // values 0..15 and 16..31 of the step
     Run<W, 8> wr[kDepth][RT];
     auto load = [&](int s, int u) {
-        const int k = 32 * (s < whole ? s : whole - 1) + k0;  // past the run: its last step again, never used
-        xr[u].load(x + k);
+        const int k = 32 * (s < whole ? s : whole - 1);  // past the run: its last step again, never used
 #pragma unroll
-        for (int i = 0; i < RT; ++i) wr[u][i].load(a[i] + k);
+        for (int h = 0; h < 2; ++h) xr[u][h].load(xl + k + 16 * h + 4 * (lane & 3));
+#pragma unroll
+        for (int i = 0; i < RT; ++i) wr[u][i].load(al[i] + k + 8 * (lane & 3));
     };
-    auto products = [&](int u) {
+    auto products = [&](const Run<float, 8>& xv, const Run<W, 8> (&w)[RT]) {
+        Products<W, 8, RT> m;
+        m.set(xv);
+        m.add(w, acc, lo);
+    };
+    auto step = [&](int u) {
+        // x: run kg of 8 is chunks 2 kg, 2 kg + 1 of 4, in panel kg / 2
+        cross_out(xr[u][0], buf);
+        cross_out(xr[u][1], buf + 1024);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int i = 0; i < RT; ++i) cross_out(wr[u][i], buf + 2048 + kPanel * i);
+        Run<float, 8> xv = *reinterpret_cast<const Run<float, 8>*>(buf + (lane >> 5) * 1024 + (lane & 15) * 64 +
+                                                                   (lane >> 4 & 1) * 32);
+        Run<W, 8> w[RT];
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(wr[u][i].get(j), xr[u].get(j), acc[i], 0, 0, 0);
+        for (int i = 0; i < RT; ++i) cross_in(w[i], buf + 2048 + kPanel * i);
+        products(xv, w);
     };
     int s = s0;
     if (s < whole) {
@@ -174,23 +285,25 @@ __device__ __forceinline__ void shrink_steps(const AdaptArgs& g, const W* const 
         for (; s + kDepth <= whole; s += kDepth)
 #pragma unroll
             for (int u = 0; u < kDepth; ++u) {
-                products(u);
+                step(u);
                 __builtin_amdgcn_sched_barrier(0);
                 load(s + kDepth + u, u);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        int left = whole - s;
+        const int left = whole - s;
 #pragma unroll
         for (int u = 0; u < kDepth - 1; ++u)
-            if (u < left) products(u);
+            if (u < left) step(u);
         s = whole;
     }
-    if (s < s1) {  // the step that ends inside the row
-        const int k = 32 * s + k0;
-        load_upto<float, 8>(xr[0], x + k, k, g.in);
+    if (s < s1) {  // the step that ends inside the row, straight to the operands
+        const int k = 32 * s + 8 * (lane >> 4);
+        Run<float, 8> xv;
+        Run<W, 8> w[RT];
+        load_upto<float, 8>(xv, x + k, k, g.in);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) load_upto<W, 8>(wr[0][i], a[i] + k, k, g.in);
-        products(0);
+        for (int i = 0; i < RT; ++i) load_upto<W, 8>(w[i], a[i] + k, k, g.in);
+        products(xv, w);
     }
 }
 
@@ -198,10 +311,15 @@ __device__ __forceinline__ void shrink_steps(const AdaptArgs& g, const W* const 
 // reduction over in, which its waves split again.
 template <typename W>
 __global__ void __launch_bounds__(64 * kShrinkWaves) adapt_shrink_kernel(AdaptArgs g) {
-    __shared__ float red[kShrinkWaves][kRowTiles][kTile * kTile];
+    // the waves' panels, then their sums
+    constexpr int kWaveBytes = 2048 + kRowTiles * 64 * 8 * (int)sizeof(W);
+    constexpr int kSumBytes = kRowTiles * kTile * kTile * (int)sizeof(float);
+    __shared__ __align__(16) char lds[kShrinkWaves * (kWaveBytes > kSumBytes ? kWaveBytes : kSumBytes)];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, kg = lane >> 4;
-    const int64_t t0 = (int64_t)blockIdx.x * kTile;
+    const int tile = tile_of(g, blockIdx.x);
+    if (tile < 0) return;
+    const int64_t t0 = (int64_t)tile * kTile;
     const int part = blockIdx.z % g.split, r0 = blockIdx.z / g.split * 16 * kRowTiles;
     const int steps = (g.in + 31) / 32, runs = g.split * kShrinkWaves, per = (steps + runs - 1) / runs;
     const int first = (part * kShrinkWaves + wave) * per;
@@ -211,33 +329,41 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) adapt_shrink_kernel(AdaptAr
         const int rows = adapter_rank(g, a) - r0;
         if (rows <= 0) return;
         const int rt = rows >= 16 * kRowTiles ? kRowTiles : (rows + 15) / 16;
-        const float* x = g.x + (t0 + (group >> r16 & 1 ? r16 : __builtin_ctz(group))) * g.xs;
+        const int one = __builtin_ctz(group);
+        const float* x = g.x + (t0 + (group >> r16 & 1 ? r16 : one)) * g.xs;
+        const float* xl = g.x + (t0 + (group >> (lane >> 2) & 1 ? lane >> 2 : one)) * g.xs;
         const W* aw[kRowTiles];
-        v4f acc[kRowTiles];
+        const W* al[kRowTiles];
+        v4f acc[kRowTiles], lo[kRowTiles];
+        const W* a0 = (const W*)g.a + ((int64_t)a * g.rank + r0) * g.in;
 #pragma unroll
         for (int i = 0; i < kRowTiles; ++i) {
-            const int row = 16 * i + r16 < rows ? 16 * i + r16 : rows - 1;
-            aw[i] = (const W*)g.a + ((int64_t)a * g.rank + r0 + row) * g.in;
-            acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+            const int row = 16 * i + r16, rowl = 16 * i + (lane >> 2);
+            aw[i] = a0 + (int64_t)(row < rows ? row : rows - 1) * g.in;
+            al[i] = a0 + (int64_t)(rowl < rows ? rowl : rows - 1) * g.in;
+            acc[i] = lo[i] = v4f{0.f, 0.f, 0.f, 0.f};
         }
+        __syncthreads();  // the last group's sums are read
+        char* buf = lds + wave * kWaveBytes;
         if (rt == 1)
-            shrink_steps<W, 1>(g, aw, x, s0, s1, acc);
+            shrink_steps<W, 1>(g, al, xl, aw, x, s0, s1, acc, lo, buf);
         else if (rt == 2)
-            shrink_steps<W, 2>(g, aw, x, s0, s1, acc);
+            shrink_steps<W, 2>(g, al, xl, aw, x, s0, s1, acc, lo, buf);
         else
-            shrink_steps<W, 4>(g, aw, x, s0, s1, acc);
+            shrink_steps<W, 4>(g, al, xl, aw, x, s0, s1, acc, lo, buf);
         // a lane has ranks 16 i + 4 kg .. + 3 of token r16
+        float* red = (float*)lds;  // [wave][row tile][token][16]
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRowTiles; ++i)
-            if (i < rt) *reinterpret_cast<v4f*>(&red[wave][i][r16 * 16 + 4 * kg]) = acc[i];
+            if (i < rt) *reinterpret_cast<v4f*>(&red[((wave * kRowTiles + i) * 16 + r16) * 16 + 4 * kg]) = acc[i] + lo[i];
         __syncthreads();
         for (int n = threadIdx.x; n < rt * kTile * kTile; n += blockDim.x) {
             const int i = n >> 8, token = n >> 4 & 15, r = n & 15;
             if (!(group >> token & 1) || 16 * i + r >= rows) continue;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < kShrinkWaves; ++w) s += red[w][i][n & 255];
+            for (int w = 0; w < kShrinkWaves; ++w) s += red[(w * kRowTiles + i) * 256 + (n & 255)];
             g.v[((int64_t)part * g.T + t0 + token) * g.vs + r0 + 16 * i + r] = s;
         }
     });
@@ -247,16 +373,35 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) adapt_shrink_kernel(AdaptAr
 // consecutive ranks per lane: 4 for ranks up to 16, else 8.
 template <typename W, int P>
 __global__ void __launch_bounds__(64 * kExpandWaves) adapt_expand_kernel(AdaptArgs g) {
-    extern __shared__ float v[];  // [16][ls]
     constexpr int kTiles = kExpandCols / 16;
+    constexpr int kRow = kExpandCols + kPad;  // floats of an output row in LDS
+    constexpr int kPanel = 64 * P * (int)sizeof(W);
+    constexpr int kWaveBytes = kTiles * kPanel > 16 * kRow * 4 ? kTiles * kPanel : 16 * kRow * 4;
+    __shared__ __align__(16) char lds[kExpandWaves][kWaveBytes];  // a wave's panels of B, or its outputs
+    extern __shared__ float v[];                                  // [16][ls]
     const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t0 = (int64_t)blockIdx.y * kTile;
-    const int64_t total = g.total;
+    const int tile = tile_of(g, blockIdx.x);
+    if (tile < 0) return;
+    const int64_t t0 = (int64_t)tile * kTile;
+    const int first = (blockIdx.y * g.turns * kExpandWaves + wave) * kExpandCols;  // the turns are 4 waves apart
+    char* buf = lds[wave];
+    float* rows = (float*)lds[wave];
     for_groups(g, t0, blockIdx.z, [&](int a, uint32_t group) {
         const int rank = a < 0 ? 0 : adapter_rank(g, a);
         if (rank == 0 && !g.copy) return;
-        const bool mine = group >> r16 & 1;
+        const int whole = rank / (4 * P) * (4 * P);
+        const W* b = (const W*)g.b + (int64_t)(a < 0 ? 0 : a) * g.out_dim * g.rank;
+        // the panels of outputs o0 .. and ranks r .. (of a whole step)
+        Run<W, P> w[kTiles];
+        auto load = [&](int o0, int r) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const int o = o0 + 16 * i + (lane >> 2);
+                w[i].load(b + (int64_t)(o < g.out_dim ? o : g.out_dim - 1) * g.rank + r + P * (lane & 3));
+            }
+        };
+        if (whole > 0) load(first, 0);
         const float scale = a >= 0 && g.scale ? g.scale[a] : 1.0f;
         // the group's v, its parts added in order, zeros past the rank (the
         // other tokens' rows hold anything: their columns are not stored)
@@ -266,61 +411,77 @@ __global__ void __launch_bounds__(64 * kExpandWaves) adapt_expand_kernel(AdaptAr
             const int token = n / ranks, r = n % ranks;
             if (!(group >> token & 1)) continue;
             float s = 0.f;
-            if (r < rank)
-                for (int p = 0; p < g.split; ++p) s += g.v[((int64_t)p * total + t0 + token) * g.vs + r];
+            if (r < rank) {
+                const float* p = g.v + (t0 + token) * g.vs + r;
+#pragma unroll 4
+                for (int i = 0; i < g.split; ++i) s += p[(int64_t)i * g.T * g.vs];
+            }
             v[token * g.ls + r] = s;
         }
         __syncthreads();
         const float* vr = v + r16 * g.ls + P * kg;
         for (int turn = 0; turn < g.turns; ++turn) {
-            const int o0 = ((blockIdx.x * g.turns + turn) * kExpandWaves + wave) * kExpandCols;
+            const int o0 = first + turn * kExpandWaves * kExpandCols, next = o0 + kExpandWaves * kExpandCols;
             if (o0 >= g.out_dim) break;
-            const float* y = g.y + (t0 + r16) * g.ys + o0 + 4 * kg;
-            v4f acc[kTiles], s[kTiles];
+            const int cols = g.out_dim - o0;
+            // a lane loads, adds and stores columns 4 r16 .. + 3 of rows kg + 4 i
+            v4f s[4];
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                acc[i] = s[i] = v4f{0.f, 0.f, 0.f, 0.f};
-                if (mine && o0 + 16 * i + 4 * kg + 4 <= g.out_dim) s[i] = load4(y + 16 * i);
-            }
-            const W* bw[kTiles];
+            for (int i = 0; i < 4; ++i)
+                if ((group >> (kg + 4 * i) & 1) && 4 * r16 + 4 <= cols)
+                    s[i] = load4(g.y + (t0 + kg + 4 * i) * g.ys + o0 + 4 * r16);
+            v4f acc[kTiles], lo[kTiles];
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                const int o = o0 + 16 * i + r16 < g.out_dim ? o0 + 16 * i + r16 : g.out_dim - 1;
-                bw[i] = (const W*)g.b + ((int64_t)(a < 0 ? 0 : a) * g.out_dim + o) * g.rank + P * kg;
-            }
-            for (int r = 0; r < rank; r += 4 * P) {
-                Run<W, P> w[kTiles];
+            for (int i = 0; i < kTiles; ++i) acc[i] = lo[i] = v4f{0.f, 0.f, 0.f, 0.f};
+            Products<W, P, kTiles> m;
+            Run<float, P> vv;
+            for (int r = 0; r < whole; r += 4 * P) {
+                Run<W, P> u[kTiles];
 #pragma unroll
-                for (int i = 0; i < kTiles; ++i)
-                    if (r + 4 * P <= rank)
-                        w[i].load(bw[i] + r);
-                    else
-                        load_upto<W, P>(w[i], bw[i] + r, r + P * kg, rank);
-                Run<float, P> vv;
+                for (int i = 0; i < kTiles; ++i) cross_out(w[i], buf + kPanel * i);
+                // the next step's panels: these ranks', or the next turn's first
+                if (r + 4 * P < whole)
+                    load(o0, r + 4 * P);
+                else
+                    load(next, 0);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) cross_in(u[i], buf + kPanel * i);
                 vv.load(vr + r);
-#pragma unroll
-                for (int j = 0; j < P; ++j)
-#pragma unroll
-                    for (int i = 0; i < kTiles; ++i)
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[i].get(j), vv.get(j), acc[i], 0, 0, 0);
+                m.set(vv);
+                m.add(u, acc, lo);
             }
-            // a lane has outputs 16 i + 4 kg .. + 3 of token r16
-            if (mine) {
-                float* out = g.out + (t0 + r16) * g.os + o0 + 4 * kg;
+            if (whole < rank) {  // the step that ends inside the rank, straight to the operands
+                Run<W, P> u[kTiles];
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) {
-                    const int o = o0 + 16 * i + 4 * kg;
-                    if (o + 4 <= g.out_dim) {
-                        if (rank > 0)
+                    const int o = o0 + 16 * i + r16;
+                    load_upto<W, P>(u[i], b + (int64_t)(o < g.out_dim ? o : g.out_dim - 1) * g.rank + whole + P * kg,
+                                    whole + P * kg, rank);
+                }
+                vv.load(vr + whole);
+                m.set(vv);
+                m.add(u, acc, lo);
+            }
+            // a lane has outputs 16 i + 4 kg .. + 3 of token r16: cross to rows
+            if (rank > 0) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) s[i][j] = fmaf(scale, acc[i][j], s[i][j]);
-                        *reinterpret_cast<v4f_any*>(out + 16 * i) = s[i];
-                    } else {
-                        for (int j = 0; j < 4 && o + j < g.out_dim; ++j) {
-                            const float yv = y[16 * i + j];
-                            out[16 * i + j] = rank > 0 ? fmaf(scale, acc[i][j], yv) : yv;
-                        }
-                    }
+                for (int i = 0; i < kTiles; ++i)
+                    *reinterpret_cast<v4f*>(&rows[r16 * kRow + 16 * i + 4 * kg]) = acc[i] + lo[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int token = kg + 4 * i;
+                if (!(group >> token & 1)) continue;
+                const v4f d = *reinterpret_cast<const v4f*>(&rows[token * kRow + 4 * r16]);
+                const float* y = g.y + (t0 + token) * g.ys + o0 + 4 * r16;
+                float* out = g.out + (t0 + token) * g.os + o0 + 4 * r16;
+                if (4 * r16 + 4 <= cols) {
+                    if (rank > 0)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[i][j] = fmaf(scale, d[j], s[i][j]);
+                    *reinterpret_cast<v4f_any*>(out) = s[i];
+                } else {
+                    for (int j = 0; j < 4 && 4 * r16 + j < cols; ++j) out[j] = rank > 0 ? fmaf(scale, d[j], y[j]) : y[j];
                 }
             }
         }
@@ -329,42 +490,33 @@ __global__ void __launch_bounds__(64 * kExpandWaves) adapt_expand_kernel(AdaptAr
 
 template <typename W>
 hipError_t launch_typed(AdaptArgs g, hipStream_t st) {
-    const unsigned tiles = (unsigned)((g.T + kTile - 1) / kTile);
+    g.tiles = (int32_t)((g.T + kTile - 1) / kTile);
+    g.deal = g.tiles >= kDealTiles ? (g.tiles + 7) / 8 : 0;
+    const unsigned gt = g.deal ? 8 * g.deal : g.tiles;
     const unsigned ranks = (unsigned)((g.rank + 16 * kRowTiles - 1) / (16 * kRowTiles));
-    hipLaunchKernelGGL(adapt_shrink_kernel<W>, dim3(tiles, g.spread, ranks * g.split), dim3(64 * kShrinkWaves), 0, st, g);
+    hipLaunchKernelGGL(adapt_shrink_kernel<W>, dim3(gt, g.spread, ranks * g.split), dim3(64 * kShrinkWaves), 0, st, g);
     // enough workgroups to fill the chip several times, then longer ones
     const unsigned cols = (unsigned)((g.out_dim + kExpandCols * kExpandWaves - 1) / (kExpandCols * kExpandWaves));
-    unsigned gx = cols;
-    while (gx > 1 && (int64_t)tiles * (gx / 2) >= 4 * kFill) gx /= 2;
-    g.turns = (cols + gx - 1) / gx;
+    unsigned gc = cols;
+    while (gc > 1 && (int64_t)g.tiles * (gc / 2) >= 4 * kFill) gc /= 2;
+    g.turns = (cols + gc - 1) / gc;
     const size_t lds = (size_t)kTile * g.ls * sizeof(float);
-    // grid.y and grid.z hold at most 65535: tiles go over y in pieces
-    for (unsigned first = 0; first < tiles; first += 65535) {
-        AdaptArgs part = g;
-        const int64_t t0 = (int64_t)first * kTile;
-        part.x += t0 * g.xs;
-        part.y += t0 * g.ys;
-        part.out += t0 * g.os;
-        part.ids += t0;
-        part.v += t0 * g.vs;
-        part.T = g.T - t0;
-        const unsigned n = tiles - first < 65535 ? tiles - first : 65535;
-        if (g.rank <= 16)
-            hipLaunchKernelGGL((adapt_expand_kernel<W, 4>), dim3(gx, n, g.spread), dim3(64 * kExpandWaves), lds, st, part);
-        else
-            hipLaunchKernelGGL((adapt_expand_kernel<W, 8>), dim3(gx, n, g.spread), dim3(64 * kExpandWaves), lds, st, part);
-    }
+    const dim3 grid(gt, gc, g.spread);
+    if (g.rank <= 16)
+        hipLaunchKernelGGL((adapt_expand_kernel<W, 4>), grid, dim3(64 * kExpandWaves), lds, st, g);
+    else
+        hipLaunchKernelGGL((adapt_expand_kernel<W, 8>), grid, dim3(64 * kExpandWaves), lds, st, g);
     return hipGetLastError();
 }
 
 int32_t padded_rank(int32_t rank) { return (rank + 15) / 16 * 16; }
 
 // The shrink's workgroups share a reduction until they fill the chip, down to
-// one step of 32 values per wave.
+// two steps of 32 values per wave.
 int32_t shrink_split(int64_t T, int32_t rank, int32_t in) {
     const int64_t groups = T <= kSpreadTokens ? T : (T + kTile - 1) / kTile;
     const int64_t wgs = groups * ((rank + 16 * kRowTiles - 1) / (16 * kRowTiles));
-    const int64_t most = (in + 32 * kShrinkWaves - 1) / (32 * kShrinkWaves);
+    const int64_t most = (in + 64 * kShrinkWaves - 1) / (64 * kShrinkWaves);
     int64_t s = kFill / (wgs > 0 ? wgs : 1);
     if (s > most) s = most;
     if (s > kMaxSplit) s = kMaxSplit;
@@ -388,7 +540,7 @@ hipError_t launch_adapt(const AdaptLaunch& l, hipStream_t st) {
     g.scale = l.scale;
     g.ranks = l.ranks;
     g.v = (float*)l.workspace;
-    g.T = g.total = l.T;
+    g.T = l.T;
     g.xs = l.x_stride;
     g.ys = l.y_stride;
     g.os = l.out_stride;

@@ -9,6 +9,7 @@ package fails loudly when the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -551,15 +552,23 @@ def _rows(t, name: str, T: int, width: int):
 
 def _with_workspace(call, device, workspace, nbytes, stream):
     """call(workspace pointer, its bytes, stream) with the tensors' device
-    current and the given workspace, or one allocated on the stream."""
-    with torch.cuda.device(device):
-        if workspace is None:
-            s = torch.cuda.current_stream(device) if stream is None else stream
-            with torch.cuda.stream(s):
-                workspace = torch.empty(max(nbytes(), 1), dtype=torch.uint8, device=device)
-        elif workspace.device != device:
-            raise ValueError("the workspace is on another device")
-        return call(_ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    current and the given workspace, or one allocated on the stream.
+
+    A few-token call takes the GPU a few microseconds, so the common case goes
+    past torch's context managers and stream objects (5 us of host time)."""
+    index = device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(device):
+            return _with_workspace(call, device, workspace, nbytes, stream)
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if workspace is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = torch.empty(max(nbytes(), 1), dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError("the workspace is on another device")
+    elif not workspace.is_contiguous():
+        raise ValueError("expected a contiguous workspace")
+    return call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
 
 
 def strata_moe_adapt(x: torch.Tensor, ids: torch.Tensor, adapters: Adapters, y: torch.Tensor, out: torch.Tensor,
@@ -575,7 +584,8 @@ def strata_moe_adapt(x: torch.Tensor, ids: torch.Tensor, adapters: Adapters, y: 
                                                      (out, "out", adapters.out_dim)))
     _expect(ids, "ids", (T,), torch.int32)
     _one_device(x=x, ids=ids, y=y, out=out, a=adapters.a)
-    _ptr(ids)
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
 
     def call(ws, nbytes, st):
         _check(_lib.strata_moe_adapt(x.data_ptr(), xs, ids.data_ptr(), ctypes.byref(adapters.struct), T, y.data_ptr(),

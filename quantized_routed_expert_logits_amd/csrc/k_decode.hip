@@ -108,42 +108,62 @@ __device__ __forceinline__ float round_half_away(float t) {
 }
 
 // ---------------------------------------------------------------- router
-// One workgroup: 64 experts (a lane each), one slice of H, TT tokens.
-template <int TT>
-__device__ void router_slice(const DecodeArgs& g, int group, int slice, int t0, double* lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int hs = g.H / kRouterSlices, h0 = slice * hs;
-    double* xs = lds;                       // [hs][TT]
-    double* red = lds + (size_t)hs * TT;    // [waves][TT][64]
-    for (int i = threadIdx.x; i < hs * TT; i += kThreads) {
-        const int t = t0 + i / hs, h = i % hs;
-        xs[h * TT + i / hs] = t < g.T ? (double)g.x[(int64_t)t * g.H + h0 + h] : 0.0;
-    }
-    __syncthreads();
-    const int e = group * 64 + lane;
-    double acc[TT];
+// fp64 logits on the fp64 matrix unit (16x16x4): every product of two fp32
+// values is exact and the sums are 64-bit.  One workgroup: 16 experts (the
+// product's rows), all tokens (its columns, NT tiles of 16), one slice of H,
+// which the waves split.  A lane takes 4 consecutive values of h of one token,
+// one per product, and the same 4 rows of the weights.  (On the vector unit
+// with the tokens' values broadcast from LDS, 64 tokens took 18 us: every
+// broadcast read holds the LDS for as long as a full one.)
+typedef double v4d __attribute__((ext_vector_type(4)));
+
+template <int NT>
+__device__ void router_slice(const DecodeArgs& g, int tile, int slice, double* lds) {
+    constexpr int kUnroll = NT == 4 ? 1 : 2;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, kg = lane >> 4;
+    const int steps = g.H / 16, runs = kRouterSlices * kWavesD, per = (steps + runs - 1) / runs;
+    const int first = (slice * kWavesD + wave) * per;
+    const int s0 = first < steps ? first : steps, s1 = s0 + per < steps ? s0 + per : steps;
+    const int e = tile * 16 + r16;
+    const bool gate = g.shared && e == g.E;  // the shared expert's gate is one more column
+    const float* w = gate ? g.shared_gate : g.router_w + (e < g.E ? e : g.E - 1);
+    const int stride = gate ? 1 : g.E;
+    const float* x[NT];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) acc[j] = 0.0;
-    const bool gate = e == g.E && g.shared;
-    if (e < g.E || gate) {
-        const float* w = gate ? g.shared_gate + h0 : g.router_w + (int64_t)h0 * g.E + e;
-        const int64_t step = gate ? 1 : g.E;
-#pragma unroll 4
-        for (int h = wave; h < hs; h += kWavesD) {
-            const double wv = (double)w[h * step];
+    for (int n = 0; n < NT; ++n) x[n] = g.x + (int64_t)(16 * n + r16 < g.T ? 16 * n + r16 : g.T - 1) * g.H + 4 * kg;
+    v4d acc[NT];
 #pragma unroll
-            for (int j = 0; j < TT; ++j) acc[j] = fma(wv, xs[h * TT + j], acc[j]);
+    for (int n = 0; n < NT; ++n) acc[n] = v4d{0.0, 0.0, 0.0, 0.0};
+#pragma unroll kUnroll
+    for (int s = s0; s < s1; ++s) {
+        float wv[4];
+        float4 xv[NT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wv[j] = w[(int64_t)(16 * s + 4 * kg + j) * stride];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xv[n] = *reinterpret_cast<const float4*>(x[n] + 16 * s);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float xs[4] = {xv[n].x, xv[n].y, xv[n].z, xv[n].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)wv[j], (double)xs[j], acc[n], 0, 0, 0);
         }
     }
+    // a lane has experts kg + 4 i of token 16 n + r16
 #pragma unroll
-    for (int j = 0; j < TT; ++j) red[(wave * TT + j) * 64 + lane] = acc[j];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds[((wave * NT + n) * 16 + r16) * 16 + kg + 4 * i] = acc[n][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < TT * 64; i += kThreads) {
-        const int j = i >> 6, l = i & 63, ee = group * 64 + l;
-        if (t0 + j >= g.T || ee >= g.Eg) continue;
+    for (int i = threadIdx.x; i < NT * 256; i += kThreads) {
+        const int t = i >> 4, ee = tile * 16 + (i & 15);
+        if (t >= g.T || ee >= g.Eg) continue;
         double s = 0.0;
-        for (int w = 0; w < kWavesD; ++w) s += red[(w * TT + j) * 64 + l];
-        g.part[((int64_t)slice * g.T + t0 + j) * g.Eg + ee] = s;
+#pragma unroll
+        for (int o = 0; o < kWavesD; ++o) s += lds[o * NT * 256 + i];
+        g.part[((int64_t)slice * g.T + t) * g.Eg + ee] = s;
     }
 }
 
@@ -170,15 +190,13 @@ __device__ void quantize_token(const DecodeArgs& g, int t) {
     }
 }
 
-template <int TT>
+template <int NT>
 __global__ void __launch_bounds__(kThreads) decode_router_kernel(DecodeArgs g) {
-    extern __shared__ double lds[];
-    const int groups = (g.Eg + 63) / 64, tg = (g.T + TT - 1) / TT;
-    const int nr = groups * kRouterSlices * tg;
-    const int id = blockIdx.x;
-    if (id < nr)
-        router_slice<TT>(g, id % groups, id / groups % kRouterSlices, id / groups / kRouterSlices * TT, lds);
-    else {
+    __shared__ double lds[kWavesD * NT * 256];
+    const int tiles = (g.Eg + 15) / 16, nr = tiles * kRouterSlices, id = blockIdx.x;
+    if (id < nr) {
+        router_slice<NT>(g, id % tiles, id / tiles, lds);
+    } else {
         for (int i = (id - nr) * kThreads + threadIdx.x; i < g.nclear; i += g.T * kThreads) g.clear[i] = 0;
         quantize_token(g, id - nr);
     }
@@ -782,14 +800,6 @@ Plan plan(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I, bool shared) {
     return o;
 }
 
-template <int TT>
-hipError_t launch_router_tt(const DecodeArgs& g, hipStream_t st) {
-    const int groups = (g.Eg + 63) / 64, tg = (g.T + TT - 1) / TT;
-    const size_t lds = ((size_t)(g.H / kRouterSlices) * TT + (size_t)kWavesD * TT * 64) * 8;
-    hipLaunchKernelGGL(decode_router_kernel<TT>, dim3(groups * kRouterSlices * tg + g.T), dim3(kThreads), lds, st, g);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 size_t decode_workspace(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I, bool shared) {
@@ -835,8 +845,10 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     g.nchunks = (int32_t*)(ws + o.words + 512);
     g.dn_done = (int32_t*)(ws + o.dn_done);
     g.chunks = (Chunk*)(ws + o.chunks);
-    hipError_t e = g.T == 1 ? launch_router_tt<1>(g, st) : g.T <= 4 ? launch_router_tt<4>(g, st) : launch_router_tt<8>(g, st);
-    if (e != hipSuccess) return e;
+    void (*router)(DecodeArgs) =
+        g.T <= 16 ? decode_router_kernel<1> : g.T <= 32 ? decode_router_kernel<2> : decode_router_kernel<4>;
+    hipLaunchKernelGGL(router, dim3((g.Eg + 15) / 16 * kRouterSlices + g.T), dim3(kThreads), 0, st, g);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     // The waves of a slab: all 8 while the slabs are few (their latency counts),
     // fewer as the workgroups fill the chip anyway.
     const int gu = g.I / 64, dn = g.H / kSlabRows;

@@ -58,7 +58,7 @@ struct DecodeArgs {
     int32_t Kg, Eg;        // pairs per token, experts (with the shared one)
     int32_t n;             // T * Kg
     int32_t cap;           // most chunks
-    int32_t split;         // waves that share a slab's reduction: 1, 2, 4 or 8
+    int32_t split_gu, split_dn;  // waves that share a slab's reduction: 2, 4 or 8
     int32_t gw, dw;        // workgroups per chunk: gate/up, down
     float* out;
     double* part;          // [slices][T][Eg] partial logits (column E: the shared gate's dot product)
@@ -203,87 +203,135 @@ __global__ void __launch_bounds__(kThreads) decode_router_kernel(DecodeArgs g) {
 }
 
 // ------------------------------------------------------------ top-K, softmax
-// One workgroup, one token.  A wave takes 64 logits and keeps those with
-// fewer than K larger ones among them, counted on the logits rounded to 32
-// bits (rounding never turns an order around, so a superset of the wave's
-// best K stays); the kept ones are ranked in 64 bits, ties by the lower
-// index.  A NaN ranks as -inf, so the ids are always K different ones.
+// The largest (or with kMin the smallest) of a wave's values, on every lane.
+template <bool kMin>
+__device__ __forceinline__ float wave_extreme(float x) {
+    auto step = [&](auto ctrl) {
+        const float o = __builtin_bit_cast(
+            float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, x), __builtin_bit_cast(int, x), ctrl(), 0xf, 0xf, false));
+        x = kMin ? fminf(x, o) : fmaxf(x, o);
+    };
+    step([] { return 0x111; });  // row_shr 1, 2, 4, 8
+    step([] { return 0x112; });
+    step([] { return 0x114; });
+    step([] { return 0x118; });
+    step([] { return 0x142; });  // the last lane of each row to the next row, of each half to the next half
+    step([] { return 0x143; });
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+
+// One workgroup, one token.  A wave takes 64 logits at a time and finds the
+// best few of them, on the logits rounded to 32 bits (rounding never turns an
+// order around).  The best few of every 64 together are at least K logits, so
+// the K-th of those is a floor of the K-th of all: what reaches it, hardly
+// more than K logits, is ranked in 64 bits, ties by the lower index.  A NaN
+// ranks as -inf, so the ids are always K different ones.
 struct TopkLds {
-    double v[kMaxExperts];
+    double v[kMaxExperts];  // the candidates
     int e[kMaxExperts];
-    int rank[kMaxExperts];
     double best[kMaxTopK], w[kMaxTopK];
+    float4 top[16];         // the best few of every 64
     int count;
-    int id[kMaxTopK];    // the result: experts in rank order,
-    float p[kMaxTopK];   // their weights; the shared expert's behind them
+    int id[kMaxTopK];       // the result: experts in rank order,
+    float p[kMaxTopK];      // their weights; the shared expert's behind them
 };
 
 __device__ void topk_token(const DecodeArgs& g, int t, TopkLds& l) {
+    constexpr int kGroups = kMaxExperts / 64 / kWavesD;  // groups of 64 logits per wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const double ninf = -__builtin_huge_val();
+    const float ninf = -__builtin_huge_valf();
+    const int groups = (g.E + 63) / 64, few = (g.K + groups - 1) / groups + 1;  // groups * few <= 64
     if (threadIdx.x == 0) l.count = 0;
-    __syncthreads();
-    for (int c = wave; c * 64 < g.E; c += kWavesD) {
-        const int e = c * 64 + lane;
-        double v = ninf;
+    float* top = (float*)l.top;
+    if (threadIdx.x < 64) top[threadIdx.x] = ninf;
+    double v[kGroups];
+    float f[kGroups];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int e = (wave + i * kWavesD) * 64 + lane;
+        v[i] = ninf;
+        f[i] = ninf;
         if (e < g.E) {
             double q[kRouterSlices];
 #pragma unroll
             for (int s = 0; s < kRouterSlices; ++s) q[s] = g.part[((int64_t)s * g.T + t) * g.Eg + e];
-            v = 0.0;
+            v[i] = 0.0;
 #pragma unroll
-            for (int s = 0; s < kRouterSlices; ++s) v += q[s];
-            if (g.bias) v += (double)g.bias[e];
-            if (!(v == v)) v = ninf;
+            for (int s = 0; s < kRouterSlices; ++s) v[i] += q[s];
+            if (g.bias) v[i] += (double)g.bias[e];
+            if (!(v[i] == v[i])) v[i] = ninf;
+            f[i] = (float)v[i];
         }
-        const float f = (float)v;
-        int larger = 0;
-#pragma unroll 16
-        for (int j = 0; j < 64; ++j) {
-            const float o = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), j));
-            larger += o > f ? 1 : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int c = wave + i * kWavesD;
+        if (c >= groups) break;
+        float x = f[i];
+        for (int n = 0; n < few; ++n) {  // equal ones count as one: the floor is lower then
+            const float m = wave_extreme<false>(x);
+            if (lane == 0) top[c * few + n] = m;
+            if (x == m) x = ninf;
         }
-        const bool keep = e < g.E && larger < g.K;
+    }
+    __syncthreads();
+    float floor;
+    {
+        const float x = top[lane];
+        int above = 0;
+        for (int j = 0; 4 * j < groups * few; j += 8) {  // -inf in the places behind
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 o = l.top[j + i];
+                above += (int)(o.x > x) + (int)(o.y > x) + (int)(o.z > x) + (int)(o.w > x);
+            }
+        }
+        floor = wave_extreme<true>(above < g.K && lane < groups * few ? x : __builtin_huge_valf());
+    }
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int e = (wave + i * kWavesD) * 64 + lane;
+        const bool keep = e < g.E && f[i] >= floor;
         const uint64_t kept = __ballot(keep);
+        if (kept == 0) continue;
         int base = 0;
         if (lane == 0) base = atomicAdd(&l.count, __popcll(kept));
         base = __builtin_amdgcn_readfirstlane(base);
         if (keep) {
             const int at = base + __popcll(kept & ((1ull << lane) - 1));
-            l.v[at] = v;
+            l.v[at] = v[i];
             l.e[at] = e;
-            l.rank[at] = 0;
         }
     }
-    __syncthreads();
-    const int n = l.count;
-    // rank candidate i among 4 quarters of the candidates
-    for (int i = threadIdx.x & 127; i < n; i += 128) {
-        const double v = l.v[i];
-        const int e = l.e[i], part = threadIdx.x >> 7;
-        int r = 0;
-#pragma unroll 8
-        for (int j = part; j < n; j += 4) r += (int)(l.v[j] > v) | ((int)(l.v[j] == v) & (int)(l.e[j] < e));
-        if (r) atomicAdd(&l.rank[i], r);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        if (l.rank[i] < g.K) {
-            l.best[l.rank[i]] = l.v[i];
-            l.id[l.rank[i]] = l.e[i];
-        }
     __syncthreads();
     if (wave == 0) {
-        double w = lane < g.K ? exp(l.best[lane] - l.best[0]) : 0.0;
-        double z = 0.0;
-        for (int k = 0; k < g.K; ++k) z += __shfl(w, k);
-        if (lane < g.K) l.p[lane] = (float)(w / z);
+        const int n = l.count;
+        for (int i = lane; i < n; i += 64) {
+            const double c = l.v[i];
+            const int e = l.e[i];
+            int r = 0;
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) r += (int)(l.v[j] > c) | ((int)(l.v[j] == c) & (int)(l.e[j] < e));
+            if (r < g.K) {
+                l.best[r] = c;
+                l.id[r] = e;
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (lane < g.K) l.w[lane] = exp(l.best[lane] - l.best[0]);
+        __builtin_amdgcn_wave_barrier();
+        if (lane < g.K) {
+            double z = 0.0;
+            for (int k = 0; k < g.K; ++k) z += l.w[k];
+            l.p[lane] = (float)(l.w[lane] / z);
+        }
     } else if (wave == 1 && g.shared) {
-        double v = lane < kRouterSlices ? g.part[((int64_t)lane * g.T + t) * g.Eg + g.E] : 0.0;
-        for (int o = 1; o < kRouterSlices; o <<= 1) v += __shfl_xor(v, o);
+        double s = lane < kRouterSlices ? g.part[((int64_t)lane * g.T + t) * g.Eg + g.E] : 0.0;
+        for (int o = 1; o < kRouterSlices; o <<= 1) s += __shfl_xor(s, o);
         if (lane == 0) {
             l.id[g.K] = g.E;
-            l.p[g.K] = (float)(1.0 / (1.0 + exp(-v)));
+            l.p[g.K] = (float)(1.0 / (1.0 + exp(-s)));
         }
     }
     __syncthreads();
@@ -528,10 +576,10 @@ __device__ __forceinline__ void share_sums(const Work& w, const double (&acc)[8]
 
 // Sum `at` (row j, fragment order) of the workgroup's slab s, its waves in order.
 template <bool kSym, int NI>
-__device__ __forceinline__ double slab_sum(const DecodeArgs& g, const double* lds, int s, int j, int at) {
+__device__ __forceinline__ double slab_sum(int split, const double* lds, int s, int j, int at) {
     constexpr double unit = kSym ? 0.5 : 1.0;  // the symmetric map's codes are 2 (q - 1.5)
     double v = 0.0;
-    for (int o = 0; o < g.split; ++o) v += lds[((s * g.split + o) * 4 * NI + j) * 128 + at];
+    for (int o = 0; o < split; ++o) v += lds[((s * split + o) * 4 * NI + j) * 128 + at];
     return unit * v;
 }
 
@@ -554,8 +602,8 @@ __device__ void gate_up_slabs(const DecodeArgs& g, const Work& w, double* lds) {
     const int l = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < 2 * w.nslab * w.rows; i += kThreads / 32) {
         const int hb = i & 1, s = (i >> 1) % w.nslab, j = (i >> 1) / w.nslab;
-        const double gt = slab_sum<kSym, NI>(g, lds, s, j, 32 * hb + l);
-        const double up = slab_sum<kSym, NI>(g, lds, s, j, 64 + 32 * hb + l);
+        const double gt = slab_sum<kSym, NI>(g.split_gu, lds, s, j, 32 * hb + l);
+        const double up = slab_sum<kSym, NI>(g.split_gu, lds, s, j, 64 + 32 * hb + l);
         const float h = (float)(gt / (1.0 + exp(-gt)) * up);
         float m = fabsf(h);
 #pragma unroll
@@ -613,7 +661,7 @@ __device__ void down_slabs(const DecodeArgs& g, const Work& w, double* lds, Rows
     for (int i = threadIdx.x; i < w.nslab * w.rows * 128; i += kThreads) {
         const int at = i & 127, s = (i >> 7) % w.nslab, j = (i >> 7) / w.nslab;
         poke(&g.dm[(int64_t)rows.pair[j] * g.H + 128 * (w.slab0 + s) + at],
-             (float)((double)rows.weight[j] * slab_sum<kSym, NI>(g, lds, s, j, at)));
+             (float)((double)rows.weight[j] * slab_sum<kSym, NI>(g.split_dn, lds, s, j, at)));
     }
     publish();
     if ((int)threadIdx.x < w.nslab * w.rows) {
@@ -740,12 +788,13 @@ __global__ void __launch_bounds__(kThreads, 4) decode_experts_kernel(DecodeArgs 
     const int tk = __builtin_amdgcn_readfirstlane(todo[3]);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool gate_up = tk < g.gw;
-    const int slabs = gate_up ? g.I / 64 : g.H / kSlabRows, per = kWavesD / g.split;
+    const int slabs = gate_up ? g.I / 64 : g.H / kSlabRows, split = gate_up ? g.split_gu : g.split_dn;
+    const int per = kWavesD / split;
     w.slab0 = (gate_up ? tk : tk - g.gw) * per;
     w.nslab = slabs - w.slab0 < per ? slabs - w.slab0 : per;
-    w.slab = w.slab0 + wave / g.split;
-    w.part = wave % g.split;
-    const int nblk = (gate_up ? g.H : g.I) / kBlock, run = (nblk + g.split - 1) / g.split;
+    w.slab = w.slab0 + wave / split;
+    w.part = wave % split;
+    const int nblk = (gate_up ? g.H : g.I) / kBlock, run = (nblk + split - 1) / split;
     w.b0 = w.part * run;
     w.nb = w.b0 + run <= nblk ? run : nblk - w.b0;
     // a wave without blocks or a slab still meets the others' barriers
@@ -849,14 +898,18 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
         g.T <= 16 ? decode_router_kernel<1> : g.T <= 32 ? decode_router_kernel<2> : decode_router_kernel<4>;
     hipLaunchKernelGGL(router, dim3((g.Eg + 15) / 16 * kRouterSlices + g.T), dim3(kThreads), 0, st, g);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    // The waves of a slab: all 8 while the slabs are few (their latency counts),
-    // fewer as the workgroups fill the chip anyway.
+    // The waves of a slab: all 8 while the slabs are few (the latency of one
+    // counts), fewer as the workgroups fill the chip anyway; down, whose
+    // reduction is the shorter one, halves first.  In us at H = 2560, I = 1024,
+    // E = 512, K = 10 (gate/up, down waves): one token 30.0 (8, 8), 29.2 (8,
+    // 4), 32.3 (4, 2); 8 tokens 73.6 (8, 4), 64.9 (4, 2), 73.7 (2, 2); 32
+    // tokens 184.8 (8, 4), 157.6 (4, 2), 150.7 (2, 2).
     const int gu = g.I / 64, dn = g.H / kSlabRows;
-    g.split = 8;
-    while (g.split > 2 && (int64_t)g.cap * (gu + dn) * g.split / kWavesD > 2 * kResident) g.split /= 2;
-    const int per = kWavesD / g.split;
-    g.gw = (gu + per - 1) / per;
-    g.dw = (dn + per - 1) / per;
+    const int64_t slabs = (int64_t)g.cap * (gu + dn);
+    g.split_gu = slabs <= 2000 ? 8 : slabs <= 4000 ? 4 : 2;
+    g.split_dn = slabs <= 288 ? 8 : slabs <= 2000 ? 4 : 2;
+    g.gw = (gu * g.split_gu + kWavesD - 1) / kWavesD;
+    g.dw = (dn * g.split_dn + kWavesD - 1) / kWavesD;
     size_t lds = sizeof(TopkLds) > sizeof(GroupLds) ? sizeof(TopkLds) : sizeof(GroupLds);
     const size_t sums = (size_t)kWavesD * (g.T <= kPairTokens ? 4 : 8) * 128 * 8;
     if (sums > lds) lds = sums;

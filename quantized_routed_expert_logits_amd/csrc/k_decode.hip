@@ -444,10 +444,12 @@ struct Work {
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
-template <int NI>
-struct Block {
+struct Weights {
     v4u c, d;    // a lane's 16 code bytes, its weight row's 8 fp16 scales
-    v2u q;       // its 8 activation codes
+};
+template <int NI>
+struct Acts {
+    v2u q;       // a lane's 8 activation codes
     v2u s[NI];   // scale (fp32), code sum of its activation rows
 };
 
@@ -464,17 +466,17 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int b
 
 // One block's products and scaling.
 template <bool kSym, int NI>
-__device__ __forceinline__ void block_sums(const Block<NI>& r, double (&acc)[8][NI]) {
+__device__ __forceinline__ void block_sums(const Weights& r, const Acts<NI>& x, double (&acc)[8][NI]) {
     constexpr int zp = kSym ? -3 : -1;
     double sc[NI];
     v4i z{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        sc[i] = (double)__builtin_bit_cast(float, r.s[i][0]);
-        z[i] = __mul24((int)r.s[i][1], zp);  // |sum| <= 32 * 127: a full-rate 24-bit multiply
+        sc[i] = (double)__builtin_bit_cast(float, x.s[i][0]);
+        z[i] = __mul24((int)x.s[i][1], zp);  // |sum| <= 32 * 127: a full-rate 24-bit multiply
     }
-    const v4i aA{(int)__builtin_amdgcn_perm(0u, r.q[0], 0x0c010c00u), (int)__builtin_amdgcn_perm(0u, r.q[0], 0x0c030c02u),
-                 (int)__builtin_amdgcn_perm(0u, r.q[1], 0x0c010c00u), (int)__builtin_amdgcn_perm(0u, r.q[1], 0x0c030c02u)};
+    const v4i aA{(int)__builtin_amdgcn_perm(0u, x.q[0], 0x0c010c00u), (int)__builtin_amdgcn_perm(0u, x.q[0], 0x0c030c02u),
+                 (int)__builtin_amdgcn_perm(0u, x.q[1], 0x0c010c00u), (int)__builtin_amdgcn_perm(0u, x.q[1], 0x0c030c02u)};
     const v4i aB{(int)((uint32_t)aA[0] << 8), (int)((uint32_t)aA[1] << 8), (int)((uint32_t)aA[2] << 8),
                  (int)((uint32_t)aA[3] << 8)};
     // the products of dword p + 1 run beside the scaling of dword p
@@ -504,41 +506,101 @@ __device__ __forceinline__ void block_sums(const Block<NI>& r, double (&acc)[8][
     }
 }
 
-// acc[f][i]: the sums of weight row f * 16 + r and activation row kg + 4 i
-// over the wave's blocks.  act / scl with the lane's byte offsets qo / so[i]:
-// its code row's 8 codes of the first block, its rows' scales.  ready() is
-// called once the first blocks' weights are on their way and before the
-// activations are read; kAgent: they come from other workgroups.
-template <bool kSym, int NI, bool kAgent, typename Ready>
-__device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, __amdgpu_buffer_rsrc_t act, int qo,
-                                          __amdgpu_buffer_rsrc_t scl, const int (&so)[NI], double (&acc)[8][NI],
-                                          Ready ready) {
-    constexpr int kDepth = 4;  // blocks in flight
+// Where a chunk's activation rows are: row j's codes at q + row(j) * Kd, its
+// blocks' (scale, code sum) at s + row(j) * Kd / 32 * 8.
+struct ActRows {
+    const int8_t* q;
+    const int2* s;
+    int rows_bound;  // rows of the arrays
+};
+
+// A chunk's rows in LDS: codes, act_stride() bytes apart (8 banks from row to
+// row: the 4 lanes of 8 rows read without conflict), then (scale, code sum) of
+// row j and block b at [b * kChunkTokens + j].
+__device__ __forceinline__ int act_stride(int Kd) { return Kd + 32; }
+
+template <bool kAgent, typename Row>
+__device__ __forceinline__ void stage_acts(const ActRows& a, int Kd, int rows, Row row, char* lds) {
     constexpr int aux = kAgent ? kAgentLoad : 0;
-    const int lane = threadIdx.x & 63, r16 = lane & 15;
-    const int last = w.nb > 0 ? w.nb - 1 : 0;  // past the run: its last block again, never used
+    const int nblk = Kd / kBlock, per = Kd / 16;
+    const __amdgpu_buffer_rsrc_t rq = buffer_of(a.q, a.rows_bound * Kd), rs = buffer_of(a.s, a.rows_bound * nblk * 8);
+    uint64_t* sa = (uint64_t*)(lds + kChunkTokens * act_stride(Kd));
+    for (int i = threadIdx.x; i < rows * per; i += kThreads) {
+        const int j = i / per, k = i % per;
+        *reinterpret_cast<v4u*>(lds + j * act_stride(Kd) + 16 * k) =
+            __builtin_amdgcn_raw_buffer_load_b128(rq, row(j) * Kd + 16 * k, 0, aux);
+    }
+    for (int i = threadIdx.x; i < rows * nblk; i += kThreads) {
+        const int j = i / nblk, k = i % nblk;
+        const v2u v = __builtin_amdgcn_raw_buffer_load_b64(rs, (row(j) * nblk + k) * 8, 0, aux);
+        sa[k * kChunkTokens + j] = __builtin_bit_cast(uint64_t, v);
+    }
+}
+
+// acc[f][i]: the sums of weight row f * 16 + r and activation row kg + 4 i
+// over the wave's blocks.  ready() is called once the first blocks' weights
+// are on their way and before the activations are read; kAgent: they come
+// from other workgroups.
+// kDirect: the activations come with the weights, block by block, into
+// registers (one row, where the latency of the first block counts).
+// Otherwise the workgroup stages them in LDS: their loads, 16 bytes a lane or
+// less of every 1280-byte block, took as long in the address path as those of
+// the weights (32 tokens 151 us, 136 with the activations left out).
+template <bool kSym, int NI, bool kAgent, bool kDirect, typename Row, typename Ready>
+__device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, const ActRows& a, int Kd, Row row, char* lds,
+                                          double (&acc)[8][NI], Ready ready) {
+    constexpr int kDepth = 4;  // blocks in flight (6 took 172 us for 32 tokens: the registers)
+    constexpr int aux = kAgent ? kAgentLoad : 0;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
+    const int nblk = Kd / kBlock;
+    const int mine = (r16 >> 2) + 4 * (r16 & 3);  // the row in product row r16
+    const int last = w.nb > 0 ? w.nb - 1 : 0;     // past the run: its last block again, never used
     const __amdgpu_buffer_rsrc_t rr = buffer_of(rec, (last + 1) * kRecordBytes);
-    auto load_w = [&](int b, Block<NI>& r) {
+    const __amdgpu_buffer_rsrc_t rq = buffer_of(a.q, a.rows_bound * Kd), rs = buffer_of(a.s, a.rows_bound * nblk * 8);
+    const int qrow = mine < w.rows ? mine : 0;
+    int srow[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) srow[i] = kg + 4 * i < w.rows ? kg + 4 * i : 0;
+    int qo = 0, so[NI] = {};
+    const char* ql = lds + qrow * act_stride(Kd) + w.b0 * kBlock + 8 * kg;
+    const uint64_t* sl = (const uint64_t*)(lds + kChunkTokens * act_stride(Kd)) + w.b0 * kChunkTokens;
+    if constexpr (kDirect) {
+        qo = row(qrow) * Kd + w.b0 * kBlock + 8 * kg;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) so[i] = (row(srow[i]) * nblk + w.b0) * 8;
+    }
+    auto load_w = [&](int b, Weights& r) {
         const int at = (b < last ? b : last) * kRecordBytes;
         r.c = __builtin_amdgcn_raw_buffer_load_b128(rr, lane * 16, at, 0);
         r.d = __builtin_amdgcn_raw_buffer_load_b128(rr, kRecordCodeBytes + r16 * 16, at, 0);
     };
-    auto load_a = [&](int b, Block<NI>& r) {
+    auto load_a = [&](int b, Acts<NI>& x) {
         b = b < last ? b : last;
-        r.q = __builtin_amdgcn_raw_buffer_load_b64(act, qo, b * kBlock, aux);
+        x.q = __builtin_amdgcn_raw_buffer_load_b64(rq, qo, b * kBlock, aux);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) r.s[i] = __builtin_amdgcn_raw_buffer_load_b64(scl, so[i], b * 8, aux);
+        for (int i = 0; i < NI; ++i) x.s[i] = __builtin_amdgcn_raw_buffer_load_b64(rs, so[i], b * 8, aux);
     };
-    Block<NI> ring[kDepth];
+    auto lds_a = [&](int b, Acts<NI>& x) {
+        x.q = *reinterpret_cast<const v2u*>(ql + b * kBlock);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) x.s[i] = __builtin_bit_cast(v2u, sl[b * kChunkTokens + srow[i]]);
+    };
+    Weights ring[kDepth];
+    Acts<NI> act[kDirect ? kDepth : 1];
 #pragma unroll
     for (int j = 0; j < kDepth; ++j) load_w(j, ring[j]);
     __builtin_amdgcn_sched_barrier(0);
     ready();
     asm volatile("" ::: "memory");
+    if constexpr (kDirect) {
 #pragma unroll
-    for (int j = 0; j < kDepth; ++j) {
-        load_a(j, ring[j]);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < kDepth; ++j) {
+            load_a(j, act[j]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else {
+        stage_acts<kAgent>(a, Kd, w.rows, row, lds);
+        __syncthreads();
     }
 #pragma unroll
     for (int f = 0; f < 8; ++f)
@@ -550,15 +612,22 @@ __device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, __a
     for (; b + kDepth <= w.nb; b += kDepth) {
 #pragma unroll
         for (int j = 0; j < kDepth; ++j) {
-            block_sums<kSym, NI>(ring[j], acc);
+            Acts<NI>& x = act[kDirect ? j : 0];
+            if constexpr (!kDirect) lds_a(b + j, x);
+            block_sums<kSym, NI>(ring[j], x, acc);
             load_w(b + j + kDepth, ring[j]);
-            load_a(b + j + kDepth, ring[j]);
+            if constexpr (kDirect) load_a(b + j + kDepth, x);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
 #pragma unroll
     for (int j = 0; j < kDepth - 1; ++j)
-        if (b + j < w.nb) block_sums<kSym, NI>(ring[j], acc);
+        if (b + j < w.nb) {
+            Acts<NI>& x = act[kDirect ? j : 0];
+            if constexpr (!kDirect) lds_a(b + j, x);
+            block_sums<kSym, NI>(ring[j], x, acc);
+        }
+    if constexpr (!kDirect) __syncthreads();  // the activations are read: their LDS takes the sums
 }
 
 // Every wave's sums to LDS: [wave][4 NI][128], row j of the chunk, fragment
@@ -586,18 +655,13 @@ __device__ __forceinline__ double slab_sum(int split, const double* lds, int s, 
 // Gate/up of the workgroup's slabs: h = silu(G) U, rounded to int8.  Slab
 // columns 0..63 are gate rows, 64..127 the up rows of the same H values; half
 // a wave takes a block of 32.
-template <bool kSym, int NI>
+template <bool kSym, int NI, bool kDirect>
 __device__ void gate_up_slabs(const DecodeArgs& g, const Work& w, double* lds) {
-    const int nblk = g.H / kBlock;
-    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
-    const int mine = (r16 >> 2) + 4 * (r16 & 3);  // the row in product row r16
-    const int qo = w.tok[mine < w.rows ? mine : 0] * g.H + w.b0 * kBlock + 8 * kg;
-    int so[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) so[i] = (w.tok[kg + 4 * i < w.rows ? kg + 4 * i : 0] * nblk + w.b0) * 8;
-    const uint8_t* rec = g.gate_up + (int64_t)w.e * g.gate_up_stride + ((int64_t)w.slab * nblk + w.b0) * kRecordBytes;
+    const uint8_t* rec = g.gate_up + (int64_t)w.e * g.gate_up_stride +
+                         ((int64_t)w.slab * (g.H / kBlock) + w.b0) * kRecordBytes;
     double acc[8][NI];
-    slab_sums<kSym, NI, false>(w, rec, buffer_of(g.qx, g.T * g.H), qo, buffer_of(g.sx, g.T * nblk * 8), so, acc, [] {});
+    slab_sums<kSym, NI, false, kDirect>(
+        w, rec, ActRows{g.qx, g.sx, g.T}, g.H, [&](int j) { return w.tok[j]; }, (char*)lds, acc, [] {});
     share_sums<NI>(w, acc, lds);
     const int l = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < 2 * w.nslab * w.rows; i += kThreads / 32) {
@@ -635,18 +699,13 @@ struct Rows {
     int last[kChunkTokens * kWavesD];  // [slab][row]
 };
 
-template <bool kSym, int NI>
+template <bool kSym, int NI, bool kDirect>
 __device__ void down_slabs(const DecodeArgs& g, const Work& w, double* lds, Rows& rows, bool known) {
-    const int nblk = g.I / kBlock, nslab = g.H / kSlabRows;
-    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
-    const int mine = (r16 >> 2) + 4 * (r16 & 3);
-    const int qo = (w.row0 + (mine < w.rows ? mine : 0)) * g.I + w.b0 * kBlock + 8 * kg;
-    int so[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) so[i] = ((w.row0 + (kg + 4 * i < w.rows ? kg + 4 * i : 0)) * nblk + w.b0) * 8;
-    const uint8_t* rec = g.down + (int64_t)w.e * g.down_stride + ((int64_t)w.slab * nblk + w.b0) * kRecordBytes;
+    const int nslab = g.H / kSlabRows;
+    const uint8_t* rec = g.down + (int64_t)w.e * g.down_stride +
+                         ((int64_t)w.slab * (g.I / kBlock) + w.b0) * kRecordBytes;
     double acc[8][NI];
-    slab_sums<kSym, NI, true>(w, rec, buffer_of(g.qh, g.n * g.I), qo, buffer_of(g.sh, g.n * nblk * 8), so, acc, [&] {
+    auto ready = [&] {
         // the rows' pairs and weights, then the chunk's H rows
         if (!known && (int)threadIdx.x < w.rows) {
             const int pair = peek(&g.row_pair[w.row0 + threadIdx.x]);
@@ -656,7 +715,9 @@ __device__ void down_slabs(const DecodeArgs& g, const Work& w, double* lds, Rows
         if (threadIdx.x == 0)
             for (int n = 0; n < kMaxPolls && peek(&g.chunks[w.c].gu_done) < g.gw; ++n) __builtin_amdgcn_s_sleep(2);
         __syncthreads();
-    });
+    };
+    slab_sums<kSym, NI, true, kDirect>(
+        w, rec, ActRows{g.qh, g.sh, g.n}, g.I, [&](int j) { return w.row0 + j; }, (char*)lds, acc, ready);
     share_sums<NI>(w, acc, lds);
     for (int i = threadIdx.x; i < w.nslab * w.rows * 128; i += kThreads) {
         const int at = i & 127, s = (i >> 7) % w.nslab, j = (i >> 7) / w.nslab;
@@ -802,14 +863,14 @@ __global__ void __launch_bounds__(kThreads, 4) decode_experts_kernel(DecodeArgs 
     if (w.slab >= slabs) w.nb = 0, w.slab = w.slab0;
     if (gate_up) {
         if (!kPairs && w.rows > 4)
-            gate_up_slabs<kSym, 2>(g, w, lds);
+            gate_up_slabs<kSym, 2, false>(g, w, lds);
         else
-            gate_up_slabs<kSym, 1>(g, w, lds);
+            gate_up_slabs<kSym, 1, kPairs>(g, w, lds);
     } else {
         if (!kPairs && w.rows > 4)
-            down_slabs<kSym, 2>(g, w, lds, rows, false);
+            down_slabs<kSym, 2, false>(g, w, lds, rows, false);
         else
-            down_slabs<kSym, 1>(g, w, lds, rows, kPairs);
+            down_slabs<kSym, 1, kPairs>(g, w, lds, rows, kPairs);
     }
 }
 
@@ -913,6 +974,11 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     size_t lds = sizeof(TopkLds) > sizeof(GroupLds) ? sizeof(TopkLds) : sizeof(GroupLds);
     const size_t sums = (size_t)kWavesD * (g.T <= kPairTokens ? 4 : 8) * 128 * 8;
     if (sums > lds) lds = sums;
+    if (g.T > kPairTokens)
+        for (const int Kd : {g.H, g.I}) {
+            const size_t acts = (size_t)kChunkTokens * (Kd + 32) + (size_t)kChunkTokens * (Kd / kBlock) * 8;
+            if (acts > lds) lds = acts;
+        }
     const dim3 grid(g.cap * (g.gw + g.dw));
     void (*kernel)(DecodeArgs);
     if (g.T <= kPairTokens)

@@ -31,8 +31,7 @@ constexpr int kResident = 512;     // workgroups of the expert kernel that run a
 // caller let two calls share a workspace; then the results are lost, not the GPU.
 constexpr int kMaxPolls = 1 << 21;
 
-// A chunk is up to 8 rows of one expert.  head and mask are nonzero once
-// written.  What is polled, counted and drawn has a line of its own (next to
+// A chunk is up to 8 rows of one expert.  What is polled, counted and drawn has a line of its own (next to
 // each other the counters' additions queued behind the polls).
 struct Chunk {
     uint64_t head;  // expert << 32 | first row << 16 | rows
@@ -746,112 +745,33 @@ __device__ void down_slabs(const DecodeArgs& g, const Work& w, double* lds, Rows
     }
 }
 
-// Everything after the router in one launch.  Workgroup id -> chunk is fixed
-// (chunk_of); what the workgroup does for its chunk is its next group of
-// slabs, gate/up before down, by the chunk's ticket.  A workgroup that waits
-// for the H rows of its chunk thus knows that their slabs are all in the hands
-// of workgroups that run, and those wait for nothing but the top-K, which any
+// Everything after the router in one launch.  A workgroup's number gives its
+// chunk (chunk_of); what it does for the chunk is its next group of slabs,
+// gate/up before down, by the chunk's ticket.  A workgroup that waits for the
+// H rows of its chunk thus knows that their slabs are all in the hands of
+// workgroups that run, and those wait for nothing but the top-K, which any
 // waiting workgroup takes on itself while there are tokens left: every wait
 // ends whatever order the workgroups start in and whatever else runs on the
-// GPU.
-// Up to kPairTokens tokens a chunk is one pair and every workgroup finds its
-// expert by the token's top-K itself: the experts that two tokens share are
-// few there, and the hand-offs of the grouping cost more than the top-K.
-__device__ int chunk_of(const DecodeArgs& g, int id) {
+// GPU.  (One ticket for all workgroups in a loop over the work, with the next
+// ticket drawn ahead, took 162 us for 32 tokens against 138.)
+__device__ int chunk_of(const DecodeArgs& g, int id, int nch) {
     // gate/up runs `lag` chunks ahead of down, more than run at once
     int lag = kResident / g.gw + 1;
-    if (lag > g.cap) lag = g.cap;
+    if (lag > nch) lag = nch;
     if (id < lag * g.gw) return id / g.gw;
     id -= lag * g.gw;
-    const int both = g.gw + g.dw, whole = (g.cap - lag) * both;
+    const int both = g.gw + g.dw, whole = (nch - lag) * both;
     if (id < whole) return id % both < g.gw ? lag + id / both : id / both;
-    return g.cap - lag + (id - whole) / g.dw;
+    return nch - lag + (id - whole) / g.dw;
 }
 
-template <bool kSym, bool kPairs>
-__global__ void __launch_bounds__(kThreads, 4) decode_experts_kernel(DecodeArgs g) {
-    extern __shared__ double lds[];
-    __shared__ int todo[4];      // what thread 0 found
-    __shared__ uint64_t chunk[2];
-    __shared__ int tok[kChunkTokens];
-    __shared__ Rows rows;
-    const int c = chunk_of(g, blockIdx.x);
-    int ticket = 0;
-    if (threadIdx.x == 0) ticket = bump(&g.chunks[c].ticket);
-    Work w;
-    w.c = c;
-    w.tok = tok;
-    if constexpr (kPairs) {
-        TopkLds& l = *(TopkLds*)lds;
-        const int t = c / g.Kg, k = c % g.Kg;
-        topk_token(g, t, l);
-        w.e = __builtin_amdgcn_readfirstlane(l.id[k]);
-        w.row0 = c;
-        w.rows = 1;
-        if (threadIdx.x == 0) {
-            todo[3] = ticket;
-            tok[0] = t;
-            rows.pair[0] = c;
-            rows.weight[0] = l.p[k];
-        }
-    } else {
-        for (;;) {
-            if (threadIdx.x == 0) {
-                int what = 3;  // give up
-                for (int n = 0; n < kMaxPolls; ++n) {
-                    const uint64_t head = peek(&g.chunks[c].head), mask = peek(&g.chunks[c].mask);
-                    const int nch = peek(g.nchunks);
-                    if (nch > 0 && c >= nch - 1) break;
-                    if (nch > 0 && head != 0 && mask != 0) {
-                        chunk[0] = head, chunk[1] = mask;
-                        what = 0;
-                        break;
-                    }
-                    if (nch == 0 && peek(g.topk_next) < g.T) {
-                        const int t = bump(g.topk_next);
-                        if (t < g.T) {
-                            todo[1] = t;
-                            what = 1;
-                            break;
-                        }
-                    }
-                    __builtin_amdgcn_s_sleep(1);
-                }
-                todo[0] = what;
-                todo[3] = ticket;
-            }
-            __syncthreads();
-            const int what = __builtin_amdgcn_readfirstlane(todo[0]);
-            if (what == 3) return;
-            if (what == 0) break;
-            TopkLds& l = *(TopkLds*)lds;
-            const int t = todo[1];
-            topk_token(g, t, l);
-            if ((int)threadIdx.x < g.Kg) {
-                poke(&g.ids[t * g.Kg + threadIdx.x], l.id[threadIdx.x]);
-                poke(&g.p[t * g.Kg + threadIdx.x], l.p[threadIdx.x]);
-            }
-            publish();
-            if (threadIdx.x == 0) todo[2] = bump(g.topk_done) == g.T - 1;
-            __syncthreads();
-            if (todo[2]) group_pairs(g, *(GroupLds*)lds);
-            __syncthreads();
-        }
-        w.e = __builtin_amdgcn_readfirstlane((int)(chunk[0] >> 32));
-        w.row0 = __builtin_amdgcn_readfirstlane((int)(chunk[0] >> 16 & 0xffff));
-        w.rows = __builtin_amdgcn_readfirstlane((int)(chunk[0] & 0xffff));
-        if (threadIdx.x < 64) {
-            const uint64_t mask = chunk[1];
-            if (mask >> threadIdx.x & 1) tok[__popcll(mask & ((1ull << threadIdx.x) - 1))] = threadIdx.x;
-        }
-    }
-    __syncthreads();
-    const int tk = __builtin_amdgcn_readfirstlane(todo[3]);
+// The wave's part of the workgroup's slabs.
+__device__ __forceinline__ bool split_slabs(const DecodeArgs& g, int ticket, Work& w) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const bool gate_up = tk < g.gw;
+    const bool gate_up = ticket < g.gw;
     const int slabs = gate_up ? g.I / 64 : g.H / kSlabRows, split = gate_up ? g.split_gu : g.split_dn;
     const int per = kWavesD / split;
-    w.slab0 = (gate_up ? tk : tk - g.gw) * per;
+    w.slab0 = (gate_up ? ticket : ticket - g.gw) * per;
     w.nslab = slabs - w.slab0 < per ? slabs - w.slab0 : per;
     w.slab = w.slab0 + wave / split;
     w.part = wave % split;
@@ -861,16 +781,116 @@ __global__ void __launch_bounds__(kThreads, 4) decode_experts_kernel(DecodeArgs 
     // a wave without blocks or a slab still meets the others' barriers
     if (w.nb <= 0) w.nb = 0, w.b0 = 0;
     if (w.slab >= slabs) w.nb = 0, w.slab = w.slab0;
-    if (gate_up) {
-        if (!kPairs && w.rows > 4)
+    return gate_up;
+}
+
+// Up to kPairTokens tokens: a chunk is one pair and every workgroup finds its
+// expert by the token's top-K itself.  The experts that two tokens share are
+// few there, and the hand-offs of the grouping cost more than the top-K.
+template <bool kSym>
+__global__ void __launch_bounds__(kThreads, 4) decode_pairs_kernel(DecodeArgs g) {
+    extern __shared__ double lds[];
+    __shared__ int taken;
+    __shared__ int tok[kChunkTokens];
+    __shared__ Rows rows;
+    const int c = chunk_of(g, blockIdx.x, g.n);
+    int ticket = 0;
+    if (threadIdx.x == 0) ticket = bump(&g.chunks[c].ticket);
+    TopkLds& l = *(TopkLds*)lds;
+    const int t = c / g.Kg, k = c % g.Kg;
+    topk_token(g, t, l);
+    Work w;
+    w.c = w.row0 = c;
+    w.tok = tok;
+    w.e = __builtin_amdgcn_readfirstlane(l.id[k]);
+    w.rows = 1;
+    if (threadIdx.x == 0) {
+        taken = ticket;
+        tok[0] = t;
+        rows.pair[0] = c;
+        rows.weight[0] = l.p[k];
+    }
+    __syncthreads();
+    if (split_slabs(g, __builtin_amdgcn_readfirstlane(taken), w))
+        gate_up_slabs<kSym, 1, true>(g, w, lds);
+    else
+        down_slabs<kSym, 1, true>(g, w, lds, rows, true);
+}
+
+// More tokens: the top-K of the tokens and the grouping by whichever
+// workgroups come first, then a chunk's slabs each.
+template <bool kSym>
+__global__ void __launch_bounds__(kThreads, 4) decode_chunks_kernel(DecodeArgs g) {
+    extern __shared__ double lds[];
+    __shared__ int todo[4];  // what thread 0 found
+    __shared__ Chunk chunk;
+    __shared__ int tok[kChunkTokens];
+    __shared__ Rows rows;
+    for (;;) {
+        if (threadIdx.x == 0) {
+            int what = 2;  // nothing
+            for (int n = 0; n < kMaxPolls; ++n) {
+                const int nch = peek(g.nchunks) - 1;
+                if (nch >= 0) {
+                    // (more workgroups are launched than the chunks may need)
+                    if ((int)blockIdx.x < nch * (g.gw + g.dw)) {
+                        const int c = chunk_of(g, blockIdx.x, nch);
+                        const uint64_t head = peek(&g.chunks[c].head), mask = peek(&g.chunks[c].mask);
+                        chunk.ticket = bump(&g.chunks[c].ticket);
+                        chunk.head = head, chunk.mask = mask;
+                        todo[1] = c;
+                        what = 0;
+                    }
+                    break;
+                }
+                if (peek(g.topk_next) < g.T) {
+                    const int t = bump(g.topk_next);
+                    if (t < g.T) {
+                        todo[1] = t;
+                        what = 1;
+                        break;
+                    }
+                }
+                __builtin_amdgcn_s_sleep(1);
+            }
+            todo[0] = what;
+        }
+        __syncthreads();
+        const int what = __builtin_amdgcn_readfirstlane(todo[0]);
+        if (what == 2) return;
+        if (what == 0) break;
+        TopkLds& l = *(TopkLds*)lds;
+        const int t = todo[1];
+        topk_token(g, t, l);
+        if ((int)threadIdx.x < g.Kg) {
+            poke(&g.ids[t * g.Kg + threadIdx.x], l.id[threadIdx.x]);
+            poke(&g.p[t * g.Kg + threadIdx.x], l.p[threadIdx.x]);
+        }
+        publish();
+        if (threadIdx.x == 0) todo[2] = bump(g.topk_done) == g.T - 1;
+        __syncthreads();
+        if (todo[2]) group_pairs(g, *(GroupLds*)lds);
+        __syncthreads();
+    }
+    const uint64_t mask = chunk.mask;
+    if (threadIdx.x < 64 && (mask >> threadIdx.x & 1)) tok[__popcll(mask & ((1ull << threadIdx.x) - 1))] = threadIdx.x;
+    __syncthreads();
+    Work w;
+    w.c = __builtin_amdgcn_readfirstlane(todo[1]);
+    w.e = __builtin_amdgcn_readfirstlane((int)(chunk.head >> 32));
+    w.row0 = __builtin_amdgcn_readfirstlane((int)(chunk.head >> 16 & 0xffff));
+    w.rows = __builtin_amdgcn_readfirstlane((int)(chunk.head & 0xffff));
+    w.tok = tok;
+    if (split_slabs(g, __builtin_amdgcn_readfirstlane(chunk.ticket), w)) {
+        if (w.rows > 4)
             gate_up_slabs<kSym, 2, false>(g, w, lds);
         else
-            gate_up_slabs<kSym, 1, kPairs>(g, w, lds);
+            gate_up_slabs<kSym, 1, false>(g, w, lds);
     } else {
-        if (!kPairs && w.rows > 4)
+        if (w.rows > 4)
             down_slabs<kSym, 2, false>(g, w, lds, rows, false);
         else
-            down_slabs<kSym, 1, kPairs>(g, w, lds, rows, kPairs);
+            down_slabs<kSym, 1, false>(g, w, lds, rows, false);
     }
 }
 
@@ -982,9 +1002,9 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     const dim3 grid(g.cap * (g.gw + g.dw));
     void (*kernel)(DecodeArgs);
     if (g.T <= kPairTokens)
-        kernel = l.sym ? decode_experts_kernel<true, true> : decode_experts_kernel<false, true>;
+        kernel = l.sym ? decode_pairs_kernel<true> : decode_pairs_kernel<false>;
     else
-        kernel = l.sym ? decode_experts_kernel<true, false> : decode_experts_kernel<false, false>;
+        kernel = l.sym ? decode_chunks_kernel<true> : decode_chunks_kernel<false>;
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), lds, st, g);
     return hipGetLastError();
 }

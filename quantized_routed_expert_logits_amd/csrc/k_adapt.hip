@@ -51,6 +51,11 @@ constexpr int kPad = 4;           // floats between the LDS rows of v (spreads t
 // ones have tiles enough to fill the chip.
 constexpr int kSpreadTokens = 256;
 constexpr int kFill = 512;        // workgroups that fill the chip
+// The outputs are stored past the caches, and y is read past them from this
+// many bytes on: x then stays in the Infinity Cache (8192 tokens of 2560: 109
+// us at rank 64 and 72 at rank 16 without either, 105 and 67 with the stores,
+// 90 and 59 with both; 2048 tokens at rank 16: 28.0, 27.4, 29.5).
+constexpr int64_t kStreamBytes = (int64_t)48 << 20;
 // From this many tiles on every XCD takes a run of neighbouring tiles: prompts
 // share adapters with their neighbours, and an L2 then holds two or three of
 // them instead of all (8192 tokens, 16 adapters of rank 64, the shrink: 52 us
@@ -310,7 +315,7 @@ __device__ __forceinline__ void shrink_steps(const AdaptArgs& g, const W* const 
 // One workgroup: a tile, up to 64 ranks of its groups, one part of the
 // reduction over in, which its waves split again.
 template <typename W>
-__global__ void __launch_bounds__(64 * kShrinkWaves) adapt_shrink_kernel(AdaptArgs g) {
+__global__ void __launch_bounds__(64 * kShrinkWaves, 4) adapt_shrink_kernel(AdaptArgs g) {
     // the waves' panels, then their sums
     constexpr int kWaveBytes = 2048 + kRowTiles * 64 * 8 * (int)sizeof(W);
     constexpr int kSumBytes = kRowTiles * kTile * kTile * (int)sizeof(float);
@@ -370,9 +375,10 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) adapt_shrink_kernel(AdaptAr
 }
 
 // One workgroup: a tile's groups, `turns` runs of 64 outputs per wave.  P
-// consecutive ranks per lane: 4 for ranks up to 16, else 8.
-template <typename W, int P>
-__global__ void __launch_bounds__(64 * kExpandWaves) adapt_expand_kernel(AdaptArgs g) {
+// consecutive ranks per lane: 4 for ranks up to 16, else 8.  kStream: y is
+// large, and is read past the caches.
+template <typename W, int P, bool kStream>
+__global__ void __launch_bounds__(64 * kExpandWaves, 3) adapt_expand_kernel(AdaptArgs g) {
     constexpr int kTiles = kExpandCols / 16;
     constexpr int kRow = kExpandCols + kPad;  // floats of an output row in LDS
     constexpr int kPanel = 64 * P * (int)sizeof(W);
@@ -428,8 +434,10 @@ __global__ void __launch_bounds__(64 * kExpandWaves) adapt_expand_kernel(AdaptAr
             v4f s[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if ((group >> (kg + 4 * i) & 1) && 4 * r16 + 4 <= cols)
-                    s[i] = load4(g.y + (t0 + kg + 4 * i) * g.ys + o0 + 4 * r16);
+                if ((group >> (kg + 4 * i) & 1) && 4 * r16 + 4 <= cols) {
+                    const v4f_any* y = reinterpret_cast<const v4f_any*>(g.y + (t0 + kg + 4 * i) * g.ys + o0 + 4 * r16);
+                    s[i] = kStream ? __builtin_nontemporal_load(y) : *y;
+                }
             v4f acc[kTiles], lo[kTiles];
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) acc[i] = lo[i] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(64 * kExpandWaves) adapt_expand_kernel(AdaptAr
                     if (rank > 0)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) s[i][j] = fmaf(scale, d[j], s[i][j]);
-                    *reinterpret_cast<v4f_any*>(out) = s[i];
+                    __builtin_nontemporal_store(s[i], reinterpret_cast<v4f_any*>(out));
                 } else {
                     for (int j = 0; j < 4 && 4 * r16 + j < cols; ++j) out[j] = rank > 0 ? fmaf(scale, d[j], y[j]) : y[j];
                 }
@@ -502,10 +510,12 @@ hipError_t launch_typed(AdaptArgs g, hipStream_t st) {
     g.turns = (cols + gc - 1) / gc;
     const size_t lds = (size_t)kTile * g.ls * sizeof(float);
     const dim3 grid(gt, gc, g.spread);
-    if (g.rank <= 16)
-        hipLaunchKernelGGL((adapt_expand_kernel<W, 4>), grid, dim3(64 * kExpandWaves), lds, st, g);
+    void (*expand)(AdaptArgs);
+    if (g.T * g.out_dim * 4 >= kStreamBytes)
+        expand = g.rank <= 16 ? adapt_expand_kernel<W, 4, true> : adapt_expand_kernel<W, 8, true>;
     else
-        hipLaunchKernelGGL((adapt_expand_kernel<W, 8>), grid, dim3(64 * kExpandWaves), lds, st, g);
+        expand = g.rank <= 16 ? adapt_expand_kernel<W, 4, false> : adapt_expand_kernel<W, 8, false>;
+    hipLaunchKernelGGL(expand, grid, dim3(64 * kExpandWaves), lds, st, g);
     return hipGetLastError();
 }
 

@@ -81,10 +81,14 @@ SIZES = [
     (65, 96, 80, 5, 3, 0, "runs"),
     (100, 260, 100, 100, 2, 0, "runs"),
     (130, 384, 640, 256, 3, 0, "runs"),
+    (256, 100, 70, 9, 6, 0, "random"),       # the last call that spreads a tile's adapters
+    (257, 100, 70, 9, 6, 0, "random"),
     (500, 33, 65, 17, 9, 5, "random"),
+    (1000, 544, 200, 65, 4, 0, "runs"),      # a second run of 64 ranks, a step that ends inside it
     (1025, 512, 256, 8, 7, 0, "runs"),
     (2049, 640, 1024, 32, 6, 0, "runs"),
     (700, 2560, 2560, 64, 8, 0, "runs"),
+    (5000, 48, 2564, 20, 3, 0, "runs"),      # y read past the caches, outputs that end inside a run
     (3, 65536, 5, 3, 2, 0, "random"),
     (2, 8, 65536, 4, 2, 0, "random"),
 ]

@@ -58,7 +58,11 @@ SIZES = [
     S.custom(T=33, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),
     S.custom(T=40, H=256, E=31, K=15, I=64, skewed=True, shared=True),    # n = 640 pairs, hot experts
     S.custom(T=5, H=1280, E=12, K=3, I=448),
+    S.custom(T=4, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),       # the last call with every pair on its own
+    S.custom(T=5, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),       # the first grouped one
+    S.custom(T=16, H=768, E=129, K=9, I=256, skewed=True),                # three groups of logits, one of one expert
     S.custom(T=3, H=4096, E=3, K=1, I=64),                                # the widest hidden size
+    S.custom(T=9, H=4096, E=3, K=2, I=128, shared=True),
     S.custom(T=2, H=128, E=3, K=2, I=4096),                               # the widest FFN
     S.custom(T=64, H=128, E=1024, K=16, I=64),                            # the most experts and pairs
     S.custom(T=64, H=128, E=1023, K=15, I=64, shared=True),
@@ -115,6 +119,18 @@ def test_equal_logits_zero_rows_and_tiny_values(qm):
     err = np.abs(y.cpu().numpy() - ref["y"])
     assert np.all(err <= _bound(s, ref) + 2.0 ** -148)  # an fp32 subnormal's own spacing
     assert np.all(y[1].cpu().numpy() == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 6])
+def test_ties_over_many_experts(qm, T):
+    """Equal logits across the groups of 64 that the top-K takes at a time:
+    every expert equal, and columns that come in equal pairs far apart."""
+    s = S.custom(T=T, H=128, E=300, K=12, I=64)
+    x, ex = S.activations(s), gpu_experts(s)
+    for wr in (np.zeros((s.H, s.E), np.float32), np.tile(S.router_weight(s)[:, :150], (1, 2))):
+        y = qm.strata_moe_decode(_t(x), _t(wr), ex, s.K, torch.empty((s.T, s.H), device="cuda"))
+        _check(s, y, _oracle(s, x, wr))
 
 
 @pytest.mark.gpu
@@ -205,6 +221,48 @@ def test_adapters_beside_the_layer(qm):
     p = qm.strata_moe_prefill(x, wr, ex, s.K, torch.empty_like(x))
     qm.strata_moe_adapt(x, ids, ad, p, p)
     assert rel_err(y.cpu().numpy(), p.cpu().numpy()) <= 2e-3
+    # captured, with other requests in each replay
+    out = torch.empty_like(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qm.strata_moe_decode(x, wr, ex, s.K, out, adapters=ad, adapter_ids=ids)
+    for i in range(3):
+        ids.copy_(torch.randint(-1, 4, (s.T,), generator=rng, dtype=torch.int32).cuda())
+        ref = qm.strata_moe_decode(x, wr, ex, s.K, torch.empty_like(x), adapters=ad, adapter_ids=ids)
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+
+
+@pytest.mark.gpu
+def test_a_decode_loop_on_a_stream_of_its_own(qm):
+    """Calls one after another on one stream and one workspace, each on the
+    output of the last, beside other work on the default stream."""
+    s = S.custom(T=8, H=256, E=16, K=2, I=128)
+    wr, ex = _t(S.router_weight(s)), gpu_experts(s)
+
+    def loop(stream):
+        with torch.cuda.stream(stream):
+            x = _t(S.activations(s))
+            ws = torch.empty(qm.strata_moe_decode_workspace_bytes(s.T, s.K, ex), dtype=torch.uint8, device="cuda")
+            for _ in range(6):
+                y = qm.strata_moe_decode(x, wr, ex, s.K, torch.empty_like(x), workspace=ws)
+                x = y / y.abs().amax(1, keepdim=True)
+        return x
+
+    ref = loop(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    busy = torch.randn((2048, 2048), device="cuda")
+    for _ in range(20):
+        busy = torch.tanh(busy @ busy / 64)
+    y = loop(side)
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref)
 
 
 # -------------------------------------------------------- refusals (no GPU)

@@ -27,8 +27,10 @@ constexpr int kWavesD = kThreads / 64;
 constexpr int kChunkTokens = 8;    // rows of a chunk at most
 constexpr int kPairTokens = 4;     // calls of at most this many tokens keep every pair on its own
 constexpr int kResident = 512;     // workgroups of the expert kernel that run at once, about
-// Polls before a wait gives up (seconds).  A wait ends by itself unless the
-// caller let two calls share a workspace; then the results are lost, not the GPU.
+// Polls before a wait gives up (seconds).  A wait ends by itself unless two
+// calls at once were given one workspace.  Their results are lost then, but
+// every wait still ends, and what a workgroup reads from the workspace as an
+// index is held inside its range, so nothing outside the arrays is touched.
 constexpr int kMaxPolls = 1 << 21;
 
 // A chunk is up to 8 rows of one expert.  What is polled, counted and drawn has a line of its own (next to
@@ -93,6 +95,8 @@ __device__ __forceinline__ void poke(V* p, V v) {
 __device__ __forceinline__ int bump(int32_t* p) {
     return __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// An index read from the workspace, in [0, n) whatever was read.
+__device__ __forceinline__ int in_range(int i, int n) { return (uint32_t)i < (uint32_t)n ? i : n - 1; }
 // The wave's stores are done.
 __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // Every wave's stores are done once the workgroup is past this.
@@ -354,7 +358,7 @@ __device__ void group_pairs(const DecodeArgs& g, GroupLds& l) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int i = threadIdx.x + j * kThreads;
-        id[j] = i < g.n ? peek(&g.ids[i]) & (kMaxExperts - 1) : -1;
+        id[j] = i < g.n ? in_range(peek(&g.ids[i]), g.Eg) : -1;
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
@@ -386,7 +390,7 @@ __device__ void group_pairs(const DecodeArgs& g, GroupLds& l) {
         for (int r = 0; r < c; r += kChunkTokens) {
             uint64_t rest = left;
             for (int k = 0; k < kChunkTokens; ++k) rest &= rest - 1;  // without the lowest 8 tokens
-            const int ci = (g.shared && e == g.E ? 0 : first + (at >> 16)) + r / kChunkTokens;
+            const int ci = in_range((g.shared && e == g.E ? 0 : first + (at >> 16)) + r / kChunkTokens, g.cap);
             const int rows = c - r < kChunkTokens ? c - r : kChunkTokens;
             poke(&g.chunks[ci].head, ((uint64_t)e << 32) | ((uint64_t)((at & 0xffff) + r) << 16) | (uint64_t)rows);
             poke(&g.chunks[ci].mask, left ^ rest);
@@ -707,7 +711,7 @@ __device__ void down_slabs(const DecodeArgs& g, const Work& w, double* lds, Rows
     auto ready = [&] {
         // the rows' pairs and weights, then the chunk's H rows
         if (!known && (int)threadIdx.x < w.rows) {
-            const int pair = peek(&g.row_pair[w.row0 + threadIdx.x]);
+            const int pair = in_range(peek(&g.row_pair[w.row0 + threadIdx.x]), g.n);
             rows.pair[threadIdx.x] = pair;
             rows.weight[threadIdx.x] = peek(&g.p[pair]);
         }
@@ -768,6 +772,7 @@ __device__ int chunk_of(const DecodeArgs& g, int id, int nch) {
 // The wave's part of the workgroup's slabs.
 __device__ __forceinline__ bool split_slabs(const DecodeArgs& g, int ticket, Work& w) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    ticket = in_range(ticket, g.gw + g.dw);
     const bool gate_up = ticket < g.gw;
     const int slabs = gate_up ? g.I / 64 : g.H / kSlabRows, split = gate_up ? g.split_gu : g.split_dn;
     const int per = kWavesD / split;
@@ -830,8 +835,9 @@ __global__ void __launch_bounds__(kThreads, 4) decode_chunks_kernel(DecodeArgs g
         if (threadIdx.x == 0) {
             int what = 2;  // nothing
             for (int n = 0; n < kMaxPolls; ++n) {
-                const int nch = peek(g.nchunks) - 1;
+                int nch = peek(g.nchunks) - 1;
                 if (nch >= 0) {
+                    if (nch > g.cap) nch = g.cap;
                     // (more workgroups are launched than the chunks may need)
                     if ((int)blockIdx.x < nch * (g.gw + g.dw)) {
                         const int c = chunk_of(g, blockIdx.x, nch);
@@ -845,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_chunks_kernel(DecodeArgs g
                 }
                 if (peek(g.topk_next) < g.T) {
                     const int t = bump(g.topk_next);
-                    if (t < g.T) {
+                    if ((uint32_t)t < (uint32_t)g.T) {
                         todo[1] = t;
                         what = 1;
                         break;
@@ -873,14 +879,19 @@ __global__ void __launch_bounds__(kThreads, 4) decode_chunks_kernel(DecodeArgs g
         __syncthreads();
     }
     const uint64_t mask = chunk.mask;
-    if (threadIdx.x < 64 && (mask >> threadIdx.x & 1)) tok[__popcll(mask & ((1ull << threadIdx.x) - 1))] = threadIdx.x;
-    __syncthreads();
+    const int most = g.n < kChunkTokens ? g.n : kChunkTokens, rows_of = (int)(chunk.head & 0xffff);
     Work w;
     w.c = __builtin_amdgcn_readfirstlane(todo[1]);
-    w.e = __builtin_amdgcn_readfirstlane((int)(chunk.head >> 32));
-    w.row0 = __builtin_amdgcn_readfirstlane((int)(chunk.head >> 16 & 0xffff));
-    w.rows = __builtin_amdgcn_readfirstlane((int)(chunk.head & 0xffff));
+    w.e = in_range(__builtin_amdgcn_readfirstlane((int)(chunk.head >> 32)), g.Eg);
+    w.rows = __builtin_amdgcn_readfirstlane(rows_of < most ? rows_of : most);
+    w.row0 = in_range(__builtin_amdgcn_readfirstlane((int)(chunk.head >> 16 & 0xffff)), g.n - w.rows + 1);
     w.tok = tok;
+    if (threadIdx.x < 64) {
+        const int row = __popcll(mask & ((1ull << threadIdx.x) - 1));
+        if ((mask >> threadIdx.x & 1) && row < kChunkTokens) tok[row] = in_range(threadIdx.x, g.T);
+        if ((int)threadIdx.x >= __popcll(mask) && threadIdx.x < kChunkTokens) tok[threadIdx.x] = 0;
+    }
+    __syncthreads();
     if (split_slabs(g, __builtin_amdgcn_readfirstlane(chunk.ticket), w)) {
         if (w.rows > 4)
             gate_up_slabs<kSym, 2, false>(g, w, lds);

@@ -374,7 +374,8 @@ int strata_moe_adapt_workspace_bytes(int64_t T, const strata_moe_adapters* adapt
  *       its adapter, any order is right
  *   y   [T] rows of out_dim fp32, y_stride apart: the shared projection's output
  *   out [T] rows of out_dim fp32, out_stride apart; may be y itself (the same
- *       pointer and stride), and must not overlap x or y otherwise
+ *       pointer and stride), and must not overlap x or y otherwise (columns of
+ *       one array, with its stride for both, do not overlap)
  * Strides are at least the row's width (y and out are only read or written
  * within it); all rows are 4-byte aligned.  The shared projection may be any:
  * the layer itself (after strata_moe_prefill, y = its output), the router, or

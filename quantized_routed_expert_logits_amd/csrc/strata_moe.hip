@@ -697,12 +697,22 @@ int check_workspace(const void* ws, size_t have, size_t need) {
     return 0;
 }
 
-// Bytes from the first to past the last element of T rows `stride` apart.
-uintptr_t row_span(int64_t T, int64_t stride, int64_t width) { return (uintptr_t)(((T - 1) * stride + width) * 4); }
+// T rows of `width` fp32, `stride` apart.
+struct RowSet {
+    uintptr_t base;
+    int64_t T, stride, width;
+    uintptr_t bytes() const { return (uintptr_t)(((T - 1) * stride + width) * 4); }  // first element to past the last
+};
 
-bool overlap(const void* a, uintptr_t an, const void* b, uintptr_t bn) {
-    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
-    return pa < pb + bn && pb < pa + an;
+bool overlap(uintptr_t a, uintptr_t an, uintptr_t b, uintptr_t bn) { return a < b + bn && b < a + an; }
+
+// Rows of one stride may lie beside each other, as columns of one array do.
+bool overlap(const RowSet& a, const RowSet& b) {
+    if (!overlap(a.base, a.bytes(), b.base, b.bytes())) return false;
+    if (a.stride != b.stride) return true;
+    const uintptr_t pitch = (uintptr_t)a.stride * 4;
+    const uintptr_t from = b.base >= a.base ? (b.base - a.base) % pitch : pitch - 1 - (a.base - b.base - 1) % pitch;
+    return from < (uintptr_t)a.width * 4 || from + (uintptr_t)b.width * 4 > pitch;
 }
 
 AdaptLaunch adapt_launch(const strata_moe_adapters* ad, const int32_t* ids, int64_t T, char* ws) {
@@ -1243,12 +1253,15 @@ int strata_moe_adapt(const float* x, int64_t x_stride, const int32_t* ids, const
     if (!aligned(x, 4) || !aligned(ids, 4) || !aligned(y, 4) || !aligned(out, 4))
         return fail(STRATA_MOE_EINVAL, "x, ids, y and out must be 4-byte aligned");
     TRY(check_adapter_pointers(adapters));
-    const uintptr_t nx = row_span(T, x_stride, adapters->in_dim), ny = row_span(T, y_stride, adapters->out_dim),
-                    no = row_span(T, out_stride, adapters->out_dim);
-    if (overlap(out, no, x, nx)) return fail(STRATA_MOE_EINVAL, "out overlaps x");
-    if (!(out == y && out_stride == y_stride) && overlap(out, no, y, ny))
+    const RowSet rx{(uintptr_t)x, T, x_stride, adapters->in_dim}, ry{(uintptr_t)y, T, y_stride, adapters->out_dim},
+        ro{(uintptr_t)out, T, out_stride, adapters->out_dim};
+    if (overlap(ro, rx)) return fail(STRATA_MOE_EINVAL, "out overlaps x");
+    if (!(out == y && out_stride == y_stride) && overlap(ro, ry))
         return fail(STRATA_MOE_EINVAL, "out overlaps y without being y");
     TRY(check_workspace(workspace, workspace_bytes, need));
+    for (const RowSet& rows : {rx, ry, ro})
+        if (overlap((uintptr_t)workspace, need, rows.base, rows.bytes()))
+            return fail(STRATA_MOE_EINVAL, "the workspace overlaps x, y or out");
     TRY(check_device());
     AdaptLaunch l = adapt_launch(adapters, ids, T, (char*)workspace);
     l.x = x;
@@ -1289,6 +1302,9 @@ int strata_moe_decode(const float* x, const float* router_w, const strata_moe_ex
         return fail(STRATA_MOE_EINVAL, "adapter_ids without adapters");
     }
     TRY(check_workspace(workspace, workspace_bytes, layer + ad));
+    for (const float* rows : {x, (const float*)out})
+        if (overlap((uintptr_t)workspace, layer + ad, (uintptr_t)rows, (uintptr_t)(T * experts->hidden * 4)))
+            return fail(STRATA_MOE_EINVAL, "the workspace overlaps x or out");
     TRY(check_device());
     DecodeLaunch l{};
     l.x = x;

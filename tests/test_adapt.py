@@ -234,6 +234,38 @@ def test_beside_the_router_on_two_streams(qm):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 70])
+def test_columns_of_one_array(qm, T):
+    """x, y and out as neighbouring columns of one buffer; what is beside them
+    stays as it was."""
+    x, ids, a, b, scale, y = _case(T, 64, 48, 16, 4, torch.float32, seed=6)
+    ad = qm.Adapters(a, b, scale)
+    ref = qm.strata_moe_adapt(x, ids, ad, y, torch.empty_like(y))
+    buf = torch.full((T, 48 + 64 + 48 + 5), 7.0, device="cuda")
+    out, xc, yc = buf[:, :48], buf[:, 48:112], buf[:, 112:160]
+    xc.copy_(x)
+    yc.copy_(y)
+    qm.strata_moe_adapt(xc, ids, ad, yc, out)
+    assert torch.equal(out, ref) and torch.equal(xc, x) and torch.equal(yc, y) and torch.all(buf[:, 160:] == 7.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 70])
+def test_columns_of_one_array(qm, T):
+    """x, y and out as neighbouring columns of one buffer; what is beside them
+    stays as it was."""
+    x, ids, a, b, scale, y = _case(T, 64, 48, 16, 4, torch.float32, seed=6)
+    ad = qm.Adapters(a, b, scale)
+    ref = qm.strata_moe_adapt(x, ids, ad, y, torch.empty_like(y))
+    buf = torch.full((T, 48 + 64 + 48 + 5), 7.0, device="cuda")
+    out, xc, yc = buf[:, :48], buf[:, 48:112], buf[:, 112:160]
+    xc.copy_(x)
+    yc.copy_(y)
+    qm.strata_moe_adapt(xc, ids, ad, yc, out)
+    assert torch.equal(out, ref) and torch.equal(xc, x) and torch.equal(yc, y) and torch.all(buf[:, 160:] == 7.0)
+
+
+@pytest.mark.gpu
 def test_workspace_contents_and_size(qm):
     x, ids, a, b, scale, y = _case(77, 320, 192, 16, 5, torch.float16, seed=4)
     ad = qm.Adapters(a, b, scale)
@@ -308,3 +340,49 @@ def test_binding_refusals(qm):
             qm.strata_moe_adapt(xx, ii, ad, yy, oo)
     with pytest.raises(TypeError):
         qm.strata_moe_adapt(x, ids.long(), ad, y, y)
+
+
+def test_overlaps(qm):
+    """Rows of one stride beside each other do not overlap (such a call gets as
+    far as the workspace's size), whatever comes first; rows that share an
+    element do."""
+    ad = _ad(qm, n_in=24, n_out=16)
+    base, s = 1 << 24, 100
+
+    def code(xc, yc, oc, strides=(s, s, s), T=4, ws=1 << 28, n=1):
+        return _call(qm, ad, T=T, x=base + 4 * xc, xs=strides[0], y=base + 4 * yc, ys=strides[1], out=base + 4 * oc,
+                     os_=strides[2], ws=ws, n=n)
+
+    for xc, yc, oc in ((0, 24, 40), (16, 40, 0), (40, 0, 24), (24, 84, 300), (0, 24, 24), (60, 44, 84), (60, 44, 184),
+                       (76, 160, 60), (400, 84, 284)):
+        assert code(xc, yc, oc) == qm.ENOMEM, (xc, yc, oc)
+    for xc, yc, oc in ((0, 24, 23), (0, 24, 39), (0, 24, 9), (16, 40, 1), (16, 40, 99), (0, 300, 285), (0, 40, 123),
+                       (285, 0, 100)):
+        assert code(xc, yc, oc) == qm.EINVAL, (xc, yc, oc)
+    assert code(0, 24, 40, (s, s, s + 1)) == qm.EINVAL  # other strides: by the whole ranges
+    assert code(0, 24, 40, (s, s, s + 1), T=1) == qm.ENOMEM
+    assert code(0, 24, 40, ws=base, n=1 << 30) == qm.EINVAL  # the workspace on the rows
+    assert code(0, 24, 40, ws=base - 256, n=1 << 30) == qm.EINVAL
+
+
+def test_overlaps(qm):
+    """Rows of one stride beside each other do not overlap (such a call gets as
+    far as the workspace's size), whatever comes first; rows that share an
+    element do."""
+    ad = _ad(qm, n_in=24, n_out=16)
+    base, s = 1 << 24, 100
+
+    def code(xc, yc, oc, strides=(s, s, s), T=4, ws=1 << 28, n=1):
+        return _call(qm, ad, T=T, x=base + 4 * xc, xs=strides[0], y=base + 4 * yc, ys=strides[1], out=base + 4 * oc,
+                     os_=strides[2], ws=ws, n=n)
+
+    for xc, yc, oc in ((0, 24, 40), (16, 40, 0), (40, 0, 24), (24, 84, 300), (0, 24, 24), (60, 44, 84), (60, 44, 184),
+                       (76, 144, 60), (424, 84, 200), (16, 40, 99)):
+        assert code(xc, yc, oc) == qm.ENOMEM, (xc, yc, oc)
+    for xc, yc, oc in ((0, 24, 23), (0, 24, 39), (0, 24, 9), (16, 40, 1), (16, 40, 101), (0, 300, 285), (0, 40, 123),
+                       (285, 0, 100)):
+        assert code(xc, yc, oc) == qm.EINVAL, (xc, yc, oc)
+    assert code(0, 24, 40, (s, s, s + 1)) == qm.EINVAL  # other strides: by the whole ranges
+    assert code(0, 24, 40, (s, s, s + 1), T=1) == qm.ENOMEM
+    assert code(0, 24, 40, ws=base, n=1 << 30) == qm.EINVAL  # the workspace on the rows
+    assert code(0, 24, 40, ws=base + 256, n=1 << 30) == qm.EINVAL

@@ -299,6 +299,13 @@ def test_refusals_on_the_host(qm):
         assert _call(qm, st, ad=bad, ids=64) == qm.EINVAL
 
 
+def test_workspace_on_the_rows(qm):
+    st = _struct(qm)
+    for ws in (1 << 16, 1 << 24, (1 << 16) + 512):
+        assert _call(qm, st, ws=ws) == qm.EINVAL
+        assert "workspace overlaps" in qm.strata_moe_last_error()
+
+
 def test_workspace_size_query(qm):
     b = ctypes.c_size_t()
     lib, st = qm.library(), _struct(qm)

@@ -131,6 +131,22 @@ def test_ranks_per_adapter(qm, T, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16], ids=["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("T, rank", [(40, 16), (40, 64), (300, 64), (40, 72)])
+def test_ranks_that_end_inside_a_step(qm, T, rank, dtype):
+    """Ranks at and around the steps' ends, below rows of B that go on past
+    the last step: their rest is read, and none of it is used."""
+    use = [r for r in (1, 7, 8, 15, 16, 31, 32, 33, 47, 63, 64, 65, 72) if r <= rank]
+    x, _, a, b, scale, y = _case(T, 96, 136, rank, len(use), dtype, seed=T + rank)
+    ids = (torch.arange(T) * 5 % len(use)).to(torch.int32).cuda()
+    for n, r in enumerate(use):
+        a[n, r:], b[n, :, r:] = float("inf"), float("nan")
+    ranks = torch.tensor(use, dtype=torch.int32).cuda()
+    out = qm.strata_moe_adapt(x, ids, qm.Adapters(a, b, scale, ranks), y, torch.empty_like(y))
+    _check(out, _reference(x, ids, a, b, scale, ranks, y))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 31, 200])
 def test_ids_outside_the_adapters_and_no_scale(qm, T):
     x, _, a, b, _, y = _case(T, 128, 72, 8, 3, torch.bfloat16, seed=1)

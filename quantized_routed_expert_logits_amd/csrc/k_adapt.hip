@@ -30,9 +30,19 @@
 //
 // Loads and stores go row by row, 4 or 16 neighbouring lanes to a row, and
 // cross to the products' layout (neighbouring lanes in different rows)
-// through LDS that belongs to the wave alone.  Loaded in the products' layout,
-// every lane's 16 bytes were an access of their own: 50 us against 23 for the
-// shrink of 8192 tokens at rank 64 with a quarter of the loads.
+// through LDS that belongs to the wave alone: in the products' layout every
+// lane's 16 bytes are an access of their own.  (8192 tokens, rank 64, bf16
+// weights on the fp32 unit: crossing took the shrink from 50 to 46 us; with
+// the bf16 unit and the tiles dealt to the XCDs it was 37.)
+//
+// What bounds them.  Many tokens: memory, x once for the shrink, y and out
+// once for the expand.  8192 tokens of 2560, 16 adapters of rank 64, bf16: the
+// shrink 35 us (90 MB, 2.6 TB/s), the expand 49 to 58 us (175 MB, 3.0 to 3.6
+// TB/s), against 5.1 TB/s of a large copy.  Few tokens: latency, a chain of
+// ids, ranks, weights, the sums' way through the workspace, and the same
+// again: 3.8 + 5.0 us for one token at rank 16, 8.6 + 9.7 us for 32 tokens
+// with an adapter each (fp16, ranks 1 to 64), of which the products, 15 of
+// their 16 columns unused, take 1.6 and 1.2.
 #include "internal.h"
 
 namespace strata_moe {
@@ -321,7 +331,8 @@ __device__ __forceinline__ void shrink_steps(const AdaptArgs& g, const W* const 
 }
 
 // One workgroup: a tile, up to 64 ranks of its groups, one part of the
-// reduction over in, which its waves split again.
+// reduction over in, which its waves split again: a wave's run is then a few
+// steps of 128 bytes per row, and 8 waves hide each other's loads.
 template <typename W>
 __global__ void __launch_bounds__(64 * kShrinkWaves, 4) adapt_shrink_kernel(AdaptArgs g) {
     // the waves' panels, then their sums
@@ -382,7 +393,8 @@ __global__ void __launch_bounds__(64 * kShrinkWaves, 4) adapt_shrink_kernel(Adap
     });
 }
 
-// One workgroup: a tile's groups, `turns` runs of 64 outputs per wave.  P
+// One workgroup: a tile's groups, `turns` runs of 64 outputs per wave (256
+// bytes of each of 16 rows of y and out at a time).  P
 // consecutive ranks per lane: 4 for ranks up to 16, else 8.  kStream: y is
 // large, and is read past the caches.
 template <typename W, int P, bool kStream>

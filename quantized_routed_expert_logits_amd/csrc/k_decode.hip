@@ -13,8 +13,17 @@
 // The block sums are exact integers; a block sum times the fp16 d is exact in
 // 32 bits (13 + 11 bits), and the sums over blocks are held in 64 bits: one
 // 64-bit FMA per output and block runs at the rate of a 32-bit one here, and
-// it makes the H codes those of the definition (a 32-bit G moves about one
-// code in 10^5 over a rounding border).
+// it makes the H codes those of the definition (a 32-bit sum can move a code
+// over a rounding border, and the output by 1e-4 of its largest value).
+//
+// Two launches.  What bounds them, at H = 2560, I = 1024, E = 512, K = 10: one
+// token is a chain of latencies, 4.9 + 25.9 us (router, experts) for 30 MB of
+// weights, of which the top-K takes about 4.5, the gate/up products 3.6, what
+// follows them 3, the hand-off to down 1 and down with the combine 6, the
+// launch the rest.  32 tokens are bound by memory: 7.6 + 132 to 144 us for 595
+// MB, 4.1 to 4.5 TB/s (a large copy reaches 5.1).  64 tokens on few hot
+// experts (131 MB, 10.3 + 92 us) are bound by the vector unit: a block's 16
+// outputs a lane take two conversions, a product with d and a 64-bit FMA each.
 #include "internal.h"
 
 namespace strata_moe {
@@ -117,7 +126,8 @@ __device__ __forceinline__ float round_half_away(float t) {
 // which the waves split.  A lane takes 4 consecutive values of h of one token,
 // one per product, and the same 4 rows of the weights.  (On the vector unit
 // with the tokens' values broadcast from LDS, 64 tokens took 18 us: every
-// broadcast read holds the LDS for as long as a full one.)
+// broadcast read holds the LDS for as long as a full one; this form takes 10.3,
+// one token 4.9, of which the weights' 5.2 MB are one at 5.1 TB/s.)
 typedef double v4d __attribute__((ext_vector_type(4)));
 
 template <int NT>
@@ -421,9 +431,13 @@ __device__ void group_pairs(const DecodeArgs& g, GroupLds& l) {
 // one 32-wide block, exact in int32, with the map's offset -z sum a as the
 // product's initial value.
 // The activations are the product's rows and the weights its columns: a lane
-// gets, for its own weight row, the four activation rows 4 (lane / 16) + i.
-// Row j of the chunk sits in product row 4 (j % 4) + j / 4, so up to 4 NI rows
-// need only the results i < NI: lane (r, kg) has rows kg + 4 i.
+// gets, for its own weight row, the four product rows 4 kg + i, kg = lane /
+// 16.  Activation row j has two product rows, 4 (j % 4) + 2 (j / 4) for its A
+// spread and the next one for B, so one product serves both fragments, lane
+// (r, kg) has rows kg and kg + 4 (NI = 2), and up to 4 rows need only the
+// first two results (NI = 1).  Of a single row (kOne) every kg has the same
+// sums: each takes the two fragments 2 kg and 2 kg + 1, a quarter of the
+// scaling.
 typedef int v4i __attribute__((ext_vector_type(4)));
 
 template <bool kSym>
@@ -448,7 +462,7 @@ typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
 struct Weights {
-    v4u c, d;    // a lane's 16 code bytes, its weight row's 8 fp16 scales
+    v4u c, d;    // a lane's 16 code bytes, its weight row's 8 fp16 scales (kOne: the two of its fragments)
 };
 template <int NI>
 struct Acts {
@@ -467,45 +481,56 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int b
                                              __builtin_amdgcn_readfirstlane(bytes), kBufferWord3);
 }
 
-// One block's products and scaling.
-template <bool kSym, int NI>
-__device__ __forceinline__ void block_sums(const Weights& r, const Acts<NI>& x, double (&acc)[8][NI]) {
+// Sums of a lane: fragments (of 8, or the lane's two) times rows.
+template <int NI, bool kOne>
+using Sums = double[kOne ? 2 : 8][NI];
+
+// One block's products and scaling.  spread: the byte selectors of the lane's
+// product row.
+template <bool kSym, int NI, bool kOne>
+__device__ __forceinline__ void block_sums(const Weights& r, const Acts<NI>& x, v2u spread, Sums<NI, kOne>& acc) {
     constexpr int zp = kSym ? -3 : -1;
     double sc[NI];
     v4i z{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         sc[i] = (double)__builtin_bit_cast(float, x.s[i][0]);
-        z[i] = __mul24((int)x.s[i][1], zp);  // |sum| <= 32 * 127: a full-rate 24-bit multiply
+        z[2 * i] = z[2 * i + 1] = __mul24((int)x.s[i][1], zp);  // |sum| <= 32 * 127: a full-rate 24-bit multiply
     }
-    const v4i aA{(int)__builtin_amdgcn_perm(0u, x.q[0], 0x0c010c00u), (int)__builtin_amdgcn_perm(0u, x.q[0], 0x0c030c02u),
-                 (int)__builtin_amdgcn_perm(0u, x.q[1], 0x0c010c00u), (int)__builtin_amdgcn_perm(0u, x.q[1], 0x0c030c02u)};
-    const v4i aB{(int)((uint32_t)aA[0] << 8), (int)((uint32_t)aA[1] << 8), (int)((uint32_t)aA[2] << 8),
-                 (int)((uint32_t)aA[3] << 8)};
-    // the products of dword p + 1 run beside the scaling of dword p
-    v4i cw = code_bytes<kSym>(r.c[0]);
-    v4i pa = __builtin_amdgcn_mfma_i32_16x16x64_i8(aA, cw, z, 0, 0, 0);
-    v4i pb = __builtin_amdgcn_mfma_i32_16x16x64_i8(aB, cw, z, 0, 0, 0);
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        v4i na, nb;
-        if (p < 3) {
-            cw = code_bytes<kSym>(r.c[p + 1]);
-            na = __builtin_amdgcn_mfma_i32_16x16x64_i8(aA, cw, z, 0, 0, 0);
-            nb = __builtin_amdgcn_mfma_i32_16x16x64_i8(aB, cw, z, 0, 0, 0);
-        }
-        const float da = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.d[p] & 0xffffu));
-        const float db = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.d[p] >> 16));
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            acc[2 * p][i] = fma((double)((float)pa[i] * da), sc[i], acc[2 * p][i]);
-            acc[2 * p + 1][i] = fma((double)((float)pb[i] * db), sc[i], acc[2 * p + 1][i]);
-        }
-        // the results that no row uses stay allocated until here: a register
-        // that a running product still writes cannot be taken without a stall
-        asm volatile("" ::"v"(pa), "v"(pb));
-        if (p < 3) pa = na, pb = nb;
+    const v4i a{(int)__builtin_amdgcn_perm(0u, x.q[0], spread[0]), (int)__builtin_amdgcn_perm(0u, x.q[0], spread[1]),
+                (int)__builtin_amdgcn_perm(0u, x.q[1], spread[0]), (int)__builtin_amdgcn_perm(0u, x.q[1], spread[1])};
+    auto product = [&](int p) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, code_bytes<kSym>(r.c[p]), z, 0, 0, 0); };
+    auto scale = [&](int pa, int pb, uint32_t d, int f, int i) {
+        const float da = (float)__builtin_bit_cast(_Float16, (uint16_t)(d & 0xffffu));
+        const float db = (float)__builtin_bit_cast(_Float16, (uint16_t)(d >> 16));
+        acc[f][i] = fma((double)((float)pa * da), sc[i], acc[f][i]);
+        acc[f + 1][i] = fma((double)((float)pb * db), sc[i], acc[f + 1][i]);
+    };
+    // the results that no row uses stay allocated until the product is done: a
+    // register that a running product still writes cannot be taken without a stall
+    auto hold = [](const v4i& v) { asm volatile("" ::"v"(v)); };
+    if constexpr (kOne) {
+        const v4i c0 = product(0), c1 = product(1), c2 = product(2), c3 = product(3);
+        const int kg = threadIdx.x >> 4 & 3;
+        const bool odd = kg & 1, high = kg & 2;
+        hold(c0), hold(c1), hold(c2), hold(c3);
+        const int a0 = odd ? c1[0] : c0[0], b0 = odd ? c1[1] : c0[1];
+        const int a1 = odd ? c3[0] : c2[0], b1 = odd ? c3[1] : c2[1];
+        scale(high ? a1 : a0, high ? b1 : b0, r.d[0], 0, 0);
         __builtin_amdgcn_sched_barrier(0);
+    } else {
+        // product p + 1 runs beside the scaling of product p
+        v4i cur = product(0);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            v4i next;
+            if (p < 3) next = product(p + 1);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) scale(cur[2 * i], cur[2 * i + 1], r.d[p], 2 * p, i);
+            hold(cur);
+            if (p < 3) cur = next;
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 }
 
@@ -549,14 +574,15 @@ __device__ __forceinline__ void stage_acts(const ActRows& a, int Kd, int rows, R
 // Otherwise the workgroup stages them in LDS: their loads, 16 bytes a lane or
 // less of every 1280-byte block, took as long in the address path as those of
 // the weights (32 tokens 151 us, 136 with the activations left out).
-template <bool kSym, int NI, bool kAgent, bool kDirect, typename Row, typename Ready>
+template <bool kSym, int NI, bool kOne, bool kAgent, bool kDirect, typename Row, typename Ready>
 __device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, const ActRows& a, int Kd, Row row, char* lds,
-                                          double (&acc)[8][NI], Ready ready) {
+                                          Sums<NI, kOne>& acc, Ready ready) {
     constexpr int kDepth = 4;  // blocks in flight (6 took 172 us for 32 tokens: the registers)
     constexpr int aux = kAgent ? kAgentLoad : 0;
     const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
     const int nblk = Kd / kBlock;
-    const int mine = (r16 >> 2) + 4 * (r16 & 3);  // the row in product row r16
+    const int mine = (r16 >> 2) + 4 * (r16 >> 1 & 1);  // the row in product row r16
+    const v2u spread = r16 & 1 ? v2u{0x010c000cu, 0x030c020cu} : v2u{0x0c010c00u, 0x0c030c02u};
     const int last = w.nb > 0 ? w.nb - 1 : 0;     // past the run: its last block again, never used
     const __amdgpu_buffer_rsrc_t rr = buffer_of(rec, (last + 1) * kRecordBytes);
     const __amdgpu_buffer_rsrc_t rq = buffer_of(a.q, a.rows_bound * Kd), rs = buffer_of(a.s, a.rows_bound * nblk * 8);
@@ -575,7 +601,10 @@ __device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, con
     auto load_w = [&](int b, Weights& r) {
         const int at = (b < last ? b : last) * kRecordBytes;
         r.c = __builtin_amdgcn_raw_buffer_load_b128(rr, lane * 16, at, 0);
-        r.d = __builtin_amdgcn_raw_buffer_load_b128(rr, kRecordCodeBytes + r16 * 16, at, 0);
+        if constexpr (kOne)
+            r.d[0] = __builtin_amdgcn_raw_buffer_load_b32(rr, kRecordCodeBytes + r16 * 16 + 4 * kg, at, 0);
+        else
+            r.d = __builtin_amdgcn_raw_buffer_load_b128(rr, kRecordCodeBytes + r16 * 16, at, 0);
     };
     auto load_a = [&](int b, Acts<NI>& x) {
         b = b < last ? b : last;
@@ -606,7 +635,7 @@ __device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, con
         __syncthreads();
     }
 #pragma unroll
-    for (int f = 0; f < 8; ++f)
+    for (int f = 0; f < (kOne ? 2 : 8); ++f)
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[f][i] = 0.0;
     // whole turns of the ring have no branches inside (each block's wait
@@ -617,7 +646,7 @@ __device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, con
         for (int j = 0; j < kDepth; ++j) {
             Acts<NI>& x = act[kDirect ? j : 0];
             if constexpr (!kDirect) lds_a(b + j, x);
-            block_sums<kSym, NI>(ring[j], x, acc);
+            block_sums<kSym, NI, kOne>(ring[j], x, spread, acc);
             load_w(b + j + kDepth, ring[j]);
             if constexpr (kDirect) load_a(b + j + kDepth, x);
             __builtin_amdgcn_sched_barrier(0);
@@ -628,21 +657,26 @@ __device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, con
         if (b + j < w.nb) {
             Acts<NI>& x = act[kDirect ? j : 0];
             if constexpr (!kDirect) lds_a(b + j, x);
-            block_sums<kSym, NI>(ring[j], x, acc);
+            block_sums<kSym, NI, kOne>(ring[j], x, spread, acc);
         }
     if constexpr (!kDirect) __syncthreads();  // the activations are read: their LDS takes the sums
 }
 
 // Every wave's sums to LDS: [wave][4 NI][128], row j of the chunk, fragment
 // order f * 16 + r.  The waves of a slab are next to each other.
-template <int NI>
-__device__ __forceinline__ void share_sums(const Work& w, const double (&acc)[8][NI], double* lds) {
+template <int NI, bool kOne>
+__device__ __forceinline__ void share_sums(const Work& w, const Sums<NI, kOne>& acc, double* lds) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, kg = lane >> 4;
+    if constexpr (kOne) {
+        lds[wave * 4 * NI * 128 + 2 * kg * 16 + r16] = acc[0][0];
+        lds[wave * 4 * NI * 128 + (2 * kg + 1) * 16 + r16] = acc[1][0];
+    } else {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-        if (kg + 4 * i < w.rows)
+        for (int i = 0; i < NI; ++i)
+            if (kg + 4 * i < w.rows)
 #pragma unroll
-            for (int f = 0; f < 8; ++f) lds[(wave * 4 * NI + kg + 4 * i) * 128 + f * 16 + r16] = acc[f][i];
+                for (int f = 0; f < 8; ++f) lds[(wave * 4 * NI + kg + 4 * i) * 128 + f * 16 + r16] = acc[f][i];
+    }
     __syncthreads();
 }
 
@@ -658,14 +692,14 @@ __device__ __forceinline__ double slab_sum(int split, const double* lds, int s, 
 // Gate/up of the workgroup's slabs: h = silu(G) U, rounded to int8.  Slab
 // columns 0..63 are gate rows, 64..127 the up rows of the same H values; half
 // a wave takes a block of 32.
-template <bool kSym, int NI, bool kDirect>
+template <bool kSym, int NI, bool kOne, bool kDirect>
 __device__ void gate_up_slabs(const DecodeArgs& g, const Work& w, double* lds) {
     const uint8_t* rec = g.gate_up + (int64_t)w.e * g.gate_up_stride +
                          ((int64_t)w.slab * (g.H / kBlock) + w.b0) * kRecordBytes;
-    double acc[8][NI];
-    slab_sums<kSym, NI, false, kDirect>(
+    Sums<NI, kOne> acc;
+    slab_sums<kSym, NI, kOne, false, kDirect>(
         w, rec, ActRows{g.qx, g.sx, g.T}, g.H, [&](int j) { return w.tok[j]; }, (char*)lds, acc, [] {});
-    share_sums<NI>(w, acc, lds);
+    share_sums<NI, kOne>(w, acc, lds);
     const int l = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < 2 * w.nslab * w.rows; i += kThreads / 32) {
         const int hb = i & 1, s = (i >> 1) % w.nslab, j = (i >> 1) / w.nslab;
@@ -702,12 +736,12 @@ struct Rows {
     int last[kChunkTokens * kWavesD];  // [slab][row]
 };
 
-template <bool kSym, int NI, bool kDirect>
+template <bool kSym, int NI, bool kOne, bool kDirect>
 __device__ void down_slabs(const DecodeArgs& g, const Work& w, double* lds, Rows& rows, bool known) {
     const int nslab = g.H / kSlabRows;
     const uint8_t* rec = g.down + (int64_t)w.e * g.down_stride +
                          ((int64_t)w.slab * (g.I / kBlock) + w.b0) * kRecordBytes;
-    double acc[8][NI];
+    Sums<NI, kOne> acc;
     auto ready = [&] {
         // the rows' pairs and weights, then the chunk's H rows
         if (!known && (int)threadIdx.x < w.rows) {
@@ -719,9 +753,9 @@ __device__ void down_slabs(const DecodeArgs& g, const Work& w, double* lds, Rows
             for (int n = 0; n < kMaxPolls && peek(&g.chunks[w.c].gu_done) < g.gw; ++n) __builtin_amdgcn_s_sleep(2);
         __syncthreads();
     };
-    slab_sums<kSym, NI, true, kDirect>(
+    slab_sums<kSym, NI, kOne, true, kDirect>(
         w, rec, ActRows{g.qh, g.sh, g.n}, g.I, [&](int j) { return w.row0 + j; }, (char*)lds, acc, ready);
-    share_sums<NI>(w, acc, lds);
+    share_sums<NI, kOne>(w, acc, lds);
     for (int i = threadIdx.x; i < w.nslab * w.rows * 128; i += kThreads) {
         const int at = i & 127, s = (i >> 7) % w.nslab, j = (i >> 7) / w.nslab;
         poke(&g.dm[(int64_t)rows.pair[j] * g.H + 128 * (w.slab0 + s) + at],
@@ -817,9 +851,9 @@ __global__ void __launch_bounds__(kThreads, 4) decode_pairs_kernel(DecodeArgs g)
     }
     __syncthreads();
     if (split_slabs(g, __builtin_amdgcn_readfirstlane(taken), w))
-        gate_up_slabs<kSym, 1, true>(g, w, lds);
+        gate_up_slabs<kSym, 1, true, true>(g, w, lds);
     else
-        down_slabs<kSym, 1, true>(g, w, lds, rows, true);
+        down_slabs<kSym, 1, true, true>(g, w, lds, rows, true);
 }
 
 // More tokens: the top-K of the tokens and the grouping by whichever
@@ -894,14 +928,18 @@ __global__ void __launch_bounds__(kThreads, 4) decode_chunks_kernel(DecodeArgs g
     __syncthreads();
     if (split_slabs(g, __builtin_amdgcn_readfirstlane(chunk.ticket), w)) {
         if (w.rows > 4)
-            gate_up_slabs<kSym, 2, false>(g, w, lds);
+            gate_up_slabs<kSym, 2, false, false>(g, w, lds);
+        else if (w.rows > 1)
+            gate_up_slabs<kSym, 1, false, false>(g, w, lds);
         else
-            gate_up_slabs<kSym, 1, false>(g, w, lds);
+            gate_up_slabs<kSym, 1, true, false>(g, w, lds);
     } else {
         if (w.rows > 4)
-            down_slabs<kSym, 2, false>(g, w, lds, rows, false);
+            down_slabs<kSym, 2, false, false>(g, w, lds, rows, false);
+        else if (w.rows > 1)
+            down_slabs<kSym, 1, false, false>(g, w, lds, rows, false);
         else
-            down_slabs<kSym, 1, false>(g, w, lds, rows, false);
+            down_slabs<kSym, 1, true, false>(g, w, lds, rows, false);
     }
 }
 

@@ -34,7 +34,14 @@ constexpr int kRouterSlices = 8;   // ranges of the router's reduction
 constexpr int kThreads = 512;      // 8 waves
 constexpr int kWavesD = kThreads / 64;
 constexpr int kChunkTokens = 8;    // rows of a chunk at most
-constexpr int kPairTokens = 4;     // calls of at most this many tokens keep every pair on its own
+// Calls whose pairs read at most this many bytes of weights keep every pair on
+// its own, larger ones group the pairs by expert: the grouping and its
+// hand-offs cost 7 to 12 us, and the weights of one expert are read once for
+// up to 8 rows.  Pairs against groups, in us: 4 tokens of the layer below (98
+// MB) 43.9, 43.9, 6 tokens (147 MB) 56, 50, 8 tokens (197 MB) 66, 59; H, I =
+// 1280, 512, 60 experts, 4 a token: 16 tokens (39 MB) 27, 33, 32 tokens (79
+// MB) 33, 37, 64 tokens (157 MB) 47, 44.
+constexpr int64_t kPairBytes = 80000000;
 constexpr int kResident = 512;     // workgroups of the expert kernel that run at once, about
 // Polls before a wait gives up (seconds).  A wait ends by itself unless two
 // calls at once were given one workspace.  Their results are lost then, but
@@ -577,7 +584,7 @@ __device__ __forceinline__ void stage_acts(const ActRows& a, int Kd, int rows, R
 template <bool kSym, int NI, bool kOne, bool kAgent, bool kDirect, typename Row, typename Ready>
 __device__ __forceinline__ void slab_sums(const Work& w, const uint8_t* rec, const ActRows& a, int Kd, Row row, char* lds,
                                           Sums<NI, kOne>& acc, Ready ready) {
-    constexpr int kDepth = 4;  // blocks in flight (6 took 172 us for 32 tokens: the registers)
+    constexpr int kDepth = kDirect ? 2 : 4;  // blocks in flight
     constexpr int aux = kAgent ? kAgentLoad : 0;
     const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
     const int nblk = Kd / kBlock;
@@ -823,11 +830,12 @@ __device__ __forceinline__ bool split_slabs(const DecodeArgs& g, int ticket, Wor
     return gate_up;
 }
 
-// Up to kPairTokens tokens: a chunk is one pair and every workgroup finds its
-// expert by the token's top-K itself.  The experts that two tokens share are
-// few there, and the hand-offs of the grouping cost more than the top-K.
+// A chunk is one pair, and every workgroup finds its expert by the token's
+// top-K itself.  Two blocks in flight leave room for 3 workgroups per CU (4
+// tokens: 42.7 us, with four blocks and 2 workgroups 48.5; one token 27.4,
+// 28.1).
 template <bool kSym>
-__global__ void __launch_bounds__(kThreads, 4) decode_pairs_kernel(DecodeArgs g) {
+__global__ void __launch_bounds__(kThreads, 6) decode_pairs_kernel(DecodeArgs g) {
     extern __shared__ double lds[];
     __shared__ int taken;
     __shared__ int tok[kChunkTokens];
@@ -945,9 +953,12 @@ __global__ void __launch_bounds__(kThreads, 4) decode_chunks_kernel(DecodeArgs g
 
 // Most chunks of n pairs: one for every expert hit, and one more for every 8
 // rows of an expert.
-int64_t chunk_cap(int64_t n, int64_t Eg, int32_t T) {
-    return T <= kPairTokens || n < Eg + n / kChunkTokens ? n : Eg + n / kChunkTokens;
+int64_t chunk_cap(int64_t n, int64_t Eg, bool pairs) {
+    return pairs || n < Eg + n / kChunkTokens ? n : Eg + n / kChunkTokens;
 }
+
+// The form of a call of n pairs: every pair on its own, or grouped.
+bool keep_pairs(int64_t n, int32_t H, int32_t I) { return n * 3 * H * I / 16 * 5 <= kPairBytes; }
 
 // The workspace of one call.
 struct Plan {
@@ -955,7 +966,7 @@ struct Plan {
 };
 
 Plan plan(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I, bool shared) {
-    const int64_t Eg = E + shared, n = (int64_t)T * (K + shared), cap = chunk_cap(n, Eg, T);
+    const int64_t Eg = E + shared, n = (int64_t)T * (K + shared), cap = chunk_cap(n, Eg, keep_pairs(n, H, I));
     size_t off = 0;
     auto take = [&](int64_t bytes) {
         const size_t at = off;
@@ -1007,7 +1018,8 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     g.out = l.out;
     const Plan o = plan(l.T, l.H, l.E, l.K, l.I, g.shared);
     char* ws = l.workspace;
-    g.cap = (int32_t)chunk_cap(g.n, g.Eg, g.T);
+    const bool pairs = keep_pairs(g.n, g.H, g.I);
+    g.cap = (int32_t)chunk_cap(g.n, g.Eg, pairs);
     g.part = (double*)(ws + o.part);
     g.qx = (int8_t*)(ws + o.qx);
     g.sx = (int2*)(ws + o.sx);
@@ -1031,26 +1043,31 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     // The waves of a slab: all 8 while the slabs are few (the latency of one
     // counts), fewer as the workgroups fill the chip anyway; down, whose
     // reduction is the shorter one, halves first.  In us at H = 2560, I = 1024,
-    // E = 512, K = 10 (gate/up, down waves): one token 30.0 (8, 8), 29.2 (8,
-    // 4), 32.3 (4, 2); 8 tokens 73.6 (8, 4), 64.9 (4, 2), 73.7 (2, 2); 32
-    // tokens 184.8 (8, 4), 157.6 (4, 2), 150.7 (2, 2).
+    // E = 512, K = 10 (gate/up, down waves), before the later steps: one token
+    // 30.0 (8, 8), 29.2 (8, 4), 32.3 (4, 2); 8 tokens 73.6 (8, 4), 64.9 (4,
+    // 2), 73.7 (2, 2); 32 tokens 184.8 (8, 4), 157.6 (4, 2), 150.7 (2, 2).
+    // But a wave has 4 blocks at least where the reduction gives them: H = 512,
+    // I = 640, 6 experts, 33 tokens 26.5 us, without this 36; H = I = 256, 64
+    // experts, 64 tokens 29, 37.
     const int gu = g.I / 64, dn = g.H / kSlabRows;
     const int64_t slabs = (int64_t)g.cap * (gu + dn);
     g.split_gu = slabs <= 2000 ? 8 : slabs <= 4000 ? 4 : 2;
     g.split_dn = slabs <= 288 ? 8 : slabs <= 2000 ? 4 : 2;
+    while (g.split_gu > 2 && g.H / kBlock < 4 * g.split_gu) g.split_gu /= 2;
+    while (g.split_dn > 2 && g.I / kBlock < 4 * g.split_dn) g.split_dn /= 2;
     g.gw = (gu * g.split_gu + kWavesD - 1) / kWavesD;
     g.dw = (dn * g.split_dn + kWavesD - 1) / kWavesD;
     size_t lds = sizeof(TopkLds) > sizeof(GroupLds) ? sizeof(TopkLds) : sizeof(GroupLds);
-    const size_t sums = (size_t)kWavesD * (g.T <= kPairTokens ? 4 : 8) * 128 * 8;
+    const size_t sums = (size_t)kWavesD * (pairs ? 4 : 8) * 128 * 8;
     if (sums > lds) lds = sums;
-    if (g.T > kPairTokens)
+    if (!pairs)
         for (const int Kd : {g.H, g.I}) {
             const size_t acts = (size_t)kChunkTokens * (Kd + 32) + (size_t)kChunkTokens * (Kd / kBlock) * 8;
             if (acts > lds) lds = acts;
         }
     const dim3 grid(g.cap * (g.gw + g.dw));
     void (*kernel)(DecodeArgs);
-    if (g.T <= kPairTokens)
+    if (pairs)
         kernel = l.sym ? decode_pairs_kernel<true> : decode_pairs_kernel<false>;
     else
         kernel = l.sym ? decode_chunks_kernel<true> : decode_chunks_kernel<false>;

@@ -58,8 +58,8 @@ SIZES = [
     S.custom(T=33, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),
     S.custom(T=40, H=256, E=31, K=15, I=64, skewed=True, shared=True),    # n = 640 pairs, hot experts
     S.custom(T=5, H=1280, E=12, K=3, I=448),
-    S.custom(T=4, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),       # the last call with every pair on its own
-    S.custom(T=5, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),       # the first grouped one
+    S.custom(T=4, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),       # few pairs
+    S.custom(T=5, H=512, E=6, K=2, I=640, fmt="q2_0", shared=True),       # one token more
     S.custom(T=16, H=768, E=129, K=9, I=256, skewed=True),                # three groups of logits, one of one expert
     S.custom(T=3, H=4096, E=3, K=1, I=64),                                # the widest hidden size
     S.custom(T=9, H=4096, E=3, K=2, I=128, shared=True),
@@ -69,12 +69,85 @@ SIZES = [
 ]
 
 
+# layers whose weights are large enough for the pairs to be grouped by expert
+GROUPED = [
+    S.custom(T=5, H=4096, E=8, K=3, I=2048),                              # few rows of large experts
+    S.custom(T=64, H=1280, E=12, K=3, I=448),                             # about 16 rows an expert
+    S.custom(T=63, H=640, E=40, K=8, I=1024, skewed=True, fmt="q2_0"),
+    S.custom(T=37, H=896, E=9, K=4, I=1088, shared=True),                 # chunks of every length up to 8
+    S.custom(T=64, H=2048, E=2, K=2, I=256, fmt="q2_0", shared=True),     # every expert gets every row
+    S.custom(T=64, H=256, E=1023, K=15, I=384, shared=True),              # the most experts and pairs
+    S.custom(T=17, H=4096, E=3, K=1, I=4096),                             # the widest layer
+    # either side of the choice between the two forms
+    S.custom(T=32, H=1280, E=60, K=4, I=512),
+    S.custom(T=33, H=1280, E=60, K=4, I=512),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("s", GROUPED, ids=lambda s: s.name)
+def test_grouped_layer_against_the_oracle(qm, s):
+    x, wr, bias = S.activations(s), S.router_weight(s), S.router_bias(s)
+    ex = gpu_experts(s)
+    xg, wg = _t(x), _t(wr)
+    y = qm.strata_moe_decode(xg, wg, ex, s.K, torch.full_like(xg, float("nan")))
+    _check(s, y, _oracle(s, x, wr, bias))
+    assert torch.equal(qm.strata_moe_decode(xg, wg, ex, s.K, torch.empty_like(xg)), y)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("s", SIZES, ids=lambda s: s.name)
 def test_layer_against_the_oracle(qm, s):
     x, wr, bias = S.activations(s), S.router_weight(s), S.router_bias(s)
     y = qm.strata_moe_decode(_t(x), _t(wr), gpu_experts(s), s.K, torch.full((s.T, s.H), float("nan"), device="cuda"))
     _check(s, y, _oracle(s, x, wr, bias))
+
+
+@pytest.mark.gpu
+def test_grouped_layer_replayed_and_at_once(qm):
+    """The grouped form: equal logits (hot experts, ties), tokens that are not
+    finite beside others, any workspace contents, a graph replayed between
+    eager calls, two streams at once."""
+    s = S.custom(T=64, H=1280, E=12, K=3, I=448)
+    x, wr, ex = S.activations(s), S.router_weight(s), gpu_experts(s)
+    zero = np.zeros_like(wr)
+    y = qm.strata_moe_decode(_t(x), _t(zero), ex, s.K, torch.empty((s.T, s.H), device="cuda"))
+    ref = _oracle(s, x, zero)
+    assert np.all(ref["ids"] == [0, 1, 2])
+    _check(s, y, ref)
+    xg, wg = _t(x), _t(wr)
+    good = qm.strata_moe_decode(xg, wg, ex, s.K, torch.empty_like(xg))
+    need = qm.strata_moe_decode_workspace_bytes(s.T, s.K, ex)
+    for fill in (0x00, 0xff, 0x7f):
+        ws = torch.full((need + 1024,), fill, dtype=torch.uint8, device="cuda")
+        assert torch.equal(qm.strata_moe_decode(xg, wg, ex, s.K, torch.empty_like(xg), workspace=ws[:need]), good)
+        assert torch.all(ws[need:] == fill)
+    bad = xg.clone()
+    bad[4, 7], bad[60, 3] = float("nan"), float("inf")
+    y = qm.strata_moe_decode(bad, wg, ex, s.K, torch.empty_like(xg))
+    keep = [t for t in range(s.T) if t not in (4, 60)]
+    assert torch.equal(y[keep], good[keep])
+    # captured, replayed with other inputs between eager calls
+    xin, out = xg.clone(), torch.empty_like(xg)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qm.strata_moe_decode(xin, wg, ex, s.K, out)
+    for i in range(4):
+        xin.copy_(torch.roll(xg, i, 0))
+        want = qm.strata_moe_decode(xin, wg, ex, s.K, torch.empty_like(xg))
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.full_like(xg, float("nan")) for _ in range(8)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for st, o in zip(streams, outs):
+            qm.strata_moe_decode(xg, wg, ex, s.K, o[i], stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, good) for o2 in outs for o in o2)
 
 
 @pytest.mark.gpu

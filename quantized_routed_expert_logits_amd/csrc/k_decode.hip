@@ -17,13 +17,14 @@
 // over a rounding border, and the output by 1e-4 of its largest value).
 //
 // Two launches.  What bounds them, at H = 2560, I = 1024, E = 512, K = 10: one
-// token is a chain of latencies, 4.9 + 25.9 us (router, experts) for 30 MB of
-// weights, of which the top-K takes about 4.5, the gate/up products 3.6, what
-// follows them 3, the hand-off to down 1 and down with the combine 6, the
-// launch the rest.  32 tokens are bound by memory: 7.6 + 132 to 144 us for 595
-// MB, 4.1 to 4.5 TB/s (a large copy reaches 5.1).  64 tokens on few hot
-// experts (131 MB, 10.3 + 92 us) are bound by the vector unit: a block's 16
-// outputs a lane take two conversions, a product with d and a 64-bit FMA each.
+// token is a chain of latencies, 4.8 + 24.0 us (router, experts) for 30 MB of
+// weights: the top-K takes about 4.5 of it, the gate/up products 3, what
+// follows them 3, the hand-off to down 1, down with the combine 6, the launch
+// the rest.  32 tokens are bound by memory: 8.0 + 124 to 132 us for 595 MB,
+// 4.5 to 4.8 TB/s (a large copy reaches 5.1).  64 tokens on few hot experts
+// (131 MB, 10.2 + 87 us) are bound by the vector unit, 58% busy, and by how
+// evenly 144 chunks fill the chip: a block's 16 outputs a lane take two
+// conversions, a product with d and a 64-bit FMA each.
 #include "internal.h"
 
 namespace strata_moe {
@@ -134,7 +135,7 @@ __device__ __forceinline__ float round_half_away(float t) {
 // one per product, and the same 4 rows of the weights.  (On the vector unit
 // with the tokens' values broadcast from LDS, 64 tokens took 18 us: every
 // broadcast read holds the LDS for as long as a full one; this form takes 10.3,
-// one token 4.9, of which the weights' 5.2 MB are one at 5.1 TB/s.)
+// one token 4.8, of which the weights' 5.2 MB are one at 5.1 TB/s.)
 typedef double v4d __attribute__((ext_vector_type(4)));
 
 template <int NT>

@@ -43,7 +43,7 @@
 // again: 3.8 + 5.0 us for one token at rank 16, 8.6 + 9.7 us for 32 tokens
 // with an adapter each (fp16, ranks 1 to 64), of which the products, 15 of
 // their 16 columns unused, take 1.6 and 1.2.
-#include "internal.h"
+#include "few_tokens.h"
 
 namespace strata_moe {
 

@@ -25,7 +25,7 @@
 // (131 MB, 10.2 + 87 us) are bound by the vector unit, 58% busy, and by how
 // evenly 144 chunks fill the chip: a block's 16 outputs a lane take two
 // conversions, a product with d and a 64-bit FMA each.
-#include "internal.h"
+#include "few_tokens.h"
 
 namespace strata_moe {
 

@@ -21,6 +21,7 @@
 #include <vector>
 
 #include "../../include/strata_moe.h"
+#include "few_tokens.h"
 #include "internal.h"
 
 using namespace strata_moe;

@@ -43,7 +43,7 @@ constexpr int kChunkTokens = 8;    // rows of a chunk at most
 // 1280, 512, 60 experts, 4 a token: 16 tokens (39 MB) 27, 33, 32 tokens (79
 // MB) 33, 37, 64 tokens (157 MB) 47, 44.
 constexpr int64_t kPairBytes = 80000000;
-constexpr int kResident = 512;     // workgroups of the expert kernel that run at once, about
+constexpr int kResident = 768;     // workgroups of an expert kernel that run at once, at most
 // Polls before a wait gives up (seconds).  A wait ends by itself unless two
 // calls at once were given one workspace.  Their results are lost then, but
 // every wait still ends, and what a workgroup reads from the workspace as an

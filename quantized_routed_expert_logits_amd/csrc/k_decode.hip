@@ -10,11 +10,15 @@
 //   h       = silu(G) U, rounded to int8 per 32 values again
 //   out[t]  = sum_k p_k sum over blocks of d s sum (c - z) q_h, k ascending
 //
-// The block sums are exact integers; a block sum times the fp16 d is exact in
-// 32 bits (13 + 11 bits), and the sums over blocks are held in 64 bits: one
-// 64-bit FMA per output and block runs at the rate of a 32-bit one here, and
-// it makes the H codes those of the definition (a 32-bit sum can move a code
-// over a rounding border, and the output by 1e-4 of its largest value).
+// The block sums P are exact integers: |P| <= 8128 for Q2_0, and twice the
+// symmetric map's reach 12192, 14 bits.  P d s is exact in 64 bits (14 + 11 +
+// 24), and the sums over blocks are held in 64, so the H codes are those of the
+// definition.  A 32-bit sum can move a code over a rounding border, and the
+// output by 1e-4 of its largest value; so can a 32-bit P d of the symmetric map
+// where blocks cancel (it rounds from 2^24 on: 12189 times 2047/1024).  Q2_0's
+// P d is exact in 32 bits and is taken there (64 tokens on hot experts 93.9 us,
+// 94.6 with d s in 64; the symmetric 32 tokens 133.8, 133.3 with the rounded
+// product).  One 64-bit FMA per output and block runs at the rate of a 32-bit one.
 //
 // Two launches.  What bounds them, at H = 2560, I = 1024, E = 512, K = 10: one
 // token is a chain of latencies, 4.8 + 24.0 us (router, experts) for 30 MB of
@@ -508,11 +512,15 @@ __device__ __forceinline__ void block_sums(const Weights& r, const Acts<NI>& x, 
     const v4i a{(int)__builtin_amdgcn_perm(0u, x.q[0], spread[0]), (int)__builtin_amdgcn_perm(0u, x.q[0], spread[1]),
                 (int)__builtin_amdgcn_perm(0u, x.q[1], spread[0]), (int)__builtin_amdgcn_perm(0u, x.q[1], spread[1])};
     auto product = [&](int p) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, code_bytes<kSym>(r.c[p]), z, 0, 0, 0); };
+    // P d s, exactly: the symmetric map's P has 14 bits, so d s is formed first,
+    // in 64; Q2_0's has 13, and P d is exact in 32
+    auto term = [&](int p, float d, double s, double to) {
+        if constexpr (kSym) return fma((double)p, (double)d * s, to);
+        return fma((double)((float)p * d), s, to);
+    };
     auto scale = [&](int pa, int pb, uint32_t d, int f, int i) {
-        const float da = (float)__builtin_bit_cast(_Float16, (uint16_t)(d & 0xffffu));
-        const float db = (float)__builtin_bit_cast(_Float16, (uint16_t)(d >> 16));
-        acc[f][i] = fma((double)((float)pa * da), sc[i], acc[f][i]);
-        acc[f + 1][i] = fma((double)((float)pb * db), sc[i], acc[f + 1][i]);
+        acc[f][i] = term(pa, (float)__builtin_bit_cast(_Float16, (uint16_t)(d & 0xffffu)), sc[i], acc[f][i]);
+        acc[f + 1][i] = term(pb, (float)__builtin_bit_cast(_Float16, (uint16_t)(d >> 16)), sc[i], acc[f + 1][i]);
     };
     // the results that no row uses stay allocated until the product is done: a
     // register that a running product still writes cannot be taken without a stall

@@ -338,6 +338,62 @@ def test_a_decode_loop_on_a_stream_of_its_own(qm):
     assert torch.equal(y, ref)
 
 
+def _cancelling_layer(H, I, where, fmt):
+    """One expert whose first two blocks nearly cancel, and the rows for it.
+    The codes add up to 4063 and 4061 (31 of 127 and a 126, 29 and three), the
+    weights' codes are 3 and 0, their scales 2047/1024 (11 bits).  In the
+    symmetric map the blocks are 12189 and -12183 (14 bits) times 2047/1024 / 2:
+    24950883 / 1024 is a tie in 24 bits and rounds by 1 / 1024, and the two
+    rounded products together miss their sum, 12282 / 1024, by 2^-12.6 of it.
+    where: the products that cancel."""
+    code = np.full(64, 127.0, np.float32)
+    code[5], code[[33, 40, 63]] = 126, 126
+    half = lambda v: np.float16(v).view(np.uint16)  # noqa: E731
+    cgu, sgu = np.zeros((2 * I, H), np.uint8), np.zeros((2 * I, H // 32), np.uint16)
+    cd, sd = np.zeros((H, I), np.uint8), np.zeros((H, I // 32), np.uint16)
+    rng = np.random.default_rng(5)
+    cgu[:, :32] = 3
+    if where == "gate_up":
+        sgu[:, :2] = half(2047 / 1024)
+        sgu[I:, 1] = 0                       # up: the first block alone
+        cd[:] = rng.integers(0, 4, cd.shape)
+        sd[:] = rng.uniform(0.005, 0.02, sd.shape).astype(np.float16).view(np.uint16)
+    else:
+        sgu[:I, 0] = half(2.0 ** -10)
+        sgu[I:I + 64, 0] = half(code / 128)  # h follows the same pattern, in 64 columns
+        cd[:, :32] = 3
+        sd[:, :2] = half(2047 / 1024)
+    x = lambda T: np.concatenate([code, np.zeros(H - 64, np.float32)]) * 2.0 ** (np.arange(T) % 5 - 2)[:, None]  # noqa: E731
+    return S.Expert(cgu, sgu, cd, sd), lambda T: x(T).astype(np.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["q2_sym", "q2_0"])
+@pytest.mark.parametrize("where", ["gate_up", "down"])
+@pytest.mark.parametrize("T, H, I", [(1, 128, 64), (5, 256, 128),         # every pair on its own
+                                     (17, 4096, 1280), (20, 4096, 1088)],  # chunks of 8, 4 and 1 rows
+                         ids=["1", "5", "17", "20"])
+def test_the_largest_block_sums(qm, T, H, I, where, fmt):
+    ex, rows = _cancelling_layer(H, I, where, fmt)
+    s = S.custom(T=T, H=H, E=1, K=1, I=I, fmt=fmt)
+    x, wr = rows(T), np.zeros((H, 1), np.float32)
+    ref = oracle.layer(x, wr, None, lambda e: ex, 1, 1, fmt=fmt)
+    if fmt == "q2_sym":  # the blocks are what the construction says
+        q, c = (ref["qx"], ex.codes_gu) if where == "gate_up" else (ref["qh"], ex.codes_d)
+        P = ((2 * c[0, :64].astype(int) - 3) * q[0, :64].astype(int)).reshape(2, 32).sum(1)
+        assert list(P) == [12189, -12183] and np.float32(P[0]) * np.float32(2047 / 1024) != P[0] * (2047 / 1024)
+    packed = qm.Experts(1, H, I, fmt=fmt)
+    packed.pack(0, ex.codes_gu[None], ex.scales_gu[None], ex.codes_d[None], ex.scales_d[None])
+    y = qm.strata_moe_decode(_t(x), _t(wr), packed, 1, torch.empty((T, H), device="cuda"))
+    # where the blocks of D cancel, both 64-bit sums (this one and the
+    # oracle's) may be off by a rounding of 2^-53 per block and part
+    codes = (ex.codes_d.astype(float) - oracle.code_zero(fmt)).reshape(H, -1, 32)
+    P = np.einsum("obi,tbi->tob", codes, ref["qh"].astype(float).reshape(T, -1, 32))
+    terms = (np.abs(P) * ex.scales_d.view(np.float16).astype(float) * ref["sh"][:, None, :].astype(float)).sum(2)
+    err = np.abs(y.cpu().numpy().astype(np.float64) - ref["y"])
+    assert np.all(err <= _bound(s, ref) + 4 * (I // 32 + 8) * 2.0 ** -53 * terms), "a block's product was rounded"
+
+
 # -------------------------------------------------------- refusals (no GPU)
 def _struct(qm, E=16, H=256, I=128, fmt=1):
     gu, dn = qm.strata_moe_packed_bytes(H, I)

@@ -362,7 +362,8 @@ typedef struct strata_moe_adapters {
 #define STRATA_MOE_ADAPTER_F16 2
 #define STRATA_MOE_ADAPTER_BF16 3
 
-/* Device workspace of a strata_moe_adapt call of T tokens.  Errors: EINVAL
+/* Device workspace of a strata_moe_adapt call of T tokens, and of any call of
+ * fewer with the same adapters (it never decreases with T).  Errors: EINVAL
  * for sizes outside the limits above or T outside [0, 2^24], EUNSUPPORTED for
  * an unknown dtype. */
 int strata_moe_adapt_workspace_bytes(int64_t T, const strata_moe_adapters* adapters, size_t* bytes);
@@ -394,7 +395,8 @@ int strata_moe_adapt(const float* x, int64_t x_stride, const int32_t* ids, const
 #define STRATA_MOE_DECODE_MAX_TOKENS 64
 
 /* Device workspace of a strata_moe_decode call of T tokens (adapters may be
- * NULL).  Errors: those of strata_moe_decode's size checks. */
+ * NULL), and of any call of fewer with the same K, experts and adapters (it
+ * never decreases with T).  Errors: those of strata_moe_decode's size checks. */
 int strata_moe_decode_workspace_bytes(int64_t T, int32_t K, const strata_moe_experts* experts,
                                       const strata_moe_adapters* adapters, size_t* bytes);
 

@@ -43,6 +43,8 @@
 // again: 3.8 + 5.0 us for one token at rank 16, 8.6 + 9.7 us for 32 tokens
 // with an adapter each (fp16, ranks 1 to 64), of which the products, 15 of
 // their 16 columns unused, take 1.6 and 1.2.
+#include <algorithm>
+
 #include "few_tokens.h"
 
 namespace strata_moe {
@@ -570,8 +572,19 @@ int32_t shrink_split(int64_t T, int32_t rank, int32_t in) {
 
 }  // namespace
 
+// The parts of v: split * T rows.  The split falls as T grows, and so may the
+// product; the size is the largest of any call of up to T tokens, so that a
+// workspace for the largest call serves the smaller ones.
 size_t adapt_workspace(int64_t T, int32_t rank, int32_t in) {
-    return (size_t)round_up(shrink_split(T, rank, in) * T * padded_rank(rank) * 4, 256);
+    const int64_t parts = (rank + 16 * kRowTiles - 1) / (16 * kRowTiles);
+    const int64_t most = (in + 64 * kShrinkWaves - 1) / (64 * kShrinkWaves);
+    int64_t rows = T;
+    for (int64_t s = 2; s <= most && s <= kMaxSplit; ++s) {
+        const int64_t groups = kFill / (s * parts);  // the most that are split into s
+        const int64_t spread = std::min({T, (int64_t)kSpreadTokens, groups}), tiled = std::min(T, groups * kTile);
+        rows = std::max(rows, s * (tiled > kSpreadTokens ? tiled : spread));
+    }
+    return (size_t)round_up(rows * padded_rank(rank) * 4, 256);
 }
 
 hipError_t launch_adapt(const AdaptLaunch& l, hipStream_t st) {

@@ -29,6 +29,8 @@
 // (131 MB, 10.2 + 87 us) are bound by the vector unit, 58% busy, and by how
 // evenly 144 chunks fill the chip: a block's 16 outputs a lane take two
 // conversions, a product with d and a 64-bit FMA each.
+#include <algorithm>
+
 #include "few_tokens.h"
 
 namespace strata_moe {
@@ -966,8 +968,8 @@ int64_t chunk_cap(int64_t n, int64_t Eg, bool pairs) {
     return pairs || n < Eg + n / kChunkTokens ? n : Eg + n / kChunkTokens;
 }
 
-// The form of a call of n pairs: every pair on its own, or grouped.
-bool keep_pairs(int64_t n, int32_t H, int32_t I) { return n * 3 * H * I / 16 * 5 <= kPairBytes; }
+// The form of a call: up to this many pairs each stays on its own, more are grouped.
+int64_t most_pairs(int32_t H, int32_t I) { return kPairBytes / ((int64_t)3 * H * I / 16 * 5); }
 
 // The workspace of one call.
 struct Plan {
@@ -975,7 +977,7 @@ struct Plan {
 };
 
 Plan plan(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I, bool shared) {
-    const int64_t Eg = E + shared, n = (int64_t)T * (K + shared), cap = chunk_cap(n, Eg, keep_pairs(n, H, I));
+    const int64_t Eg = E + shared, n = (int64_t)T * (K + shared), cap = chunk_cap(n, Eg, n <= most_pairs(H, I));
     size_t off = 0;
     auto take = [&](int64_t bytes) {
         const size_t at = off;
@@ -1002,7 +1004,12 @@ Plan plan(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I, bool shared) {
 }  // namespace
 
 size_t decode_workspace(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I, bool shared) {
-    return plan(T, H, E, K, I, shared).total;
+    // Grouped calls need room for fewer chunks than the last call of pairs; the
+    // size is the largest of any call of up to T tokens, so that a workspace for
+    // the largest call serves the smaller ones.
+    const int64_t last = most_pairs(H, I) / (K + shared);
+    const size_t own = plan(T, H, E, K, I, shared).total;
+    return last < T ? std::max(own, plan((int32_t)last, H, E, K, I, shared).total) : own;
 }
 
 hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
@@ -1027,7 +1034,7 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     g.out = l.out;
     const Plan o = plan(l.T, l.H, l.E, l.K, l.I, g.shared);
     char* ws = l.workspace;
-    const bool pairs = keep_pairs(g.n, g.H, g.I);
+    const bool pairs = g.n <= most_pairs(g.H, g.I);
     g.cap = (int32_t)chunk_cap(g.n, g.Eg, pairs);
     g.part = (double*)(ws + o.part);
     g.qx = (int8_t*)(ws + o.qx);

@@ -298,6 +298,20 @@ def test_workspace_contents_and_size(qm):
     assert e.shape == (0, 192)
 
 
+@pytest.mark.gpu
+def test_one_workspace_for_the_largest_call(qm):
+    """A workspace sized for many tokens serves calls of fewer, which split the
+    reduction further, and is not written past its end."""
+    x, ids, a, b, scale, y = _case(4097, 2560, 40, 64, 5, torch.bfloat16, seed=8, layout="runs")
+    ad = qm.Adapters(a, b, scale)
+    need = qm.strata_moe_adapt_workspace_bytes(4097, ad)
+    ws = torch.full((need + 1024,), 0x7f, dtype=torch.uint8, device="cuda")
+    for T in (4097, 4096, 2048, 257, 256, 103, 102, 1):
+        ref = qm.strata_moe_adapt(x[:T], ids[:T], ad, y[:T], torch.empty_like(y[:T]))
+        out = qm.strata_moe_adapt(x[:T], ids[:T], ad, y[:T], torch.empty_like(y[:T]), workspace=ws[:need])
+        assert torch.equal(out, ref) and torch.all(ws[need:] == 0x7f)
+
+
 # -------------------------------------------------------- refusals (no GPU)
 def _call(qm, ad, T=4, x=1 << 20, xs=256, ids=64, y=1 << 24, ys=128, out=1 << 26, os_=128, ws=1 << 28, n=1 << 40):
     p = ctypes.c_void_p
@@ -402,3 +416,16 @@ def test_overlaps(qm):
     assert code(0, 24, 40, (s, s, s + 1), T=1) == qm.ENOMEM
     assert code(0, 24, 40, ws=base, n=1 << 30) == qm.EINVAL  # the workspace on the rows
     assert code(0, 24, 40, ws=base + 256, n=1 << 30) == qm.EINVAL
+
+
+@pytest.mark.parametrize("rank, n_in", [(64, 2560), (16, 2560), (65, 2560), (256, 2560), (1, 100), (13, 1000), (64, 513),
+                                        (200, 65536), (8, 65536), (256, 9000)])
+def test_workspace_sizes_never_decrease(qm, rank, n_in):
+    """One workspace sized for the largest batch serves every smaller one."""
+    b, lib = ctypes.c_size_t(), qm.library()
+    ad = _ad(qm, rank=rank, n_in=n_in)
+    last = 0
+    for T in [*range(9000), *range(9000, 1 << 24, 99991)]:
+        assert lib.strata_moe_adapt_workspace_bytes(T, ctypes.byref(ad), ctypes.byref(b)) == 0
+        assert b.value >= last, T
+        last = b.value

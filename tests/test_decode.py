@@ -394,6 +394,21 @@ def test_the_largest_block_sums(qm, T, H, I, where, fmt):
     assert np.all(err <= _bound(s, ref) + 4 * (I // 32 + 8) * 2.0 ** -53 * terms), "a block's product was rounded"
 
 
+@pytest.mark.gpu
+def test_one_workspace_for_the_largest_call(qm):
+    """A workspace sized for a grouped call serves a smaller call, whose pairs
+    stay on their own and take more chunks."""
+    s = S.custom(T=64, H=1024, E=8, K=2, I=1024)
+    x, wr, ex = _t(S.activations(s)), _t(S.router_weight(s)), gpu_experts(s)
+    for most in (41, 64):
+        need = qm.strata_moe_decode_workspace_bytes(most, s.K, ex)
+        ws = torch.full((need + 1024,), 0x7f, dtype=torch.uint8, device="cuda")
+        for T in (most, 41, 40, 7):
+            ref = qm.strata_moe_decode(x[:T], wr, ex, s.K, torch.empty_like(x[:T]))
+            y = qm.strata_moe_decode(x[:T], wr, ex, s.K, torch.empty_like(x[:T]), workspace=ws[:need])
+            assert torch.equal(y, ref) and torch.all(ws[need:] == 0x7f)
+
+
 # -------------------------------------------------------- refusals (no GPU)
 def _struct(qm, E=16, H=256, I=128, fmt=1):
     gu, dn = qm.strata_moe_packed_bytes(H, I)
@@ -462,3 +477,20 @@ def test_binding_refusals(qm):
     with pytest.raises((TypeError, ValueError)):
         qm.strata_moe_decode(x, wr, ex, 2, out, adapters=ad)
     assert qm.DECODE_MAX_TOKENS == 64
+
+
+@pytest.mark.parametrize("H, I, E, K", [(1024, 1024, 8, 2), (1024, 1024, 8, 8), (2560, 1024, 512, 10), (2560, 640, 512, 10),
+                                        (1280, 512, 60, 4), (4096, 4096, 3, 1), (128, 64, 1024, 15), (512, 640, 6, 2)])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("rank", [0, 64])
+def test_workspace_sizes_never_decrease(qm, H, I, E, K, shared, rank):
+    """One workspace sized for the largest batch serves every smaller one."""
+    st = _struct(qm, E - shared if E == 1024 else E, H, I)
+    st.shared_gate = 1 << 12 if shared else None
+    ad = qm.AdaptersStruct(2, rank, H, H, 3, 256, 256, None, None)
+    b, last = ctypes.c_size_t(), 0
+    for T in range(65):
+        assert qm.library().strata_moe_decode_workspace_bytes(T, K, ctypes.byref(st), ctypes.byref(ad) if rank else None,
+                                                              ctypes.byref(b)) == 0
+        assert b.value >= last, T
+        last = b.value

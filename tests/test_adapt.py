@@ -429,3 +429,15 @@ def test_workspace_sizes_never_decrease(qm, rank, n_in):
         assert lib.strata_moe_adapt_workspace_bytes(T, ctypes.byref(ad), ctypes.byref(b)) == 0
         assert b.value >= last, T
         last = b.value
+
+
+def test_a_workspace_that_ends_on_the_rows(qm):
+    """Its first bytes lie before the rows, the last it needs on them."""
+    ad = _ad(qm, n_in=24, n_out=16)
+    b = ctypes.c_size_t()
+    assert qm.library().strata_moe_adapt_workspace_bytes(40, ctypes.byref(ad), ctypes.byref(b)) == 0 and b.value > 256
+    for rows in ("x", "y", "out"):
+        at = dict(x=1 << 20, y=1 << 24, out=1 << 26)
+        ws = at[rows] - 256
+        assert _call(qm, ad, T=40, xs=100, ys=100, os_=100, ws=ws, n=1 << 30, **at) == qm.EINVAL
+        assert "workspace overlaps" in qm.strata_moe_last_error()

@@ -343,9 +343,9 @@ int strata_moe_prefill_streamed(const float* x, const float* router_w, const str
  *          read into any result, so it may hold anything); NULL means rank.
  * Sizes: 1 <= n_adapter <= 65536, 1 <= rank <= 256, in_dim and out_dim in
  * [1, 65536].  a and b are aligned to their element.  Products are exact or
- * rounded to fp32, and every sum is held in fp32.  (With bf16 adapters an
- * infinite input or weight may give NaN in its row where the definition has an
- * infinity.) */
+ * rounded to fp32, and every sum is held in fp32.  Infinities and NaN give what
+ * the definition gives, in the rows of their requests only (with bf16 adapters
+ * a value below 2^-126 beside an infinite one may count as zero). */
 typedef struct strata_moe_adapters {
     int32_t n_adapter;
     int32_t rank;

@@ -18,11 +18,11 @@
 // values, exactly (its 24 bits are cut into 8 + 8 + 8 from the top), so three
 // products give what one fp32 product gives, in 3/16 of its time.  The parts
 // below the first have accumulators of their own: their additions round at
-// 2^-8 of the first's.  (Below 2^-110 the lowest part is subnormal and may
-// count as zero; an infinite input or weight may give NaN in its row where
-// the definition has an infinity.)  fp16 weights do not split as cheaply: each
-// is two bf16 values, and cutting 64 rows of them costs more vector
-// instructions than the fp32 products they replace.
+// 2^-8 of the first's.  (Subnormal parts may count as zero: the lowest part of
+// values below 2^-110, and beside an infinite factor any value below 2^-126,
+// which gives NaN there.)  fp16 weights do not split as cheaply: each is two
+// bf16 values, and cutting 64 rows of them costs more vector instructions than
+// the fp32 products they replace.
 //
 // A lane's operand is row lane % 16 and a run of consecutive values of k (8,
 // or 4 in the expand of ranks up to 16).  The fp32 unit takes the run one
@@ -44,6 +44,7 @@
 // with an adapter each (fp16, ranks 1 to 64), of which the products, 15 of
 // their 16 columns unused, take 1.6 and 1.2.
 #include <algorithm>
+#include <type_traits>
 
 #include "few_tokens.h"
 
@@ -261,6 +262,21 @@ struct Products<Bf16, P, N> {
     }
 };
 
+// The sums of a lane: the first parts' and those below them.  An infinite
+// value cut into parts leaves NaN below the first, and so does an infinite
+// weight times a value with nothing below its first part; the first sum is then
+// infinite (or NaN) already, and stays so beside any finite one.
+template <typename W>
+__device__ __forceinline__ v4f whole_sum(v4f acc, v4f lo) {
+    if constexpr (std::is_same<W, Bf16>::value) {
+        float most = __FLT_MAX__;
+        asm("" : "+s"(most));  // a scalar register's: vector registers for it spill (8192 tokens, rank 64: 92.3 us, 90.2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lo[j] = __builtin_amdgcn_fmed3f(lo[j], -most, most);
+    }
+    return acc + lo;
+}
+
 // Products of steps [s0, s1) of 32 values of k: RT tiles of 16 A rows against
 // the tile's tokens.  al[i], xl: the rows that the lane loads, a[i], x: those
 // of its operands (rows and tokens outside the group repeat one of it: the
@@ -382,7 +398,7 @@ __global__ void __launch_bounds__(64 * kShrinkWaves, 4) adapt_shrink_kernel(Adap
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRowTiles; ++i)
-            if (i < rt) *reinterpret_cast<v4f*>(&red[((wave * kRowTiles + i) * 16 + r16) * 16 + 4 * kg]) = acc[i] + lo[i];
+            if (i < rt) *reinterpret_cast<v4f*>(&red[((wave * kRowTiles + i) * 16 + r16) * 16 + 4 * kg]) = whole_sum<W>(acc[i], lo[i]);
         __syncthreads();
         for (int n = threadIdx.x; n < rt * kTile * kTile; n += blockDim.x) {
             const int i = n >> 8, token = n >> 4 & 15, r = n & 15;
@@ -511,7 +527,7 @@ __global__ void __launch_bounds__(64 * kExpandWaves, 3) adapt_expand_kernel(Adap
             if (rank > 0) {
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i)
-                    *reinterpret_cast<v4f*>(&rows[r16 * kRow + 16 * i + 4 * kg]) = acc[i] + lo[i];
+                    *reinterpret_cast<v4f*>(&rows[r16 * kRow + 16 * i + 4 * kg]) = whole_sum<W>(acc[i], lo[i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

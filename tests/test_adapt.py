@@ -312,6 +312,32 @@ def test_one_workspace_for_the_largest_call(qm):
         assert torch.equal(out, ref) and torch.all(ws[need:] == 0x7f)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16], ids=["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("T, rank", [(1, 1), (40, 1), (40, 16), (40, 64), (300, 24)])
+def test_infinities_are_those_of_the_definition(qm, T, rank, dtype):
+    """Infinite inputs and weights, also beside zeros and values that bf16
+    holds whole: an infinity where 64 bits give one, NaN where they give NaN."""
+    x, ids, a, b, scale, y = _case(T, 96, 160, rank, 4, dtype, seed=T + rank, ids=torch.arange(T) % 4)
+    inf = float("inf")
+    a[0, :, 5], b[0, 0::2], b[0, 1::2] = 0.5, 0.25, -0.25
+    x[0::8, 5] = inf                          # adapter 0: +-inf in every column
+    a[0, 0, 6] = 0.0
+    x[4::8, 6] = -inf                         # adapter 0: 0 inf in the first rank, so NaN
+    b[1, 9, rank // 2] = inf
+    a[2, rank - 1, 7], b[2, 11] = -inf, 0.0   # adapter 2: infinite but for 0 inf in column 11
+    x[0::3, 7] = x[0::3, 7].bfloat16().float()
+    x[3::8, 50] = float("nan")
+    y[1::2, 3] = inf
+    with np.errstate(invalid="ignore"):
+        want, _ = _reference(x, ids, a, b, scale, None, y)
+    out = qm.strata_moe_adapt(x, ids, qm.Adapters(a, b, scale), y, torch.empty_like(y)).cpu().numpy()
+    assert np.isinf(want).any() and (T < 8 or np.isnan(want).any())
+    assert np.array_equal(np.isnan(out), np.isnan(want))
+    assert np.array_equal(out[np.isinf(want)], want[np.isinf(want)].astype(np.float32))
+    assert np.array_equal(np.isfinite(out), np.isfinite(want))
+
+
 # -------------------------------------------------------- refusals (no GPU)
 def _call(qm, ad, T=4, x=1 << 20, xs=256, ids=64, y=1 << 24, ys=128, out=1 << 26, os_=128, ws=1 << 28, n=1 << 40):
     p = ctypes.c_void_p

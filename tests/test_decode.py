@@ -409,6 +409,23 @@ def test_one_workspace_for_the_largest_call(qm):
             assert torch.equal(y, ref) and torch.all(ws[need:] == 0x7f)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("mask", [-np.inf, float(np.finfo(np.float32).min)])
+@pytest.mark.parametrize("s", [S.custom(T=3, H=256, E=200, K=4, I=128),
+                               S.custom(T=37, H=896, E=90, K=4, I=1088, shared=True)], ids=lambda s: s.name)
+def test_experts_masked_by_the_bias(qm, s, mask):
+    """All experts but two masked out: the rest of a token's K are masked ones,
+    in the order of their logits or (all -inf) of their indexes, of weight 0."""
+    x, wr = S.activations(s), S.router_weight(s)
+    bias = np.full(s.E, mask, np.float32)
+    bias[[s.E // 3, s.E - 2]] = 0.5
+    y = qm.strata_moe_decode(_t(x), _t(wr), gpu_experts(s).with_router_bias(_t(bias)), s.K,
+                             torch.empty((s.T, s.H), device="cuda"))
+    ref = _oracle(s, x, wr, bias)
+    assert np.all(ref["p"][:, 2:] == 0) and np.all(np.sort(ref["ids"][:, :2], 1) == [s.E // 3, s.E - 2])
+    _check(s, y, ref)
+
+
 # -------------------------------------------------------- refusals (no GPU)
 def _struct(qm, E=16, H=256, I=128, fmt=1):
     gu, dn = qm.strata_moe_packed_bytes(H, I)

@@ -37,7 +37,7 @@
 //
 // What bounds them.  Many tokens: memory, x once for the shrink, y and out
 // once for the expand.  8192 tokens of 2560, 16 adapters of rank 64, bf16: the
-// shrink 35 us (90 MB, 2.6 TB/s), the expand 49 to 58 us (175 MB, 3.0 to 3.6
+// shrink 35 us (90 MB, 2.6 TB/s), the expand 51 to 59 us (175 MB, 3.0 to 3.4
 // TB/s), against 5.1 TB/s of a large copy.  Few tokens: latency, a chain of
 // ids, ranks, weights, the sums' way through the workspace, and the same
 // again: 3.8 + 5.0 us for one token at rank 16, 8.6 + 9.7 us for 32 tokens
@@ -61,7 +61,12 @@ constexpr int kMaxSplit = 16;     // shrink workgroups that share a reduction
 constexpr int kPad = 4;           // floats between the LDS rows of v (spreads the banks)
 // Calls of up to this many tokens give every group of a tile workgroups of its
 // own (the latency of up to 16 groups one after another counts there); longer
-// ones have tiles enough to fill the chip.
+// ones have tiles enough to fill the chip, if prompts give a tile a group or
+// two.  One after another against side by side, in us, 2560 -> 2560, bf16,
+// prompts of 64 requests: rank 64 256 tokens 62, 32, 1000 58, 54, 2048 65, 76;
+// rank 16 256 tokens 33, 19, 512 31, 26, 1000 27, 32.  Rows of mixed adapters,
+// 16 groups a tile, would gain beyond it: rank 64 256 rows 128, 50, 512 139,
+// 79, 1000 207, 142, 2048 285, 264, 4096 490, 501.
 constexpr int kSpreadTokens = 256;
 constexpr int kFill = 512;        // workgroups that fill the chip
 // The outputs are stored past the caches, and y is read past them from this
@@ -71,8 +76,11 @@ constexpr int kFill = 512;        // workgroups that fill the chip
 constexpr int64_t kStreamBytes = (int64_t)48 << 20;
 // From this many tiles on every XCD takes a run of neighbouring tiles: prompts
 // share adapters with their neighbours, and an L2 then holds two or three of
-// them instead of all (8192 tokens, 16 adapters of rank 64, the shrink: 52 us
-// dealt round robin, 35 with a single adapter).
+// them instead of all.  Round robin against runs, in us, 16 adapters, rank 64,
+// bf16: 512 tokens 39.1, 38.1, 1024 43.5, 42.2, 4096 65.4, 61.1, 8192 84.8,
+// 90.1; fp32 65.4, 64.2 at 2048, 130, 138 at 8192; rank 16 26.4, 26.0 at 2048,
+// 58.7, 59.5 at 8192.  (Before the outputs went past the caches round robin
+// took longer at 8192 tokens, too.)
 constexpr int kDealTiles = 64;
 
 struct AdaptArgs {
@@ -269,8 +277,10 @@ struct Products<Bf16, P, N> {
 template <typename W>
 __device__ __forceinline__ v4f whole_sum(v4f acc, v4f lo) {
     if constexpr (std::is_same<W, Bf16>::value) {
+        // in a scalar register: as a constant the compiler keeps it in vector
+        // registers, and others spill (8192 tokens, rank 64: 92.3 us, 90.2)
         float most = __FLT_MAX__;
-        asm("" : "+s"(most));  // a scalar register's: vector registers for it spill (8192 tokens, rank 64: 92.3 us, 90.2)
+        asm("" : "+s"(most));
 #pragma unroll
         for (int j = 0; j < 4; ++j) lo[j] = __builtin_amdgcn_fmed3f(lo[j], -most, most);
     }
@@ -350,7 +360,8 @@ __device__ __forceinline__ void shrink_steps(const AdaptArgs& g, const W* const 
 
 // One workgroup: a tile, up to 64 ranks of its groups, one part of the
 // reduction over in, which its waves split again: a wave's run is then a few
-// steps of 128 bytes per row, and 8 waves hide each other's loads.
+// steps of 128 bytes per row, and 8 waves hide each other's loads.  (128
+// registers: the bf16 form spills 4, the fp32 form 11.)
 template <typename W>
 __global__ void __launch_bounds__(64 * kShrinkWaves, 4) adapt_shrink_kernel(AdaptArgs g) {
     // the waves' panels, then their sums
@@ -398,7 +409,9 @@ __global__ void __launch_bounds__(64 * kShrinkWaves, 4) adapt_shrink_kernel(Adap
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRowTiles; ++i)
-            if (i < rt) *reinterpret_cast<v4f*>(&red[((wave * kRowTiles + i) * 16 + r16) * 16 + 4 * kg]) = whole_sum<W>(acc[i], lo[i]);
+            if (i < rt)
+                *reinterpret_cast<v4f*>(&red[((wave * kRowTiles + i) * 16 + r16) * 16 + 4 * kg]) =
+                    whole_sum<W>(acc[i], lo[i]);
         __syncthreads();
         for (int n = threadIdx.x; n < rt * kTile * kTile; n += blockDim.x) {
             const int i = n >> 8, token = n >> 4 & 15, r = n & 15;
@@ -414,7 +427,8 @@ __global__ void __launch_bounds__(64 * kShrinkWaves, 4) adapt_shrink_kernel(Adap
 // One workgroup: a tile's groups, `turns` runs of 64 outputs per wave (256
 // bytes of each of 16 rows of y and out at a time).  P
 // consecutive ranks per lane: 4 for ranks up to 16, else 8.  kStream: y is
-// large, and is read past the caches.
+// large, and is read past the caches.  (168 registers: with P = 8 the bf16 and
+// fp32 forms spill 6.)
 template <typename W, int P, bool kStream>
 __global__ void __launch_bounds__(64 * kExpandWaves, 3) adapt_expand_kernel(AdaptArgs g) {
     constexpr int kTiles = kExpandCols / 16;
@@ -506,7 +520,7 @@ __global__ void __launch_bounds__(64 * kExpandWaves, 3) adapt_expand_kernel(Adap
                 }
                 // inside B's rows all the same: whole runs, their end zeroed
                 // (32 tokens, ranks 1..64 of 64, fp16: 9.4 us against 11.9;
-                // fp32 runs would spill for it, 146 against 137 at 8192 tokens)
+                // fp32 runs spill more for it, 146 against 137 at 8192 tokens)
                 const bool inside = sizeof(W) == 2 && whole + 4 * P <= g.rank;
                 if constexpr (sizeof(W) == 2)
                     if (inside) {

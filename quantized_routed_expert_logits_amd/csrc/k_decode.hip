@@ -26,9 +26,10 @@
 // follows them 3, the hand-off to down 1, down with the combine 6, the launch
 // the rest.  32 tokens are bound by memory: 8.0 + 124 to 132 us for 595 MB,
 // 4.5 to 4.8 TB/s (a large copy reaches 5.1).  64 tokens on few hot experts
-// (131 MB, 10.2 + 87 us) are bound by the vector unit, 58% busy, and by how
-// evenly 144 chunks fill the chip: a block's 16 outputs a lane take two
-// conversions, a product with d and a 64-bit FMA each.
+// (131 MB, 10.2 + 87 us) fill neither the memory (1.5 TB/s) nor the vector
+// unit, 57% busy (a block's 16 outputs a lane take two conversions, a product
+// and a 64-bit FMA each): 144 chunks of unequal rows are 1152 workgroups on 512
+// places.
 #include <algorithm>
 
 #include "few_tokens.h"
@@ -521,8 +522,10 @@ __device__ __forceinline__ void block_sums(const Weights& r, const Acts<NI>& x, 
         return fma((double)((float)p * d), s, to);
     };
     auto scale = [&](int pa, int pb, uint32_t d, int f, int i) {
-        acc[f][i] = term(pa, (float)__builtin_bit_cast(_Float16, (uint16_t)(d & 0xffffu)), sc[i], acc[f][i]);
-        acc[f + 1][i] = term(pb, (float)__builtin_bit_cast(_Float16, (uint16_t)(d >> 16)), sc[i], acc[f + 1][i]);
+        const float da = (float)__builtin_bit_cast(_Float16, (uint16_t)(d & 0xffffu));
+        const float db = (float)__builtin_bit_cast(_Float16, (uint16_t)(d >> 16));
+        acc[f][i] = term(pa, da, sc[i], acc[f][i]);
+        acc[f + 1][i] = term(pb, db, sc[i], acc[f + 1][i]);
     };
     // the results that no row uses stay allocated until the product is done: a
     // register that a running product still writes cannot be taken without a stall
@@ -1059,9 +1062,13 @@ hipError_t launch_decode(const DecodeLaunch& l, hipStream_t st) {
     // The waves of a slab: all 8 while the slabs are few (the latency of one
     // counts), fewer as the workgroups fill the chip anyway; down, whose
     // reduction is the shorter one, halves first.  In us at H = 2560, I = 1024,
-    // E = 512, K = 10 (gate/up, down waves), before the later steps: one token
-    // 30.0 (8, 8), 29.2 (8, 4), 32.3 (4, 2); 8 tokens 73.6 (8, 4), 64.9 (4,
-    // 2), 73.7 (2, 2); 32 tokens 184.8 (8, 4), 157.6 (4, 2), 150.7 (2, 2).
+    // E = 512, K = 10, (gate/up, down) waves (8, 8), (8, 4), (4, 4), (4, 2),
+    // (2, 2): one token 29.2, 27.9, 27.8, 30.6, 36.9; 4 tokens 46.7, 43.0, 48.8,
+    // 51.6, 51.8; 8 tokens 70.1, 61.8, 57.5, 57.1, 62.1; 16 tokens 120, 104,
+    // 93.4, 88.0, 84.7; 32 tokens 202, 170, 150, 137, 133.  The slabs are those
+    // of the most chunks possible.  Where few of these exist the rule can miss:
+    // 64 tokens on hot experts of I = 640 (144 chunks of 601 possible) 163, 128,
+    // 111, 93.1, 94.0; 8 tokens there 59.8, 50.3, 50.7, 56.9, 62.2.
     // But a wave has 4 blocks at least where the reduction gives them: H = 512,
     // I = 640, 6 experts, 33 tokens 26.5 us, without this 36; H = I = 256, 64
     // experts, 64 tokens 29, 37.

@@ -444,8 +444,8 @@ def test_overlaps(qm):
     assert code(0, 24, 40, ws=base + 256, n=1 << 30) == qm.EINVAL
 
 
-@pytest.mark.parametrize("rank, n_in", [(64, 2560), (16, 2560), (65, 2560), (256, 2560), (1, 100), (13, 1000), (64, 513),
-                                        (200, 65536), (8, 65536), (256, 9000)])
+@pytest.mark.parametrize("rank, n_in", [(64, 2560), (16, 2560), (65, 2560), (256, 2560), (1, 100), (13, 1000),
+                                        (64, 513), (200, 65536), (8, 65536), (256, 9000)])
 def test_workspace_sizes_never_decrease(qm, rank, n_in):
     """One workspace sized for the largest batch serves every smaller one."""
     b, lib = ctypes.c_size_t(), qm.library()

@@ -363,8 +363,12 @@ def _cancelling_layer(H, I, where, fmt):
         sgu[I:I + 64, 0] = half(code / 128)  # h follows the same pattern, in 64 columns
         cd[:, :32] = 3
         sd[:, :2] = half(2047 / 1024)
-    x = lambda T: np.concatenate([code, np.zeros(H - 64, np.float32)]) * 2.0 ** (np.arange(T) % 5 - 2)[:, None]  # noqa: E731
-    return S.Expert(cgu, sgu, cd, sd), lambda T: x(T).astype(np.float32)
+
+    def rows(T):
+        row = np.concatenate([code, np.zeros(H - 64, np.float32)])
+        return (row * 2.0 ** (np.arange(T) % 5 - 2)[:, None]).astype(np.float32)
+
+    return S.Expert(cgu, sgu, cd, sd), rows
 
 
 @pytest.mark.gpu
@@ -496,8 +500,9 @@ def test_binding_refusals(qm):
     assert qm.DECODE_MAX_TOKENS == 64
 
 
-@pytest.mark.parametrize("H, I, E, K", [(1024, 1024, 8, 2), (1024, 1024, 8, 8), (2560, 1024, 512, 10), (2560, 640, 512, 10),
-                                        (1280, 512, 60, 4), (4096, 4096, 3, 1), (128, 64, 1024, 15), (512, 640, 6, 2)])
+@pytest.mark.parametrize("H, I, E, K", [(1024, 1024, 8, 2), (1024, 1024, 8, 8), (2560, 1024, 512, 10),
+                                        (2560, 640, 512, 10), (1280, 512, 60, 4), (4096, 4096, 3, 1),
+                                        (128, 64, 1024, 15), (512, 640, 6, 2)])
 @pytest.mark.parametrize("shared", [False, True])
 @pytest.mark.parametrize("rank", [0, 64])
 def test_workspace_sizes_never_decrease(qm, H, I, E, K, shared, rank):
@@ -507,7 +512,7 @@ def test_workspace_sizes_never_decrease(qm, H, I, E, K, shared, rank):
     ad = qm.AdaptersStruct(2, rank, H, H, 3, 256, 256, None, None)
     b, last = ctypes.c_size_t(), 0
     for T in range(65):
-        assert qm.library().strata_moe_decode_workspace_bytes(T, K, ctypes.byref(st), ctypes.byref(ad) if rank else None,
-                                                              ctypes.byref(b)) == 0
+        assert qm.library().strata_moe_decode_workspace_bytes(
+            T, K, ctypes.byref(st), ctypes.byref(ad) if rank else None, ctypes.byref(b)) == 0
         assert b.value >= last, T
         last = b.value

@@ -4,10 +4,10 @@ Four operators are run here, each over the range of sizes it is used at:
 
 ``quantize``  rows rounded to microscaled 4-bit floating point (a power of two
               per 32 values, 1-2-1 bit values), and the values that the codes
-              stand for (``strata_moe_mx4_quantize``, ``_dequantize``).
+              stand for (``strata_moe_mxfp_quantize``, ``_dequantize``).
 ``product``   out[r] = W_e x[src[r]] for the rows r of each expert e, both sides
               in that format; with ``swiglu`` the rows of W are [gate; up] and
-              out[r] = silu(g) u (``strata_moe_mx4_product``).  With one expert
+              out[r] = silu(g) u (``strata_moe_mxfp_product``).  With one expert
               and no grouping it is a plain projection.
 ``before``    the layer's input from the residual stream: x = norm(h), a root
               mean square norm (``strata_moe_norm_before``).
@@ -220,7 +220,7 @@ def _inputs_product(case, g):
         else:
             x_rows = rows
     s["rows"] = rows
-    codes, scales = _round_mx4(_hidden(x_rows, n_in, g))
+    codes, scales = _round_mxfp(_hidden(x_rows, n_in, g))
     s["x_codes"], s["x_scales"] = _packed(codes), scales
     # weights as a 4-bit pack holds them: every code about as often, scales a few powers of two around 2^-8
     s["w_codes"] = torch.randint(0, 256, (E, n_w, n_in // 2), generator=g, device="cuda", dtype=torch.uint8)
@@ -276,7 +276,7 @@ def prepare(case, seed):
         return torch.empty((rows, cols + pad), dtype=dtype, device="cuda")[:, :cols]
 
     if case["op"] == "product":
-        w = qm.Mx4Weights(case["E"], s["w_codes"].shape[1], case["n_in"], swiglu=case["swiglu"], device="cuda")
+        w = qm.MxfpWeights(case["E"], s["w_codes"].shape[1], case["n_in"], swiglu=case["swiglu"], device="cuda")
         w.pack(0, s.pop("w_codes"), s.pop("w_scales"))
         s["weights"] = w
         s["out"] = empty(s["rows"], case["n_out"], dt, case["pad"])
@@ -307,10 +307,10 @@ def run(state):
 def _run_own(s, case):
     qm = s["qm"]
     if case["op"] == "quantize":
-        codes, scales = qm.strata_moe_mx4_quantize(s["x"], s["codes"], s["scales"])
-        return qm.strata_moe_mx4_dequantize(codes, scales, s["out"])
+        codes, scales = qm.strata_moe_mxfp_quantize(s["x"], s["codes"], s["scales"])
+        return qm.strata_moe_mxfp_dequantize(codes, scales, s["out"])
     if case["op"] == "product":
-        return qm.strata_moe_mx4_product(s["x_codes"], s["x_scales"], s["weights"], s["out"], offsets=s["offsets"],
+        return qm.strata_moe_mxfp_product(s["x_codes"], s["x_scales"], s["weights"], s["out"], offsets=s["offsets"],
                                          src=s["src"])
     if case["op"] == "before":
         qm.strata_moe_norm_before(s["h"], s["norm"], s["x_out"], codes=s["codes"], scales=s["scales"])
@@ -321,7 +321,7 @@ def _run_own(s, case):
                                  x=s["x_out"], codes=s["codes"], scales=s["scales"])
         res = [s["out"]] + ([s["x_out"]] if case["follow"] else [])
     if case["codes"]:
-        res.append(qm.strata_moe_mx4_dequantize(s["codes"], s["scales"], s["values"]))
+        res.append(qm.strata_moe_mxfp_dequantize(s["codes"], s["scales"], s["values"]))
     return res
 
 
@@ -330,7 +330,7 @@ def _power(byte):
     return torch.where(byte == 255, math.nan, torch.ldexp(torch.ones((), device=byte.device), byte.int() - 127))
 
 
-def _round_mx4(x):
+def _round_mxfp(x):
     """[..., n] -> codes 0..15 [..., n] and scale bytes [..., n / 32]: a power
     of two 2^e with e = floor(log2(largest magnitude)) - 2, and each value over
     it rounded to the nearest of the eight magnitudes (ties to the even code,
@@ -358,12 +358,12 @@ def _values(codes, scales):
 
 def _run_plain(s, case):
     if case["op"] == "quantize":
-        return _values(*_round_mx4(s["x"])).to(s["x"].dtype)
+        return _values(*_round_mxfp(s["x"])).to(s["x"].dtype)
     if case["op"] == "product":
         return _plain_product(s, case)
     if case["op"] == "before":
         x = _plain_norm(s["h"].double(), s["weight"], case["offset"]).float()
-        return [x] + ([_values(*_round_mx4(x))] if case["codes"] else [])
+        return [x] + ([_values(*_round_mxfp(x))] if case["codes"] else [])
     return _plain_after(s, case)
 
 
@@ -385,7 +385,7 @@ def _plain_after(s, case):
     if case["follow"]:
         res.append(_plain_norm(out.double(), s["next"], 0.0).float())
         if case["codes"]:
-            res.append(_values(*_round_mx4(res[1])))
+            res.append(_values(*_round_mxfp(res[1])))
     return res
 
 
@@ -411,16 +411,16 @@ def _plain_product(s, case):
 def exact(case, seed):
     s = _inputs(case, seed)
     if case["op"] == "quantize":
-        return _exact_mx4(s["x"].double())
+        return _exact_mxfp(s["x"].double())
     if case["op"] == "product":
         return _exact_product(s, case)
     if case["op"] == "before":
         x = _exact_norm(s["h"].double(), s["weight"].double() + case["offset"])
-        return [x] + ([_exact_mx4(x.float().double())] if case["codes"] else [])
+        return [x] + ([_exact_mxfp(x.float().double())] if case["codes"] else [])
     return _exact_after(s, case)
 
 
-def _exact_mx4(x):
+def _exact_mxfp(x):
     """The values that the 4-bit rounding of x stands for: on the grid of step
     max(2^(floor(log2|q|) - 1), 1/2) below 6, halves to the even multiple."""
     v = x.unflatten(-1, (-1, BLOCK))
@@ -480,5 +480,5 @@ def _exact_after(s, case):
         x = _exact_norm(out.to(s["h"].dtype).double(), s["next"].double())
         res.append(x)
         if case["codes"]:
-            res.append(_exact_mx4(x.float().double()))
+            res.append(_exact_mxfp(x.float().double()))
     return res

@@ -424,6 +424,138 @@ int strata_moe_decode(const float* x, const float* router_w, const strata_moe_ex
                       const strata_moe_adapters* adapters, const int32_t* adapter_ids, float* out, void* workspace,
                       size_t workspace_bytes, void* stream);
 
+/* ------------------------- microscaled 4-bit floating point: rows, products */
+
+/* Element types of the rows below (fp32, fp16, bf16). */
+#define STRATA_MOE_F32 1
+#define STRATA_MOE_F16 2
+#define STRATA_MOE_BF16 3
+
+/* The format: 32 consecutive values of a row share a power of two; a value is
+ * a sign and a magnitude of 0, 0.5, 1, 1.5, 2, 3, 4 or 6 (code bit 3 the sign,
+ * bits 2..1 the exponent, bit 0 the mantissa).  Arrays:
+ *   codes  [rows][cols / 2] bytes, value 2 j in the low half of byte j
+ *   scales [rows][cols / 32] bytes, 2^(byte - 127); 255 is NaN
+ * cols is a multiple of 32 in [32, 65536], rows in [0, 2^24], codes 16-byte
+ * aligned; both arrays are contiguous, scales needs no alignment. */
+
+/* x (rows of `dtype`, x_stride elements apart) rounded to it: the scale of a
+ * block is 2^(floor(log2 max|v|) - 2), not below 2^-127, and a value over it
+ * goes to the nearest magnitude, ties to the even code, above 6 to 6.  A block
+ * of zeros has scale byte 0; one that holds an infinity or NaN has byte 255
+ * and codes 0, so all its values are NaN.  Errors: EINVAL for sizes (also rows
+ * * cols >= 2^35), NULL pointers, alignment, strides or overlap, EUNSUPPORTED
+ * for an unknown dtype. */
+int strata_moe_mxfp_quantize(const void* x, int32_t dtype, int64_t x_stride, int64_t rows, int32_t cols,
+                             uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values that codes and scales stand for, into rows of `dtype` (rounded to
+ * it; bf16 and fp32 hold them exactly, bf16 except below 2^-133).  Errors:
+ * those of strata_moe_mxfp_quantize. */
+int strata_moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* out,
+                               int32_t dtype, int64_t out_stride, void* stream);
+
+/* Weight matrices in the product's own layout (strata_moe_mxfp_pack).
+ *   n_expert: 1 .. 1024 matrices, expert e at packed + e * stride
+ *   rows, cols: of one matrix (rows in [1, 65536]; the reduction is over cols)
+ *   swiglu: 1 if a matrix is [gate; up] (rows even) and the product's output
+ *           silu(gate x) (up x) of rows / 2 values, silu(v) = v / (1 + exp(-v))
+ *   stride: a multiple of 256, at least strata_moe_mxfp_packed_bytes(). */
+typedef struct strata_moe_mxfp_weights {
+    int32_t n_expert;
+    int32_t rows;
+    int32_t cols;
+    int32_t swiglu;
+    const void* packed;
+    int64_t stride;
+} strata_moe_mxfp_weights;
+
+/* Bytes of one packed matrix. */
+int strata_moe_mxfp_packed_bytes(int32_t rows, int32_t cols, int32_t swiglu, int64_t* bytes);
+
+/* Pack experts [e0, e1) from codes [e1 - e0][rows][cols / 2] and scales
+ * [e1 - e0][rows][cols / 32] (the arrays of strata_moe_mxfp_quantize) to
+ * packed + e * stride; packed is 256-byte aligned.  Asynchronous on `stream`. */
+int strata_moe_mxfp_pack(const uint8_t* codes, const uint8_t* scales, int32_t e0, int32_t e1, int32_t rows,
+                         int32_t cols, int32_t swiglu, void* packed, int64_t stride, void* stream);
+
+/* out[r] = W_e x[src[r]] for the rows r in [offsets[e], offsets[e + 1]) of each
+ * expert e (strata_moe_group's arrays), both sides in 4 bits, sums in fp32; with
+ * swiglu out[r] = silu(gate) up of it.
+ *   codes, scales: x, [x_rows] rows of weights->cols values
+ *   offsets: [n_expert + 1] int32 on the device, or NULL with one expert: all
+ *            rows are its.  Read on the device, within [0, rows]; rows that no
+ *            expert has are left as they were.
+ *   src:     [rows] int32 on the device, or NULL: row r of x (x_rows >= rows).
+ *            A row whose src is outside [0, x_rows) counts as zeros.
+ *   out:     [rows] rows of weights->rows values (rows / 2 with swiglu) of
+ *            `dtype`, out_stride elements apart; must not overlap an input
+ * rows and x_rows are at most 2^24 and x_rows * cols below 2^33.  No workspace;
+ * the call only enqueues one kernel, so calls may overlap and be captured, and
+ * repeated calls give the same bits.  Errors: EINVAL for sizes, NULL pointers,
+ * alignment, strides or overlap, EUNSUPPORTED for an unknown dtype. */
+int strata_moe_mxfp_product(const uint8_t* codes, const uint8_t* scales, int64_t x_rows,
+                            const strata_moe_mxfp_weights* weights, const int32_t* offsets, const int32_t* src,
+                            int64_t rows, void* out, int32_t dtype, int64_t out_stride, void* stream);
+
+/* ------------------------------------------ norms before and after a block */
+
+/* norm(v)_j = v_j / sqrt(mean(v^2) + eps) * (weight_offset + weight_j), with
+ * weight [H] fp32 on the device, or NULL: norm(v)_j = v_j / sqrt(...). */
+typedef struct strata_moe_norm {
+    const float* weight;
+    double weight_offset;
+    double eps;
+} strata_moe_norm;
+
+/* The layer's input from the residual stream: x = norm(h) for T rows of H.
+ *   h:  rows of `dtype`, h_stride elements apart
+ *   x:  [T][H] fp32 (what strata_moe_prefill and strata_moe_decode take), or NULL
+ *   codes, scales: x rounded as strata_moe_mxfp_quantize does (H a multiple of
+ *       32), or both NULL
+ * 0 <= T <= 2^24, 1 <= H <= 16384.  The arithmetic is in fp64, each output is
+ * rounded once.  Outputs overlap neither each other nor an input.  Errors:
+ * EINVAL for sizes, NULL pointers, alignment, strides or overlap, EUNSUPPORTED
+ * for an unknown dtype. */
+int strata_moe_norm_before(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H,
+                           const strata_moe_norm* norm, float* x, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* A block's output on its way back into the stream (host struct).
+ *   y:     y_rows rows of y_dtype, y_stride elements apart
+ *   slot, p: [T][K] int32 and fp32 on the device: v[t] = sum over k of p[t][k]
+ *          y[slot[t][k]] (the combine of strata_moe_group's rows; a slot outside
+ *          [0, y_rows) adds nothing), 1 <= K <= 16; or both NULL with K = 0:
+ *          v[t] = y[t]
+ *   norm:  applied to v, or NULL: none
+ *   gate:  fp32 factor gate[t gate_row_stride + j gate_col_stride] (column
+ *          stride 0 or 1, row stride >= 0: a channel's, a token's or each
+ *          value's), or NULL: 1 */
+typedef struct strata_moe_branch {
+    const void* y;
+    int64_t y_stride;
+    int64_t y_rows;
+    int32_t y_dtype;
+    int32_t K;
+    const int32_t* slot;
+    const float* p;
+    const strata_moe_norm* norm;
+    const float* gate;
+    int64_t gate_row_stride;
+    int32_t gate_col_stride;
+    double residual_scale;
+    double block_scale;
+} strata_moe_branch;
+
+/* out = residual_scale h + block_scale gate norm(v), rounded to `dtype`, and
+ * with `next` the input of the block that follows, x = next(out) (from out as
+ * it is stored) with x, codes and scales as in strata_moe_norm_before.
+ *   out: T rows, out_stride elements apart; may be h itself (the same pointer
+ *        and stride), and overlaps no other array
+ * Sizes, arithmetic and errors: those of strata_moe_norm_before. */
+int strata_moe_norm_after(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H,
+                          const strata_moe_branch* branch, void* out, int64_t out_stride,
+                          const strata_moe_norm* next, float* x, uint8_t* codes, uint8_t* scales, void* stream);
+
 /* ----------------------------------------------------------------- timing */
 
 /* Per-kernel GPU timing with HIP events on the launch stream.  enable=1

@@ -63,6 +63,21 @@ class AdaptersStruct(ctypes.Structure):
                 ("a", _P), ("b", _P), ("scale", _P), ("ranks", _P)]
 
 
+class MxfpWeightsStruct(ctypes.Structure):
+    _fields_ = [("n_expert", _i32), ("rows", _i32), ("cols", _i32), ("swiglu", _i32), ("packed", _P),
+                ("stride", _i64)]
+
+
+class NormStruct(ctypes.Structure):
+    _fields_ = [("weight", _P), ("weight_offset", ctypes.c_double), ("eps", ctypes.c_double)]
+
+
+class BranchStruct(ctypes.Structure):
+    _fields_ = [("y", _P), ("y_stride", _i64), ("y_rows", _i64), ("y_dtype", _i32), ("K", _i32), ("slot", _P),
+                ("p", _P), ("norm", ctypes.POINTER(NormStruct)), ("gate", _P), ("gate_row_stride", _i64),
+                ("gate_col_stride", _i32), ("residual_scale", ctypes.c_double), ("block_scale", ctypes.c_double)]
+
+
 def _sig(name, args, res=ctypes.c_int):
     f = getattr(_lib, name)
     f.argtypes = args
@@ -99,6 +114,14 @@ _sig("strata_moe_decode_workspace_bytes", [_i64, _i32, ctypes.POINTER(ExpertsStr
                                            ctypes.POINTER(ctypes.c_size_t)])
 _sig("strata_moe_decode", [_P, _P, ctypes.POINTER(ExpertsStruct), _i64, _i32, ctypes.POINTER(AdaptersStruct), _P, _P,
                            _P, ctypes.c_size_t, _P])
+_sig("strata_moe_mxfp_quantize", [_P, _i32, _i64, _i64, _i32, _P, _P, _P])
+_sig("strata_moe_mxfp_dequantize", [_P, _P, _i64, _i32, _P, _i32, _i64, _P])
+_sig("strata_moe_mxfp_packed_bytes", [_i32, _i32, _i32, ctypes.POINTER(_i64)])
+_sig("strata_moe_mxfp_pack", [_P, _P, _i32, _i32, _i32, _i32, _i32, _P, _i64, _P])
+_sig("strata_moe_mxfp_product", [_P, _P, _i64, ctypes.POINTER(MxfpWeightsStruct), _P, _P, _i64, _P, _i32, _i64, _P])
+_sig("strata_moe_norm_before", [_P, _i32, _i64, _i64, _i32, ctypes.POINTER(NormStruct), _P, _P, _P, _P])
+_sig("strata_moe_norm_after", [_P, _i32, _i64, _i64, _i32, ctypes.POINTER(BranchStruct), _P, _i64,
+                               ctypes.POINTER(NormStruct), _P, _P, _P, _P])
 _sig("strata_moe_timing", [ctypes.c_int, _i32])
 _sig("strata_moe_timing_kinds", [])
 _sig("strata_moe_timing_name", [ctypes.c_int], ctypes.c_char_p)
@@ -113,11 +136,14 @@ EXPORTED = [
     "strata_moe_timing_kinds", "strata_moe_timing_name", "strata_moe_timing_read",
     "strata_moe_ring_bytes", "strata_moe_ring_create", "strata_moe_ring_destroy", "strata_moe_prefill_streamed",
     "strata_moe_prefill_noalloc", "strata_moe_adapt_workspace_bytes", "strata_moe_adapt",
-    "strata_moe_decode_workspace_bytes", "strata_moe_decode",
+    "strata_moe_decode_workspace_bytes", "strata_moe_decode", "strata_moe_mxfp_quantize",
+    "strata_moe_mxfp_dequantize", "strata_moe_mxfp_packed_bytes", "strata_moe_mxfp_pack", "strata_moe_mxfp_product",
+    "strata_moe_norm_before", "strata_moe_norm_after",
 ]
 NOALLOC_SCRATCH_BYTES = 512 << 20  # STRATA_MOE_NOALLOC_SCRATCH_BYTES
 DECODE_MAX_TOKENS = 64             # STRATA_MOE_DECODE_MAX_TOKENS
 ADAPTER_DTYPES = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}  # STRATA_MOE_ADAPTER_*
+ROW_DTYPES = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}      # STRATA_MOE_F32, _F16, _BF16
 
 
 def library() -> ctypes.CDLL:
@@ -627,6 +653,253 @@ def strata_moe_decode(x: torch.Tensor, router_w: torch.Tensor, experts: Experts,
 
     return _with_workspace(call, x.device, workspace,
                            lambda: strata_moe_decode_workspace_bytes(T, K, experts, adapters), stream)
+
+
+# ------------------------------------- 4-bit floating point, norms of a block
+def _float_rows(t, name: str, rows: int | None = None, width: int | None = None) -> int:
+    """A [rows][width] fp32, fp16 or bf16 tensor with contiguous rows that do not overlap -> its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in ROW_DTYPES:
+        raise TypeError(f"{name} must be one of {sorted(str(d) for d in ROW_DTYPES)}, got {t.dtype}")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (width is not None and t.shape[1] != width):
+        want = "2-D" if rows is None and width is None else (rows, width)
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+    if (t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _mxfp_arrays(codes, scales, rows: int, cols: int) -> None:
+    for name, t, n in (("codes", codes, cols // 2), ("scales", scales, cols // 32)):
+        _expect(t, name, (rows, n), torch.uint8)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _on_device(device, stream, call):
+    """call(stream) with `device` current; the stream is the device's current one if none is given."""
+    index = device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(device):
+            return _on_device(device, stream, call)
+    return call(torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+
+
+def _made_on(device, stream):
+    """Where an output that a call allocates is allocated: the call's own stream."""
+    if stream is None:
+        return torch.cuda.device(device)
+    return torch.cuda.stream(stream)
+
+
+def strata_moe_mxfp_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                             stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """x [rows][cols] (fp32, fp16 or bf16; rows may be padded) -> codes uint8 [rows][cols/2], two 4-bit values a
+    byte, and scales uint8 [rows][cols/32], powers of two."""
+    xs = _float_rows(x, "x")
+    rows, cols = x.shape
+    _one_device(x=x, codes=codes, scales=scales)
+    if codes is None or scales is None:
+        with _made_on(x.device, stream):
+            if codes is None:
+                codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+            if scales is None:
+                scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
+    _mxfp_arrays(codes, scales, rows, cols)
+    _on_device(x.device, stream, lambda st: _check(
+        _lib.strata_moe_mxfp_quantize(x.data_ptr(), ROW_DTYPES[x.dtype], xs, rows, cols, codes.data_ptr(),
+                                      scales.data_ptr(), st), "strata_moe_mxfp_quantize"))
+    return codes, scales
+
+
+def strata_moe_mxfp_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> torch.Tensor:
+    """The values that codes and scales stand for, into out [rows][cols] (fp32, fp16 or bf16)."""
+    os_ = _float_rows(out, "out")
+    rows, cols = out.shape
+    _mxfp_arrays(codes, scales, rows, cols)
+    _one_device(codes=codes, scales=scales, out=out)
+    _on_device(out.device, stream, lambda st: _check(
+        _lib.strata_moe_mxfp_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
+                                        ROW_DTYPES[out.dtype], os_, st), "strata_moe_mxfp_dequantize"))
+    return out
+
+
+def strata_moe_mxfp_packed_bytes(rows: int, cols: int, swiglu: bool = False) -> int:
+    b = _i64()
+    _check(_lib.strata_moe_mxfp_packed_bytes(rows, cols, int(swiglu), ctypes.byref(b)), "strata_moe_mxfp_packed_bytes")
+    return b.value
+
+
+class MxfpWeights:
+    """n_expert packed 4-bit matrices [rows][cols] in device memory.  swiglu: a matrix is [gate; up] and the product
+    gives silu(gate x) (up x) of rows / 2 values."""
+
+    def __init__(self, n_expert: int, rows: int, cols: int, swiglu: bool = False,
+                 device: str | torch.device = "cuda"):
+        self.n_expert, self.rows, self.cols, self.swiglu = n_expert, rows, cols, bool(swiglu)
+        self.n_out = rows // 2 if self.swiglu else rows
+        self.stride = strata_moe_mxfp_packed_bytes(rows, cols, self.swiglu)
+        if not 1 <= n_expert <= 1024:
+            raise ValueError(f"n_expert {n_expert} outside [1, 1024]")
+        self.packed = torch.empty(n_expert * self.stride, dtype=torch.uint8, device=device)
+        self.struct = MxfpWeightsStruct(n_expert, rows, cols, int(self.swiglu), self.packed.data_ptr(), self.stride)
+
+    def pack(self, e0: int, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> "MxfpWeights":
+        """Pack experts [e0, e0 + n) from codes [n][rows][cols/2] and scales [n][rows][cols/32]."""
+        strata_moe_mxfp_pack(codes, scales, e0, self, stream)
+        return self
+
+
+def strata_moe_mxfp_pack(codes: torch.Tensor, scales: torch.Tensor, e0: int, weights: MxfpWeights, stream=None) -> None:
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
+        raise ValueError("codes must be [n][rows][cols/2]")
+    n = codes.shape[0]
+    _expect(codes, "codes", (n, weights.rows, weights.cols // 2), torch.uint8)
+    _expect(scales, "scales", (n, weights.rows, weights.cols // 32), torch.uint8)
+    _one_device(codes=codes, scales=scales, packed=weights.packed)
+    if e0 < 0 or e0 + n > weights.n_expert:
+        raise ValueError(f"experts [{e0}, {e0 + n}) outside [0, {weights.n_expert})")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("codes and scales must be contiguous")
+    _on_device(codes.device, stream, lambda st: _check(
+        _lib.strata_moe_mxfp_pack(codes.data_ptr(), scales.data_ptr(), e0, e0 + n, weights.rows, weights.cols,
+                                  int(weights.swiglu), weights.packed.data_ptr(), weights.stride, st),
+        "strata_moe_mxfp_pack"))
+
+
+def strata_moe_mxfp_product(codes: torch.Tensor, scales: torch.Tensor, weights: MxfpWeights, out: torch.Tensor,
+                            offsets: torch.Tensor | None = None, src: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """out[r] = W_e x[src[r]] for the rows r of expert e, [offsets[e], offsets[e+1]).  codes, scales: x in 4 bits;
+    out [rows][n_out] fp32, fp16 or bf16 (rows may be padded).  One expert needs no offsets; without src row r is
+    x's row r."""
+    if not isinstance(weights, MxfpWeights):
+        raise TypeError("weights must be an MxfpWeights object")
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError("codes must be [x_rows][cols/2]")
+    x_rows = codes.shape[0]
+    _mxfp_arrays(codes, scales, x_rows, weights.cols)
+    os_ = _float_rows(out, "out", width=weights.n_out)
+    rows = out.shape[0]
+    if offsets is not None:
+        _expect(offsets, "offsets", (weights.n_expert + 1,), torch.int32)
+    if src is not None:
+        _expect(src, "src", (rows,), torch.int32)
+    _one_device(codes=codes, scales=scales, packed=weights.packed, out=out, offsets=offsets, src=src)
+    for name, t in (("offsets", offsets), ("src", src)):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _on_device(out.device, stream, lambda st: _check(
+        _lib.strata_moe_mxfp_product(codes.data_ptr(), scales.data_ptr(), x_rows, ctypes.byref(weights.struct),
+                                     None if offsets is None else offsets.data_ptr(),
+                                     None if src is None else src.data_ptr(), rows, out.data_ptr(),
+                                     ROW_DTYPES[out.dtype], os_, st), "strata_moe_mxfp_product"))
+    return out
+
+
+class Norm:
+    """A root mean square norm: v / sqrt(mean(v^2) + eps) * (weight_offset + weight); weight [H] float32 or None."""
+
+    def __init__(self, weight: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0):
+        if weight is not None:
+            if not isinstance(weight, torch.Tensor) or weight.dim() != 1:
+                raise ValueError("weight must be a 1-D [H] tensor")
+            _dtype(weight, torch.float32, "weight")
+            if not weight.is_contiguous():
+                raise ValueError("weight must be contiguous")
+        self.weight, self.eps, self.weight_offset = weight, eps, weight_offset
+        self.struct = NormStruct(None if weight is None else weight.data_ptr(), weight_offset, eps)
+
+
+def _check_norm(norm, name: str, H: int):
+    if not isinstance(norm, Norm):
+        raise TypeError(f"{name} must be a Norm object")
+    if norm.weight is not None:
+        _expect(norm.weight, f"{name}'s weight", (H,), torch.float32)
+    return norm.weight
+
+
+def _norm_outputs(x, codes, scales, T: int, H: int) -> None:
+    if x is not None:
+        _expect(x, "x", (T, H), torch.float32)
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous")
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales come together")
+    if codes is not None:
+        _mxfp_arrays(codes, scales, T, H)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def strata_moe_norm_before(h: torch.Tensor, norm: Norm, x: torch.Tensor | None = None,
+                           codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None) -> None:
+    """x = norm(h): the layer's fp32 input from the residual stream h [T][H] (fp32, fp16 or bf16; rows may be
+    padded), and with codes and scales (uint8, as strata_moe_mxfp_quantize) x in 4 bits."""
+    hs = _float_rows(h, "h")
+    T, H = h.shape
+    weight = _check_norm(norm, "norm", H)
+    _norm_outputs(x, codes, scales, T, H)
+    _one_device(h=h, weight=weight, x=x, codes=codes, scales=scales)
+    _on_device(h.device, stream, lambda st: _check(
+        _lib.strata_moe_norm_before(h.data_ptr(), ROW_DTYPES[h.dtype], hs, T, H, ctypes.byref(norm.struct), _opt(x),
+                                    _opt(codes), _opt(scales), st), "strata_moe_norm_before"))
+
+
+def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, norm: Norm | None = None,
+                          slot: torch.Tensor | None = None, p: torch.Tensor | None = None,
+                          gate: torch.Tensor | None = None, residual_scale: float = 1.0, block_scale: float = 1.0,
+                          next_norm: Norm | None = None, x: torch.Tensor | None = None,
+                          codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """out = residual_scale h + block_scale gate norm(v), v[t] = y[t], or with slot and p [T][K] the sum over k of
+    p[t][k] y[slot[t][k]].  gate: float32 [H], [T][1] or [T][H].  out may be h.  next_norm: also the next block's
+    input x = next_norm(out) (x, codes and scales as in strata_moe_norm_before)."""
+    hs = _float_rows(h, "h")
+    T, H = h.shape
+    os_ = _float_rows(out, "out", T, H)
+    _dtype(out, h.dtype, "out")
+    ys = _float_rows(y, "y", width=H)
+    K = 0
+    if (slot is None) != (p is None):
+        raise ValueError("slot and p come together")
+    if slot is not None:
+        if not isinstance(slot, torch.Tensor) or slot.dim() != 2:
+            raise ValueError("slot must be [T][K]")
+        K = slot.shape[1]
+        _expect(slot, "slot", (T, K), torch.int32)
+        _expect(p, "p", (T, K), torch.float32)
+        if not slot.is_contiguous() or not p.is_contiguous():
+            raise ValueError("slot and p must be contiguous")
+    elif y.shape[0] != T:
+        raise ValueError(f"y has {y.shape[0]} rows for {T} tokens")
+    grow = gcol = 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch tensor")
+        _dtype(gate, torch.float32, "gate")
+        if tuple(gate.shape) not in ((H,), (T, 1), (T, H)):
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {(H,)}, {(T, 1)} or {(T, H)}")
+        grow = gate.stride(0) if gate.dim() == 2 and T > 1 else 0
+        gcol = gate.stride(-1) if gate.shape[-1] > 1 else 0
+        if gcol not in (0, 1) or grow < 0:
+            raise ValueError("gate must have contiguous or broadcast rows")
+    weight = None if norm is None else _check_norm(norm, "norm", H)
+    next_weight = None if next_norm is None else _check_norm(next_norm, "next_norm", H)
+    _norm_outputs(x, codes, scales, T, H)
+    _one_device(h=h, y=y, out=out, slot=slot, p=p, gate=gate, weight=weight, next_weight=next_weight, x=x,
+                codes=codes, scales=scales)
+    branch = BranchStruct(y.data_ptr(), ys, y.shape[0], ROW_DTYPES[y.dtype], K, _opt(slot), _opt(p),
+                          None if norm is None else ctypes.pointer(norm.struct), _opt(gate), grow, gcol,
+                          residual_scale, block_scale)
+    _on_device(h.device, stream, lambda st: _check(
+        _lib.strata_moe_norm_after(h.data_ptr(), ROW_DTYPES[h.dtype], hs, T, H, ctypes.byref(branch), out.data_ptr(),
+                                   os_, None if next_norm is None else ctypes.byref(next_norm.struct), _opt(x),
+                                   _opt(codes), _opt(scales), st), "strata_moe_norm_after"))
+    return out
 
 
 # -------------------------------------------------------------- single steps

@@ -1,0 +1,91 @@
+// Device helpers of microscaled 4-bit floating point (E2M1 values, one power
+// of two per 32) and of rows in fp32, fp16 or bf16.
+#pragma once
+
+#include "block.h"
+
+namespace strata_moe {
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(_Float16 v) { return (float)v; }
+__device__ __forceinline__ float widen(__bf16 v) { return (float)v; }
+
+__device__ __forceinline__ void load4_vec(const float* p, float* v) {
+    const float4 f = *(const float4*)p;
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+}
+__device__ __forceinline__ void load4_vec(const _Float16* p, float* v) {
+    const v4h f = *(const v4h*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)f[i];
+}
+__device__ __forceinline__ void load4_vec(const __bf16* p, float* v) {
+    const uint2 f = *(const uint2*)p;
+    v[0] = __uint_as_float(f.x << 16), v[1] = __uint_as_float(f.x & 0xffff0000u);
+    v[2] = __uint_as_float(f.y << 16), v[3] = __uint_as_float(f.y & 0xffff0000u);
+}
+
+// v (4 values that are exact in type T) to columns j..j+3 of a row of H.
+template <typename T, typename V>
+__device__ __forceinline__ void store4(T* row, int j, int H, bool vec, const float* v) {
+    if (vec && j + 4 <= H) {
+        V o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = (T)v[i];
+        *(V*)(row + j) = o;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (j + i < H) row[j + i] = (T)v[i];
+}
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void store4_any(void* base, int dtype, int64_t at, int j, int H, bool vec, const float* v) {
+    if (dtype == kF32) store4<float, v4f>((float*)base + at, j, H, vec, v);
+    else if (dtype == kF16) store4<_Float16, v4h>((_Float16*)base + at, j, H, vec, v);
+    else store4<__bf16, v4b>((__bf16*)base + at, j, H, vec, v);
+}
+
+// v in 64 bits rounded to the type, once: fp32 to nearest, and the 16-bit
+// types from a 32-bit value rounded to odd, which keeps the second rounding
+// from meeting a tie that the first one made.  *o: the value as fp32.
+__device__ __forceinline__ double round_once(double v, int dtype, float* o) {
+    float f = (float)v;
+    if (dtype == kF32) {
+        *o = f;
+        return f;
+    }
+    const double d = (double)f;
+    if (d != v && __builtin_isfinite(f)) {
+        uint32_t u = __float_as_uint(f);
+        if (!(u & 1)) u += fabs(d) < fabs(v) ? 1u : ~0u;  // f even, so its neighbours are odd
+        f = __uint_as_float(u);
+    }
+    *o = dtype == kF16 ? (float)(_Float16)f : (float)(__bf16)f;
+    return *o;
+}
+
+// ---- 4-bit blocks
+// The scale byte of a block whose largest magnitude has these fp32 bits:
+// 2^(byte - 127) = 2^(floor(log2 top) - 2), not below 2^-127; 255 (NaN) for an
+// infinite or NaN value.  A zero block has byte 0.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
+    const uint32_t e = top >> 23;
+    return e == 255 ? 255u : e < 2 ? 0u : e - 2;
+}
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+    return __uint_as_float(byte == 255 ? 0x7fc00000u : byte ? byte << 23 : 0x00400000u);
+}
+// The codes of a and b (nearest, ties to even, magnitudes above 6 to 6) into
+// byte B of q, a in the low half.
+template <int B>
+__device__ __forceinline__ uint32_t mx_code_pair(uint32_t q, float a, float b, uint32_t byte) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, a, b, mx_scale(byte), B);
+}
+
+}  // namespace strata_moe

@@ -21,6 +21,7 @@
 #include <vector>
 
 #include "../../include/strata_moe.h"
+#include "block.h"
 #include "few_tokens.h"
 #include "internal.h"
 
@@ -698,11 +699,11 @@ int check_workspace(const void* ws, size_t have, size_t need) {
     return 0;
 }
 
-// T rows of `width` fp32, `stride` apart.
+// T rows of `width` elements of `el` bytes, `stride` elements apart.
 struct RowSet {
     uintptr_t base;
-    int64_t T, stride, width;
-    uintptr_t bytes() const { return (uintptr_t)(((T - 1) * stride + width) * 4); }  // first element to past the last
+    int64_t T, stride, width, el = 4;
+    uintptr_t bytes() const { return (uintptr_t)(((T - 1) * stride + width) * el); }  // first element to past the last
 };
 
 bool overlap(uintptr_t a, uintptr_t an, uintptr_t b, uintptr_t bn) { return a < b + bn && b < a + an; }
@@ -710,10 +711,10 @@ bool overlap(uintptr_t a, uintptr_t an, uintptr_t b, uintptr_t bn) { return a < 
 // Rows of one stride may lie beside each other, as columns of one array do.
 bool overlap(const RowSet& a, const RowSet& b) {
     if (!overlap(a.base, a.bytes(), b.base, b.bytes())) return false;
-    if (a.stride != b.stride) return true;
-    const uintptr_t pitch = (uintptr_t)a.stride * 4;
+    if (a.stride * a.el != b.stride * b.el) return true;
+    const uintptr_t pitch = (uintptr_t)(a.stride * a.el);
     const uintptr_t from = b.base >= a.base ? (b.base - a.base) % pitch : pitch - 1 - (a.base - b.base - 1) % pitch;
-    return from < (uintptr_t)a.width * 4 || from + (uintptr_t)b.width * 4 > pitch;
+    return from < (uintptr_t)(a.width * a.el) || from + (uintptr_t)(b.width * b.el) > pitch;
 }
 
 AdaptLaunch adapt_launch(const strata_moe_adapters* ad, const int32_t* ids, int64_t T, char* ws) {
@@ -748,6 +749,118 @@ int decode_sizes(int64_t T, int32_t K, const strata_moe_experts* ex, const strat
     }
     *layer = decode_workspace((int32_t)T, ex->hidden, ex->n_expert, K, ex->ffn, ex->shared_gate != nullptr);
     *adapters = ad ? adapt_workspace(T, ad->rank, ad->in_dim) : 0;
+    return 0;
+}
+
+// ----------------- 4-bit floating-point products, norms around a block
+constexpr int64_t kBlockMaxRows = (int64_t)1 << 24;
+constexpr int64_t kMaxRowStride = (int64_t)1 << 32;
+
+int check_dtype(int32_t dtype) {
+    if (dtype != STRATA_MOE_F32 && dtype != STRATA_MOE_F16 && dtype != STRATA_MOE_BF16)
+        return fail(STRATA_MOE_EUNSUPPORTED, "unknown dtype %d", dtype);
+    return 0;
+}
+
+int check_rows(const char* what, int64_t rows) {
+    if (rows < 0 || rows > kBlockMaxRows)
+        return fail(STRATA_MOE_EINVAL, "%s = %lld outside [0, %lld]", what, (long long)rows, (long long)kBlockMaxRows);
+    return 0;
+}
+
+int check_stride(const char* what, int64_t stride, int64_t width) {
+    if (stride < width || stride > kMaxRowStride)
+        return fail(STRATA_MOE_EINVAL, "%s %lld below the width %lld or above 2^32", what, (long long)stride,
+                    (long long)width);
+    return 0;
+}
+
+int check_mxfp_cols(int32_t cols) {
+    if (cols < kBlock || cols > kMxMaxCols || cols % kBlock)
+        return fail(STRATA_MOE_EINVAL, "cols %d not a multiple of 32 in [32, %d]", cols, kMxMaxCols);
+    return 0;
+}
+
+int check_mxfp_matrix(int32_t rows, int32_t cols, int32_t swiglu) {
+    TRY(check_mxfp_cols(cols));
+    if (swiglu != 0 && swiglu != 1) return fail(STRATA_MOE_EINVAL, "swiglu %d is neither 0 nor 1", swiglu);
+    if (rows < 1 || rows > kMxMaxRows || (swiglu && rows % 2))
+        return fail(STRATA_MOE_EINVAL, "%d rows outside [1, %d], or odd with swiglu", rows, kMxMaxRows);
+    return 0;
+}
+
+int64_t mxfp_packed_bytes(int32_t rows, int32_t cols, int32_t swiglu) {
+    return round_up(mx_tiles(rows, swiglu != 0) * mx_tile_bytes(cols), 256);
+}
+
+// The size checks of a rounding call, and its arrays: float rows, codes, scales.
+int check_mxfp_rows(const void* v, int32_t dtype, int64_t stride, int64_t rows, int32_t cols, const uint8_t* codes,
+                    const uint8_t* scales) {
+    TRY(check_dtype(dtype));
+    TRY(check_mxfp_cols(cols));
+    TRY(check_rows("rows", rows));
+    if (rows * cols >= (int64_t)1 << 35)
+        return fail(STRATA_MOE_EINVAL, "rows * cols = %lld at or above 2^35", (long long)(rows * cols));
+    TRY(check_stride("row stride", stride, cols));
+    if (rows == 0) return 0;
+    if (!v || !codes || !scales) return fail(STRATA_MOE_EINVAL, "null rows / codes / scales");
+    if (!aligned(v, dtype_bytes(dtype)) || !aligned(codes, 16))
+        return fail(STRATA_MOE_EINVAL, "rows must be aligned to their element and codes to 16 bytes");
+    const RowSet r{(uintptr_t)v, rows, stride, cols, (int64_t)dtype_bytes(dtype)};
+    const uintptr_t nc = (uintptr_t)(rows * cols / 2), ns = (uintptr_t)(rows * cols / 32);
+    if (overlap(r.base, r.bytes(), (uintptr_t)codes, nc) || overlap(r.base, r.bytes(), (uintptr_t)scales, ns) ||
+        overlap((uintptr_t)codes, nc, (uintptr_t)scales, ns))
+        return fail(STRATA_MOE_EINVAL, "rows, codes and scales overlap");
+    return 0;
+}
+
+int check_norm(const char* what, const strata_moe_norm* n) {
+    if (!(n->eps >= 0.0) || n->eps > 1e30 || !(n->weight_offset > -1e30 && n->weight_offset < 1e30))
+        return fail(STRATA_MOE_EINVAL, "%s: eps must be finite and not negative, weight_offset finite", what);
+    if (n->weight && !aligned(n->weight, 4)) return fail(STRATA_MOE_EINVAL, "%s: weight must be 4-byte aligned", what);
+    return 0;
+}
+
+NormScale norm_scale(const strata_moe_norm* n) {
+    NormScale s{};
+    if (n) s = NormScale{n->weight, n->weight_offset, n->eps, 1};
+    return s;
+}
+
+// The checks both norm calls share: the stream's rows, and what the norm that
+// follows writes.
+int check_norm_rows(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H, const strata_moe_norm* n,
+                    const float* x, const uint8_t* codes, const uint8_t* scales) {
+    TRY(check_dtype(dtype));
+    TRY(check_rows("T", T));
+    if (H < 1 || H > kNormMaxH) return fail(STRATA_MOE_EINVAL, "H = %d outside [1, %d]", H, kNormMaxH);
+    TRY(check_stride("h_stride", h_stride, H));
+    if (n) {
+        TRY(check_norm("norm", n));
+        if (!x && !codes) return fail(STRATA_MOE_EINVAL, "a norm needs x, or codes and scales, to write");
+    } else if (x || codes || scales) {
+        return fail(STRATA_MOE_EINVAL, "x, codes and scales need a norm");
+    }
+    if ((codes == nullptr) != (scales == nullptr)) return fail(STRATA_MOE_EINVAL, "codes and scales come together");
+    if (codes && H % kBlock) return fail(STRATA_MOE_EINVAL, "codes need H = %d to be a multiple of 32", H);
+    if (T == 0) return 0;
+    if (!h) return fail(STRATA_MOE_EINVAL, "null h");
+    if (!aligned(h, dtype_bytes(dtype)) || !aligned(x, 4) || !aligned(codes, 16))
+        return fail(STRATA_MOE_EINVAL, "h and x must be aligned to their elements and codes to 16 bytes");
+    return 0;
+}
+
+// No two of the written arrays, and none of them and a read one, share an
+// element (a null array never does).
+int check_apart(const std::vector<RowSet>& written, const std::vector<RowSet>& read) {
+    for (size_t i = 0; i < written.size(); ++i) {
+        if (!written[i].base) continue;
+        for (size_t j = i + 1; j < written.size(); ++j)
+            if (written[j].base && overlap(written[i], written[j]))
+                return fail(STRATA_MOE_EINVAL, "two of the call's outputs overlap");
+        for (const RowSet& r : read)
+            if (r.base && overlap(written[i], r)) return fail(STRATA_MOE_EINVAL, "an output overlaps an input");
+    }
     return 0;
 }
 
@@ -1335,6 +1448,218 @@ int strata_moe_decode(const float* x, const float* router_w, const strata_moe_ex
         al.out_stride = experts->hidden;
         HIP_TRY(launch_adapt(al, (hipStream_t)stream), "adapter launch");
     }
+    return 0;
+}
+
+int strata_moe_mxfp_quantize(const void* x, int32_t dtype, int64_t x_stride, int64_t rows, int32_t cols,
+                             uint8_t* codes, uint8_t* scales, void* stream) {
+    g_err.clear();
+    TRY(check_mxfp_rows(x, dtype, x_stride, rows, cols, codes, scales));
+    if (rows == 0) return 0;
+    TRY(check_device());
+    HIP_TRY(launch_mx_quantize(x, dtype, x_stride, rows, cols, codes, scales, (hipStream_t)stream), "quantize launch");
+    return 0;
+}
+
+int strata_moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* out,
+                               int32_t dtype, int64_t out_stride, void* stream) {
+    g_err.clear();
+    TRY(check_mxfp_rows(out, dtype, out_stride, rows, cols, codes, scales));
+    if (rows == 0) return 0;
+    TRY(check_device());
+    HIP_TRY(launch_mx_dequantize(codes, scales, rows, cols, out, dtype, out_stride, (hipStream_t)stream),
+            "dequantize launch");
+    return 0;
+}
+
+int strata_moe_mxfp_packed_bytes(int32_t rows, int32_t cols, int32_t swiglu, int64_t* bytes) {
+    g_err.clear();
+    if (!bytes) return fail(STRATA_MOE_EINVAL, "bytes is NULL");
+    TRY(check_mxfp_matrix(rows, cols, swiglu));
+    *bytes = mxfp_packed_bytes(rows, cols, swiglu);
+    return 0;
+}
+
+int strata_moe_mxfp_pack(const uint8_t* codes, const uint8_t* scales, int32_t e0, int32_t e1, int32_t rows,
+                         int32_t cols, int32_t swiglu, void* packed, int64_t stride, void* stream) {
+    g_err.clear();
+    TRY(check_mxfp_matrix(rows, cols, swiglu));
+    if (e0 < 0 || e1 < e0 || e1 > kMaxExperts)
+        return fail(STRATA_MOE_EINVAL, "experts [%d, %d) outside [0, %d)", e0, e1, kMaxExperts);
+    const int64_t need = mxfp_packed_bytes(rows, cols, swiglu);
+    if (stride < need || stride % 256)
+        return fail(STRATA_MOE_EINVAL, "stride %lld below %lld or not a multiple of 256", (long long)stride,
+                    (long long)need);
+    if (e0 == e1) return 0;
+    if (!codes || !scales || !packed) return fail(STRATA_MOE_EINVAL, "null codes / scales / packed");
+    if (!aligned(codes, 16) || !aligned(packed, 256))
+        return fail(STRATA_MOE_EINVAL, "codes must be 16-byte and packed 256-byte aligned");
+    const int64_t values = (int64_t)(e1 - e0) * rows * cols;
+    uint8_t* to = (uint8_t*)packed + e0 * stride;
+    const uintptr_t n = (uintptr_t)((e1 - e0 - 1) * stride + need);
+    if (overlap((uintptr_t)to, n, (uintptr_t)codes, (uintptr_t)(values / 2)) ||
+        overlap((uintptr_t)to, n, (uintptr_t)scales, (uintptr_t)(values / 32)))
+        return fail(STRATA_MOE_EINVAL, "packed overlaps codes or scales");
+    TRY(check_device());
+    HIP_TRY(launch_mx_pack(codes, scales, e1 - e0, rows, cols, swiglu != 0, to, stride, (hipStream_t)stream),
+            "pack launch");
+    return 0;
+}
+
+int strata_moe_mxfp_product(const uint8_t* codes, const uint8_t* scales, int64_t x_rows,
+                            const strata_moe_mxfp_weights* weights, const int32_t* offsets, const int32_t* src,
+                            int64_t rows, void* out, int32_t dtype, int64_t out_stride, void* stream) {
+    g_err.clear();
+    if (!weights) return fail(STRATA_MOE_EINVAL, "weights is NULL");
+    const strata_moe_mxfp_weights& w = *weights;
+    TRY(check_mxfp_matrix(w.rows, w.cols, w.swiglu));
+    TRY(check_dtype(dtype));
+    if (w.n_expert < 1 || w.n_expert > kMaxExperts)
+        return fail(STRATA_MOE_EINVAL, "n_expert %d outside [1, %d]", w.n_expert, kMaxExperts);
+    const int64_t need = mxfp_packed_bytes(w.rows, w.cols, w.swiglu);
+    if (w.stride < need || w.stride % 256)
+        return fail(STRATA_MOE_EINVAL, "stride %lld below %lld or not a multiple of 256", (long long)w.stride,
+                    (long long)need);
+    TRY(check_rows("rows", rows));
+    TRY(check_rows("x_rows", x_rows));
+    const int32_t n_out = w.swiglu ? w.rows / 2 : w.rows;
+    TRY(check_stride("out_stride", out_stride, n_out));
+    if (!offsets && w.n_expert != 1)
+        return fail(STRATA_MOE_EINVAL, "%d experts need offsets", w.n_expert);
+    if (!src && x_rows < rows)
+        return fail(STRATA_MOE_EINVAL, "%lld rows of %lld without src", (long long)rows, (long long)x_rows);
+    if (x_rows * w.cols >= (int64_t)1 << 33)
+        return fail(STRATA_MOE_EINVAL, "x_rows * cols = %lld at or above 2^33", (long long)(x_rows * w.cols));
+    if (rows == 0) return 0;
+    if (!codes || !scales || !w.packed || !out || x_rows == 0)
+        return fail(STRATA_MOE_EINVAL, "null codes / scales / packed / out, or no x rows");
+    if (!aligned(codes, 16) || !aligned(w.packed, 256) || !aligned(offsets, 4) || !aligned(src, 4) ||
+        !aligned(out, dtype_bytes(dtype)))
+        return fail(STRATA_MOE_EINVAL, "codes must be 16-byte and packed 256-byte aligned, the rest to its element");
+    const RowSet ro{(uintptr_t)out, rows, out_stride, n_out, (int64_t)dtype_bytes(dtype)};
+    const struct {
+        const void* p;
+        int64_t bytes;
+    } read[] = {{codes, x_rows * w.cols / 2}, {scales, x_rows * w.cols / 32},
+                {w.packed, (w.n_expert - 1) * w.stride + need}, {offsets, offsets ? 4 * (w.n_expert + 1) : 0},
+                {src, src ? 4 * rows : 0}};
+    for (const auto& r : read)
+        if (r.bytes && overlap(ro.base, ro.bytes(), (uintptr_t)r.p, (uintptr_t)r.bytes))
+            return fail(STRATA_MOE_EINVAL, "out overlaps an input");
+    TRY(check_device());
+    MxProduct p{};
+    p.codes = codes;
+    p.scales = scales;
+    p.x_rows = x_rows;
+    p.packed = (const uint8_t*)w.packed;
+    p.stride = w.stride;
+    p.E = w.n_expert;
+    p.n = w.rows;
+    p.cols = w.cols;
+    p.paired = w.swiglu;
+    p.offsets = offsets;
+    p.src = src;
+    p.rows = rows;
+    p.out = out;
+    p.dtype = dtype;
+    p.out_stride = out_stride;
+    HIP_TRY(launch_mx_product(p, (hipStream_t)stream), "product launch");
+    return 0;
+}
+
+int strata_moe_norm_before(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H,
+                           const strata_moe_norm* norm, float* x, uint8_t* codes, uint8_t* scales, void* stream) {
+    g_err.clear();
+    if (!norm) return fail(STRATA_MOE_EINVAL, "norm is NULL");
+    TRY(check_norm_rows(h, dtype, h_stride, T, H, norm, x, codes, scales));
+    if (T == 0) return 0;
+    const RowSet rh{(uintptr_t)h, T, h_stride, H, (int64_t)dtype_bytes(dtype)}, rw{(uintptr_t)norm->weight, 1, H, H};
+    TRY(check_apart({{(uintptr_t)x, T, H, H}, {(uintptr_t)codes, T, H / 2, H / 2, 1},
+                     {(uintptr_t)scales, T, H / 32, H / 32, 1}}, {rh, rw}));
+    TRY(check_device());
+    NormLaunch l{};
+    l.T = T;
+    l.H = H;
+    l.dtype = dtype;
+    l.h = h;
+    l.h_stride = h_stride;
+    l.before = norm_scale(norm);
+    l.x = x;
+    l.codes = codes;
+    l.scales = scales;
+    HIP_TRY(launch_norm(l, (hipStream_t)stream), "norm launch");
+    return 0;
+}
+
+int strata_moe_norm_after(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H,
+                          const strata_moe_branch* branch, void* out, int64_t out_stride,
+                          const strata_moe_norm* next, float* x, uint8_t* codes, uint8_t* scales, void* stream) {
+    g_err.clear();
+    if (!branch) return fail(STRATA_MOE_EINVAL, "branch is NULL");
+    const strata_moe_branch& b = *branch;
+    TRY(check_norm_rows(h, dtype, h_stride, T, H, next, x, codes, scales));
+    TRY(check_dtype(b.y_dtype));
+    TRY(check_stride("y_stride", b.y_stride, H));
+    TRY(check_stride("out_stride", out_stride, H));
+    TRY(check_rows("y_rows", b.y_rows));
+    if ((b.slot == nullptr) != (b.p == nullptr)) return fail(STRATA_MOE_EINVAL, "slot and p come together");
+    if (b.slot ? (b.K < 1 || b.K > kMaxTopK) : b.K != 0)
+        return fail(STRATA_MOE_EINVAL, "K = %d outside [1, %d] with slot, or not 0 without", b.K, kMaxTopK);
+    if (!b.slot && b.y_rows < T)
+        return fail(STRATA_MOE_EINVAL, "%lld rows of y for %lld tokens", (long long)b.y_rows, (long long)T);
+    if (b.norm) TRY(check_norm("norm after", b.norm));
+    if (!(b.residual_scale > -1e30 && b.residual_scale < 1e30) || !(b.block_scale > -1e30 && b.block_scale < 1e30))
+        return fail(STRATA_MOE_EINVAL, "residual_scale and block_scale must be finite");
+    if (b.gate && ((b.gate_col_stride != 0 && b.gate_col_stride != 1) || b.gate_row_stride < 0 ||
+                   b.gate_row_stride > kMaxRowStride))
+        return fail(STRATA_MOE_EINVAL, "gate strides (%lld, %d): columns 0 or 1, rows in [0, 2^32]",
+                    (long long)b.gate_row_stride, b.gate_col_stride);
+    if (T == 0) return 0;
+    if (!out || (!b.y && b.y_rows)) return fail(STRATA_MOE_EINVAL, "null out / y");
+    if (!b.y_rows) return fail(STRATA_MOE_EINVAL, "no rows of y");
+    if (!aligned(out, dtype_bytes(dtype)) || !aligned(b.y, dtype_bytes(b.y_dtype)) || !aligned(b.slot, 4) ||
+        !aligned(b.p, 4) || !aligned(b.gate, 4))
+        return fail(STRATA_MOE_EINVAL, "out, y, slot, p and gate must be aligned to their elements");
+    const int64_t el = (int64_t)dtype_bytes(dtype);
+    const RowSet rh{(uintptr_t)h, T, h_stride, H, el}, ro{(uintptr_t)out, T, out_stride, H, el};
+    const RowSet ry{(uintptr_t)b.y, b.y_rows, b.y_stride, H, (int64_t)dtype_bytes(b.y_dtype)};
+    const RowSet rs{(uintptr_t)b.slot, T, b.K, b.K}, rp{(uintptr_t)b.p, T, b.K, b.K};
+    const RowSet rw{(uintptr_t)(b.norm ? b.norm->weight : nullptr), 1, H, H};
+    const RowSet ru{(uintptr_t)(next ? next->weight : nullptr), 1, H, H};
+    const RowSet rg{(uintptr_t)b.gate, 1, 0, (T - 1) * b.gate_row_stride + (H - 1) * b.gate_col_stride + 1};
+    const RowSet rx{(uintptr_t)x, T, H, H}, rc{(uintptr_t)codes, T, H / 2, H / 2, 1},
+        rb{(uintptr_t)scales, T, H / 32, H / 32, 1};
+    TRY(check_apart({ro, rx, rc, rb}, {ry, rs, rp, rw, ru, rg}));
+    TRY(check_apart({rx, rc, rb}, {rh}));
+    if (!(out == h && out_stride == h_stride) && overlap(ro, rh))
+        return fail(STRATA_MOE_EINVAL, "out overlaps h without being h");
+    TRY(check_device());
+    NormLaunch l{};
+    l.T = T;
+    l.H = H;
+    l.dtype = dtype;
+    l.h = h;
+    l.h_stride = h_stride;
+    l.y = b.y;
+    l.y_dtype = b.y_dtype;
+    l.y_stride = b.y_stride;
+    l.y_rows = b.y_rows;
+    l.slot = b.slot;
+    l.p = b.p;
+    l.K = b.K;
+    l.after = norm_scale(b.norm);
+    l.gate = b.gate;
+    l.gate_row_stride = b.gate_row_stride;
+    l.gate_col_stride = b.gate_col_stride;
+    l.residual_scale = b.residual_scale;
+    l.block_scale = b.block_scale;
+    l.out = out;
+    l.out_stride = out_stride;
+    l.before = norm_scale(next);
+    l.x = x;
+    l.codes = codes;
+    l.scales = scales;
+    HIP_TRY(launch_norm(l, (hipStream_t)stream), "norm launch");
     return 0;
 }
 

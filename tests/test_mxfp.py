@@ -1,0 +1,467 @@
+"""Microscaled 4-bit floating point (strata_moe_mxfp_*) against its definition in
+64 bits: rounding and packing bit for bit, products within the tolerance that
+mxfp_reference.product derives, plus half a step of the output's type."""
+import ctypes
+
+import mxfp_reference as ref
+import numpy as np
+import pytest
+import torch
+
+DTYPES = [torch.float32, torch.float16, torch.bfloat16]
+IDS = ["fp32", "fp16", "bf16"]
+
+
+@pytest.fixture(scope="module")
+def qm():
+    import quantized_routed_expert_logits_amd as qm
+    return qm
+
+
+def _np(t):
+    return t.double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+# ------------------------------------------------------------------ rounding
+def _check_quantize(qm, x):
+    codes, scales = qm.strata_moe_mxfp_quantize(x)
+    want, byte = ref.quantize(_np(x))
+    assert np.array_equal(_np(scales), byte)
+    assert np.array_equal(_np(codes), ref.pack(want))
+    return codes, scales
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("rows,cols,pad", [(1, 32, 0), (1, 2560, 0), (3, 64, 1), (7, 96, 8), (33, 1056, 3), (130, 544, 0),
+                                           (1025, 32, 5), (2, 65536, 0), (600, 2560, 0)])
+def test_quantize(qm, rows, cols, pad, dtype):
+    g = torch.Generator().manual_seed(rows + cols)
+    x = torch.randn((rows, cols + pad), generator=g) * torch.exp2(torch.randint(-9, 6, (rows, 1), generator=g).float())
+    x = x.to(dtype).cuda()[:, :cols]
+    codes, scales = _check_quantize(qm, x)
+    for dt in DTYPES:  # read back, into padded rows
+        buf = torch.full((rows, cols + 3), 7.0, dtype=dt, device="cuda")
+        out = qm.strata_moe_mxfp_dequantize(codes, scales, buf[:, :cols])
+        v = ref.values(ref.unpack(_np(codes)), _np(scales))
+        assert torch.equal(out.cpu(), torch.from_numpy(v).to(dt))
+        assert torch.all(buf[:, cols:] == 7.0)
+
+
+@pytest.mark.gpu
+def test_quantize_every_border(qm):
+    """Values on, just above and just below every border between two codes, in
+    blocks whose largest value spans all exponents."""
+    marks = np.array([0.0, 0.25, 0.5, 0.75, 1.0, 1.25, 1.5, 1.75, 2.0, 2.5, 3.0, 3.5, 4.0, 5.0, 6.0, 7.0, 7.9999995],
+                     np.float32)
+    near = np.concatenate([marks, np.nextafter(marks, np.float32(9)), np.nextafter(marks, np.float32(-9))])
+    near = np.concatenate([near, -near])
+    rows = []
+    for e in list(range(-149, -120)) + [-60, -1, 0, 1, 77, 123, 125]:
+        with np.errstate(over="ignore", under="ignore"):
+            v = (near.astype(np.float64) * 2.0 ** e).astype(np.float32)
+            top = np.float32(7.0 * 2.0 ** e)
+        v = v[np.abs(v) <= max(top, np.float32(2.0 ** -149))]
+        for i in range(0, len(v), 31):
+            block = np.zeros(32, np.float32)
+            block[:len(v[i:i + 31])] = v[i:i + 31]
+            block[31] = top
+            rows.append(block)
+    x = torch.from_numpy(np.stack(rows)).cuda()
+    assert torch.isfinite(x).all()
+    _check_quantize(qm, x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_quantize_infinities_and_nan_stay_in_their_block(qm, dtype):
+    x = torch.randn((4, 128), generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    x[0, 5], x[1, 40], x[2, 127] = float("inf"), float("nan"), -float("inf")
+    x[3] = 0.0
+    codes, scales = _check_quantize(qm, x)
+    v = qm.strata_moe_mxfp_dequantize(codes, scales, torch.empty_like(x))
+    nan = torch.isnan(v)
+    assert nan.sum() == 96 and nan[0, :32].all() and nan[1, 32:64].all() and nan[2, 96:].all()
+
+
+# ------------------------------------------------------------------- product
+def _operands(rows, cols, n, E, seed, spread=6):
+    g = torch.Generator().manual_seed(seed)
+    xc = torch.randint(0, 256, (rows, cols // 2), generator=g, dtype=torch.uint8)
+    xs = torch.randint(127 - spread, 127 + spread, (rows, cols // 32), generator=g, dtype=torch.uint8)
+    wc = torch.randint(0, 256, (E, n, cols // 2), generator=g, dtype=torch.uint8)
+    ws = torch.randint(120 - spread, 120 + spread, (E, n, cols // 32), generator=g, dtype=torch.uint8)
+    return xc.cuda(), xs.cuda(), wc.cuda(), ws.cuda()
+
+
+def _offsets(E, rows, seed, how="random"):
+    g = np.random.default_rng(seed)
+    if how == "one":  # all rows to one expert in the middle
+        n = np.zeros(E, np.int64)
+        n[E // 2] = rows
+    elif how == "hot":  # half of the rows to the last expert
+        n = np.bincount(np.where(g.random(rows) < 0.5, E - 1, g.integers(0, E, rows)), minlength=E)
+    else:
+        n = np.bincount(g.integers(0, E, rows), minlength=E)
+    return torch.from_numpy(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)).cuda()
+
+
+def _check_product(qm, xc, xs, wc, ws, out, swiglu=False, offsets=None, src=None, weights=None, only=None):
+    """out (given, holds what an untouched element keeps) after the call, against the definition."""
+    before = _np(out)
+    E, n, _ = wc.shape
+    if weights is None:
+        weights = qm.MxfpWeights(E, n, xc.shape[1] * 2, swiglu=swiglu).pack(0, wc, ws)
+    qm.strata_moe_mxfp_product(xc, xs, weights, out, offsets=offsets, src=src)
+    got, dt = _np(out), torch.finfo(out.dtype)
+    x = ref.values(ref.unpack(_np(xc)), _np(xs))
+    rows = np.arange(out.shape[0]) if src is None else _np(src)
+    cuts = [0, out.shape[0]] if offsets is None else _np(offsets)
+    want, tol, written = before.copy(), np.zeros_like(got), np.zeros(out.shape[0], bool)
+    for e in range(E) if only is None else only:
+        r = np.arange(cuts[e], cuts[e + 1])
+        if len(r) == 0:
+            continue
+        xe = np.where(((rows[r] >= 0) & (rows[r] < len(x)))[:, None], x[np.clip(rows[r], 0, len(x) - 1)], 0.0)
+        w = ref.values(ref.unpack(_np(wc[e])), _np(ws[e]))
+        want[r], t = ref.product(xe, w, swiglu)
+        tol[r] = t + ref.rounding(dt.eps, dt.smallest_normal * dt.eps, np.abs(want[r]) + t)
+        written[r] = True
+    if only is None:
+        assert np.array_equal(got[~written], before[~written]), "a row of no expert changed"
+    err = np.abs(got - want)[written]
+    # rounding to nearest gives infinity from the largest value and half a step on: half a step is
+    # eps / 2 of that value's power of two, (2 - eps) of which is the largest value
+    border = dt.max * (1.0 + dt.eps / 2 / (2.0 - dt.eps))
+    over = np.isinf(got) & (np.abs(want) + tol >= border) & (np.sign(got) == np.sign(want))
+    bad = ~((err <= tol[written]) | over[written])
+    worst = np.nanmax(np.where(over[written], 0.0, err) / np.maximum(tol[written], 1e-300))
+    assert not bad.any(), f"{bad.sum()} outputs off, worst {worst:.2f} of the tolerance"
+
+
+DENSE = [  # rows, cols, n
+    (1, 32, 1), (1, 2560, 2560), (2, 64, 15), (5, 96, 17), (16, 128, 64), (17, 544, 333), (31, 640, 65), (64, 1024, 100),
+    (65, 512, 256), (128, 160, 257), (129, 1056, 128), (200, 2560, 320), (300, 4096, 96), (3, 65536, 20),
+    (2, 32, 65536), (1000, 96, 70), (2049, 512, 130),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("size", DENSE, ids=lambda s: "-".join(map(str, s)))
+def test_product_of_one_matrix(qm, size, dtype):
+    rows, cols, n = size
+    xc, xs, wc, ws = _operands(rows, cols, n, 1, seed=rows + n)
+    buf = torch.full((rows, n + 3), 7.0, dtype=dtype, device="cuda")
+    _check_product(qm, xc, xs, wc, ws, buf[:, :n])
+    assert torch.all(buf[:, n:] == 7.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("size", [(1, 32, 2), (1, 2560, 2048), (9, 96, 30), (17, 544, 34), (130, 640, 512), (257, 512, 666)],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_swiglu_of_one_matrix(qm, size, dtype):
+    rows, cols, n = size
+    # large scales: gates on both sides of where the exponential overflows
+    xc, xs, wc, ws = _operands(rows, cols, n, 1, seed=rows + n, spread=3)
+    buf = torch.full((rows, n // 2 + 1), 7.0, dtype=dtype, device="cuda")
+    _check_product(qm, xc, xs, wc, ws, buf[:, :n // 2], swiglu=True)
+    assert torch.all(buf[:, n // 2:] == 7.0)
+
+
+GROUPED = [  # rows, x rows (0: no src), cols, n, E, how, swiglu
+    (1, 1, 96, 32, 512, "random", True), (10, 1, 2560, 128, 512, "random", True), (10, 0, 1024, 80, 512, "random", False),
+    (64, 20, 160, 33, 7, "random", False), (406, 203, 544, 333, 6, "random", False), (300, 30, 640, 64, 1024, "random", True),
+    (320, 32, 256, 96, 512, "random", False), (1000, 100, 128, 48, 40, "hot", True), (777, 0, 96, 20, 5, "one", False),
+    (2000, 500, 512, 260, 16, "random", True), (1500, 0, 672, 300, 9, "hot", False), (4000, 400, 96, 16, 1024, "hot", False),
+    (520, 52, 64, 40, 3, "one", True), (33, 33, 2560, 64, 2, "random", False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", GROUPED, ids=lambda s: "-".join(map(str, s)))
+def test_product_by_expert(qm, size):
+    rows, x_rows, cols, n, E, how, swiglu = size
+    xc, xs, wc, ws = _operands(x_rows or rows, cols, n, E, seed=rows)
+    src = torch.randint(0, x_rows, (rows,), generator=torch.Generator().manual_seed(3)).int().cuda() if x_rows else None
+    for dtype in DTYPES:
+        out = torch.full((rows, n // 2 if swiglu else n), 7.0, dtype=dtype, device="cuda")
+        _check_product(qm, xc, xs, wc, ws, out, swiglu=swiglu, offsets=_offsets(E, rows, rows, how), src=src)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [40, 900])
+def test_rows_of_no_expert_are_left(qm, rows):
+    xc, xs, wc, ws = _operands(rows, 96, 40, 4, seed=1)
+    off = torch.tensor([7, 7, 19, 19, rows - 5], dtype=torch.int32, device="cuda")
+    _check_product(qm, xc, xs, wc, ws, torch.full((rows, 40), 7.0, device="cuda"), offsets=off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [30, 700])
+def test_src_outside_x_counts_as_zeros(qm, rows):
+    xc, xs, wc, ws = _operands(9, 160, 50, 3, seed=2)
+    src = torch.randint(-3, 12, (rows,), generator=torch.Generator().manual_seed(0)).int()
+    src[0], src[1], src[2] = -2 ** 31, 2 ** 31 - 1, 9
+    out = torch.full((rows, 50), 7.0, device="cuda")
+    _check_product(qm, xc, xs, wc, ws, out, offsets=_offsets(3, rows, 5), src=src.cuda())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [20, 400])
+def test_offsets_of_any_value_stay_in_the_arrays(qm, rows):
+    """Offsets that fall, are negative or lie past the rows: nothing outside out
+    is written, and an expert whose range is in order gets its rows."""
+    xc, xs, wc, ws = _operands(rows, 64, 24, 5, seed=3)
+    w = qm.MxfpWeights(5, 24, 64).pack(0, wc, ws)
+    buf = torch.full((rows + 64, 24), 7.0, device="cuda")
+    off = torch.tensor([-2 ** 31, 4, 2, 2 ** 31 - 1, -7, 3], dtype=torch.int32, device="cuda")
+    qm.strata_moe_mxfp_product(xc, xs, w, buf[:rows], offsets=off)
+    assert torch.all(buf[rows:] == 7.0)
+    x = ref.values(ref.unpack(_np(xc)), _np(xs))
+    want, tol = ref.product(x[5:], ref.values(ref.unpack(_np(wc[2])), _np(ws[2])), False)  # rows 5.. are expert 2's alone
+    assert np.all(np.abs(_np(buf[5:rows]) - want) <= tol + 2.0 ** -24 * np.abs(want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [12, 300])
+def test_nan_stays_in_its_row_and_output(qm, rows):
+    xc, xs, wc, ws = _operands(rows, 256, 48, 1, seed=4)
+    xs[3, 7], ws[0, 20, 1] = 255, 255
+    out = torch.empty((rows, 48), device="cuda")
+    qm.strata_moe_mxfp_product(xc, xs, qm.MxfpWeights(1, 48, 256).pack(0, wc, ws), out)
+    want = torch.zeros((rows, 48), dtype=torch.bool, device="cuda")
+    want[3], want[:, 20] = True, True
+    assert torch.equal(torch.isnan(out), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [5, 140])
+def test_a_row_s_result_does_not_depend_on_its_neighbours(qm, rows):
+    """The padding of a step and of a tile reads nothing: the same row beside NaN
+    rows and before the end of the array."""
+    xc, xs, wc, ws = _operands(rows, 544, 70, 1, seed=5)
+    w = qm.MxfpWeights(1, 70, 544).pack(0, wc, ws)
+    out = qm.strata_moe_mxfp_product(xc, xs, w, torch.empty((rows, 70), device="cuda"))
+    xs2 = xs.clone()
+    xs2[1::2] = 255
+    out2 = qm.strata_moe_mxfp_product(xc, xs2, w, torch.empty((rows, 70), device="cuda"))
+    assert torch.equal(out[0::2], out2[0::2]) and torch.isnan(out2[1::2]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,n_e", [(3, 1), (50, 8), (3000, 8)])
+def test_repeated_calls_give_the_same_bits(qm, rows, n_e):
+    xc, xs, wc, ws = _operands(rows, 640, 200, n_e, seed=6)
+    w = qm.MxfpWeights(n_e, 200, 640, swiglu=True).pack(0, wc, ws)
+    off = None if n_e == 1 else _offsets(n_e, rows, 1)
+    outs = [qm.strata_moe_mxfp_product(xc, xs, w, torch.empty((rows, 100), device="cuda"), offsets=off) for _ in range(3)]
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [6, 600])
+def test_graph_and_streams(qm, rows):
+    """Captured with the rounding before it and replayed with new inputs, beside
+    the same call on another stream."""
+    g = torch.Generator().manual_seed(7)
+    E, cols, n = 5, 672, 96
+    _, _, wc, ws = _operands(1, cols, n, E, seed=8)
+    w = qm.MxfpWeights(E, n, cols).pack(0, wc, ws)
+    off = _offsets(E, rows, 2)
+    x = torch.randn((rows, cols), generator=g).cuda()
+    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device="cuda")
+    out = torch.empty((rows, n), device="cuda")
+
+    def call(stream=None):
+        qm.strata_moe_mxfp_quantize(x, codes, scales, stream=stream)
+        qm.strata_moe_mxfp_product(codes, scales, w, out, offsets=off, stream=stream)
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    side = torch.cuda.Stream()
+    for i in range(4):
+        x.copy_(torch.randn((rows, cols), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        c2, s2 = qm.strata_moe_mxfp_quantize(x)
+        eager = qm.strata_moe_mxfp_product(c2, s2, w, torch.empty_like(out), offsets=off)
+        side.wait_stream(torch.cuda.current_stream())
+        other = torch.empty_like(out)
+        c3, s3 = qm.strata_moe_mxfp_quantize(x, stream=side)
+        qm.strata_moe_mxfp_product(c3, s3, w, other, offsets=off, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.equal(out, other)
+
+
+@pytest.mark.gpu
+def test_weights_and_outputs_past_32_bits(qm):
+    E, n, cols = 900, 4096, 2560  # 5 GB of packed weights
+    g = torch.Generator(device="cuda").manual_seed(9)
+    w = qm.MxfpWeights(E, n, cols)
+    wc = torch.randint(0, 256, (E, n, cols // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(114, 126, (E, n, cols // 32), generator=g, device="cuda", dtype=torch.uint8)
+    w.pack(0, wc, ws)
+    assert w.packed.numel() > 1 << 32
+    xc, xs, _, _ = _operands(6, cols, 1, 1, seed=10)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:], off[500:], off[900:] = 1, 3, 6  # experts 0, 499 and 899
+    _check_product(qm, xc, xs, wc, ws, torch.empty((6, n), device="cuda"), offsets=off.cuda(), weights=w,
+                   only=[0, 499, 899])
+    del wc, ws, w
+    rows = 1100000  # 4.5e9 outputs
+    xc, xs, wc, ws = _operands(64, 32, n, 1, seed=11)
+    src = (torch.arange(rows, device="cuda") % 64).int()
+    out = torch.empty((rows, n), dtype=torch.bfloat16, device="cuda")
+    qm.strata_moe_mxfp_product(xc, xs, qm.MxfpWeights(1, n, 32).pack(0, wc, ws), out, src=src)
+    first = torch.empty((64, n), dtype=torch.bfloat16, device="cuda")
+    _check_product(qm, xc, xs, wc, ws, first)
+    for r0 in (0, 524288, 1048512, rows - rows % 64 - 64):
+        assert torch.equal(out[r0:r0 + 64], first)
+    assert torch.equal(out[rows - rows % 64:], first[:rows % 64])
+
+
+# ------------------------------------------------------------------ refusals
+PTR = 1 << 20
+
+
+def _refused(qm, rc, code):
+    assert rc == code and qm.strata_moe_last_error()
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(rows=-1), -1), (dict(rows=(1 << 24) + 1), -1), (dict(cols=0), -1), (dict(cols=48), -1), (dict(cols=65568), -1),
+    (dict(dtype=0), -2), (dict(dtype=4), -2), (dict(x_stride=63), -1), (dict(x_stride=(1 << 32) + 1), -1),
+    (dict(x=None), -1), (dict(codes=None), -1), (dict(scales=None), -1), (dict(x=PTR + 2), -1), (dict(codes=(2 << 20) + 8), -1),
+    (dict(rows=1 << 24, cols=65536, x_stride=65536), -1), (dict(codes=PTR + 256), -1), (dict(scales=PTR + 1), -1),
+    (dict(scales=(2 << 20) + 5), -1),
+], ids=str)
+def test_rounding_refuses(qm, change, code):
+    a = dict(x=PTR, dtype=1, x_stride=64, rows=8, cols=64, codes=2 << 20, scales=3 << 20)
+    a.update(change)
+    lib = qm.library()
+    _refused(qm, lib.strata_moe_mxfp_quantize(a["x"], a["dtype"], a["x_stride"], a["rows"], a["cols"], a["codes"],
+                                              a["scales"], None), code)
+    _refused(qm, lib.strata_moe_mxfp_dequantize(a["codes"], a["scales"], a["rows"], a["cols"], a["x"], a["dtype"],
+                                                a["x_stride"], None), code)
+
+
+def test_no_rows_is_a_no_op(qm):
+    lib = qm.library()
+    assert lib.strata_moe_mxfp_quantize(None, 1, 64, 0, 64, None, None, None) == 0
+    assert lib.strata_moe_mxfp_dequantize(None, None, 0, 64, None, 2, 64, None) == 0
+    st = qm.MxfpWeightsStruct(1, 8, 64, 0, None, 4096)
+    assert lib.strata_moe_mxfp_product(None, None, 0, ctypes.byref(st), None, None, 0, None, 1, 8, None) == 0
+
+
+@pytest.mark.parametrize("rows,cols,swiglu", [(0, 64, 0), (65537, 64, 0), (7, 64, 1), (8, 40, 0), (8, 0, 0), (8, 64, 2)])
+def test_packed_bytes_refuses(qm, rows, cols, swiglu):
+    b = ctypes.c_int64()
+    _refused(qm, qm.library().strata_moe_mxfp_packed_bytes(rows, cols, swiglu, ctypes.byref(b)), -1)
+
+
+def test_packed_bytes(qm):
+    # a multiple of 16 rows and 512 columns is held in 4.25 bits a value
+    assert qm.strata_moe_mxfp_packed_bytes(2048, 2560, True) == 2048 * 2560 * 17 // 32
+    assert qm.strata_moe_mxfp_packed_bytes(1, 32) == 1024 + 256
+    _refused(qm, qm.library().strata_moe_mxfp_packed_bytes(8, 64, 0, None), -1)
+
+
+@pytest.mark.parametrize("change", [
+    dict(e0=-1), dict(e0=3, e1=2), dict(e1=1025), dict(stride=1024), dict(stride=1300), dict(codes=None), dict(scales=None),
+    dict(packed=None), dict(codes=PTR + 8), dict(packed=(8 << 20) + 128), dict(codes=8 << 20), dict(scales=(8 << 20) + 2600),
+    dict(rows=0), dict(cols=33),
+], ids=str)
+def test_pack_refuses(qm, change):
+    a = dict(codes=PTR, scales=2 << 20, e0=0, e1=4, rows=8, cols=64, swiglu=0, packed=8 << 20, stride=1280)
+    a.update(change)
+    _refused(qm, qm.library().strata_moe_mxfp_pack(*a.values(), None), -1)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(weights=None), -1), (dict(E=0), -1), (dict(E=1025), -1), (dict(n=0), -1), (dict(cols=72), -1), (dict(swiglu=3), -1),
+    (dict(n=7, swiglu=1), -1), (dict(stride=1024), -1), (dict(stride=1281), -1), (dict(rows=-1), -1),
+    (dict(rows=(1 << 24) + 1), -1), (dict(x_rows=-1), -1), (dict(x_rows=(1 << 24) + 1, src=7 << 20), -1),
+    (dict(dtype=9), -2), (dict(out_stride=7), -1), (dict(offsets=None), -1), (dict(rows=21), -1), (dict(x_rows=0, src=7 << 20), -1),
+    (dict(x_rows=1 << 24, cols=512, stride=5120, src=7 << 20), -1), (dict(codes=None), -1), (dict(scales=None), -1),
+    (dict(packed=None), -1), (dict(out=None), -1), (dict(codes=PTR + 4), -1), (dict(packed=(3 << 20) + 64), -1),
+    (dict(offsets=(5 << 20) + 2), -1), (dict(src=(7 << 20) + 1), -1), (dict(out=(6 << 20) + 2), -1), (dict(out=PTR + 32), -1),
+    (dict(out=3 << 20), -1), (dict(out=(5 << 20) - 4), -1), (dict(out=(2 << 20) + 4), -1), (dict(src=6 << 20), -1),
+], ids=str)
+def test_product_refuses(qm, change, code):
+    a = dict(codes=PTR, scales=2 << 20, x_rows=20, E=4, n=8, cols=64, swiglu=0, packed=3 << 20, stride=1280, offsets=5 << 20,
+             src=None, rows=20, out=6 << 20, dtype=1, out_stride=8, weights=True)
+    a.update(change)
+    st = qm.MxfpWeightsStruct(a["E"], a["n"], a["cols"], a["swiglu"], a["packed"], a["stride"])
+    _refused(qm, qm.library().strata_moe_mxfp_product(
+        a["codes"], a["scales"], a["x_rows"], ctypes.byref(st) if a["weights"] else None, a["offsets"], a["src"], a["rows"],
+        a["out"], a["dtype"], a["out_stride"], None), code)
+
+
+def test_the_binding_checks_its_tensors(qm):
+    x = torch.zeros((4, 64))
+    with pytest.raises(TypeError):
+        qm.strata_moe_mxfp_quantize(x)                      # not on the GPU
+    with pytest.raises(TypeError):
+        qm.strata_moe_mxfp_quantize(x.int())
+    with pytest.raises(ValueError):
+        qm.strata_moe_mxfp_quantize(x[0])
+    with pytest.raises(ValueError):
+        qm.strata_moe_mxfp_quantize(x.t())
+    with pytest.raises(ValueError):
+        qm.strata_moe_mxfp_quantize(torch.zeros(1, 64).expand(4, 64))
+    codes, scales = torch.zeros((4, 32), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        qm.strata_moe_mxfp_dequantize(codes.int(), scales, x)
+    with pytest.raises(ValueError):
+        qm.strata_moe_mxfp_dequantize(codes[:3], scales, x)
+    with pytest.raises(ValueError):
+        qm.strata_moe_mxfp_dequantize(codes, scales[:, :1], x)
+    with pytest.raises(ValueError):
+        qm.MxfpWeights(0, 8, 64, device="cpu")
+    with pytest.raises(qm.StrataMoeError):
+        qm.MxfpWeights(1, 8, 65, device="cpu")
+    w = qm.MxfpWeights(2, 8, 64, device="cpu")
+    wc, ws = torch.zeros((2, 8, 32), dtype=torch.uint8), torch.zeros((2, 8, 2), dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        w.pack(0, wc, ws)                                   # not on the GPU
+    with pytest.raises(ValueError):
+        w.pack(0, wc[:, :4], ws)
+    out = torch.zeros((4, 8))
+    with pytest.raises(TypeError):
+        qm.strata_moe_mxfp_product(codes, scales, None, out)
+    with pytest.raises(ValueError):
+        qm.strata_moe_mxfp_product(codes, scales, w, out[:, :7])
+    with pytest.raises(ValueError):
+        qm.strata_moe_mxfp_product(codes, scales, w, out, offsets=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        qm.strata_moe_mxfp_product(codes, scales, w, out, offsets=torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        qm.strata_moe_mxfp_product(codes, scales, w, out, offsets=torch.zeros(3, dtype=torch.int32),
+                                   src=torch.zeros(5, dtype=torch.int32))
+
+
+# ----------------------------------------------------- the reference's pins
+def test_reference_rounding_by_brute_force():
+    """Nearest of all 16 values in exact rationals, on a grid through every border."""
+    from fractions import Fraction as F
+
+    grid = np.arange(-33, 34) / 4.0
+    for base in (4.0, 5.5, 7.75):
+        vals = grid[np.abs(grid) <= base]
+        for i in range(0, len(vals), 31):
+            x = np.zeros((1, 32))
+            x[0, :len(vals[i:i + 31])] = vals[i:i + 31]
+            x[0, 31] = base
+            codes, byte = ref.quantize(x)
+            assert byte[0, 0] == 127
+            for v, c in zip(x[0], codes[0]):
+                mags = [F(m) for m in ref.MAGNITUDES.tolist()]
+                a = min(F(abs(float(v))), F(6))
+                best = min(range(8), key=lambda k: (abs(a - mags[k]), k % 2))
+                assert (c & 7) == best and (c >> 3) == np.signbit(v)
+    assert np.array_equal(ref.unpack(ref.pack(codes)), codes)

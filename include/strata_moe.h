@@ -514,7 +514,7 @@ typedef struct strata_moe_norm {
  *   codes, scales: x rounded as strata_moe_mxfp_quantize does (H a multiple of
  *       32), or both NULL
  * 0 <= T <= 2^24, 1 <= H <= 16384.  The arithmetic is in fp64, each output is
- * rounded once.  Outputs overlap neither each other nor an input.  Errors:
+ * rounded to fp32 (norm_after's out from there to its type).  Outputs overlap neither each other nor an input.  Errors:
  * EINVAL for sizes, NULL pointers, alignment, strides or overlap, EUNSUPPORTED
  * for an unknown dtype. */
 int strata_moe_norm_before(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H,

@@ -80,9 +80,10 @@ __device__ __forceinline__ int tile_row(int tile, int r, int rows, int paired) {
     return i < rows / 2 ? i + (tile & 1) * (rows / 2) : -1;
 }
 
-// One wave per (expert, tile, group of 4 steps).  Within a step lane l holds
-// row l % 16 and the 32 values 32 (l / 16) on: what the matrix unit reads.  The
-// group's scale dword of lane l: its row's scales of block l / 16 of each step.
+// One wave per (expert, tile, group of n = 4 steps, fewer in the last).  In step s
+// of a group lane l holds row l % 16 and the 32 values of block n (l / 16) + s of
+// the group: what the matrix unit reads.  A lane's blocks of the group are then
+// neighbours, and its scale dword is theirs, byte s for step s.
 __global__ __launch_bounds__(64) void pack_kernel(const uint8_t* __restrict__ codes,
                                                   const uint8_t* __restrict__ scales, int rows, int cols, int paired,
                                                   uint8_t* __restrict__ packed, int64_t stride, int64_t tile_bytes) {
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(64) void pack_kernel(const uint8_t* __restrict__ co
     uint8_t* dst = packed + e * stride + blockIdx.y * tile_bytes + (int64_t)blockIdx.x * (4 * kMxStepBytes + kMxScaleBytes);
     uint32_t sc = 0;
     for (int s = 0; s < n; ++s) {
-        const int b = (s0 + s) * 4 + g;
+        const int b = s0 * 4 + n * g + s;
         uint4 q = {0, 0, 0, 0};
         if (row >= 0 && b < blocks) {
             const int64_t at = (e * rows + row) * blocks + b;
@@ -125,10 +126,10 @@ constexpr int kMaxE = 1024;
 struct List {
     int32_t pre[kMaxE + 1];
 };
-__device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t rows) { return v < 0 ? 0 : v > rows ? rows : v; }
+__device__ __forceinline__ int32_t clamp_row(int32_t v, int32_t rows) { return v < 0 ? 0 : v > rows ? rows : v; }
 
 template <int MT>
-__device__ void make_list(const MxProduct& p, List& L, int32_t* wave_sum) {
+__device__ __forceinline__ void make_list(const MxProduct& p, List& L, int32_t* wave_sum) {
     if (!p.offsets) {
         if (threadIdx.x == 0) L.pre[0] = 0, L.pre[1] = (int32_t)((p.rows + MT - 1) / MT);
         __syncthreads();
@@ -141,8 +142,8 @@ __device__ void make_list(const MxProduct& p, List& L, int32_t* wave_sum) {
         const int e = threadIdx.x * kPer + i;
         n[i] = 0;
         if (e < p.E) {
-            const int64_t a = clamp_row(p.offsets[e], p.rows), b = clamp_row(p.offsets[e + 1], p.rows);
-            n[i] = b > a ? (int32_t)((b - a + MT - 1) / MT) : 0;
+            const int32_t a = clamp_row(p.offsets[e], (int32_t)p.rows), b = clamp_row(p.offsets[e + 1], (int32_t)p.rows);
+            n[i] = b > a ? (b - a + MT - 1) / MT : 0;
         }
         s += n[i];
     }
@@ -168,36 +169,39 @@ __device__ void make_list(const MxProduct& p, List& L, int32_t* wave_sum) {
     __syncthreads();
 }
 
+// Wave-uniform, in scalar registers.
 struct Item {
-    int32_t e, run;
-    int64_t row0;
+    int32_t e, run, row0;
     int32_t rows;  // 1 .. MT
 };
-template <int MT>
-__device__ Item find_item(const MxProduct& p, const List& L, int nb, int64_t u) {
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <int MT, int kUnit>
+__device__ __forceinline__ Item find_item(const MxProduct& p, const List& L, int nb, int64_t u) {
     const int lane = threadIdx.x % 64;
     Item it;
     int e = 0;
     if (p.offsets) {
-        // the last expert whose first item is not behind u, 16 at a time, then one by one
+        // the last expert whose first item is not behind u: among every 16th, then among the 16
         const bool a = lane * 16 <= p.E && (int64_t)L.pre[lane * 16 <= p.E ? lane * 16 : 0] * nb <= u;
         e = (__popcll(__ballot(a)) - 1) * 16;
         const bool b = lane < 16 && e + lane < p.E && (int64_t)L.pre[e + lane < p.E ? e + lane : 0] * nb <= u;
         e += __popcll(__ballot(b)) - 1;
     }
-    e = __builtin_amdgcn_readfirstlane(e);
-    const int32_t tiles = L.pre[e + 1] - L.pre[e];
-    const int64_t left = u - (int64_t)L.pre[e] * nb;
-    const int32_t run = (int32_t)(left / tiles), t = (int32_t)(left - (int64_t)run * tiles);
-    const int64_t r0 = p.offsets ? clamp_row(p.offsets[e], p.rows) : 0;
-    const int64_t r1 = p.offsets ? clamp_row(p.offsets[e + 1], p.rows) : p.rows;
-    // rows dealt evenly to the tiles, in whole 16s
-    const int32_t frags = (int32_t)((r1 - r0 + 15) / 16);
-    const int32_t f0 = (int32_t)((int64_t)frags * t / tiles), f1 = (int32_t)((int64_t)frags * (t + 1) / tiles);
+    e = uniform(e);
+    const int32_t first = uniform(L.pre[e]), tiles = uniform(L.pre[e + 1]) - first;
+    const uint32_t left = (uint32_t)(u - (int64_t)first * nb);  // below tiles * nb < 2^31
+    const uint32_t run = left / (uint32_t)tiles, t = left - run * (uint32_t)tiles;
+    const int32_t rows = (int32_t)p.rows;
+    const int32_t r0 = p.offsets ? clamp_row(uniform(p.offsets[e]), rows) : 0;
+    const int32_t r1 = p.offsets ? clamp_row(uniform(p.offsets[e + 1]), rows) : rows;
+    // rows dealt evenly to the tiles, in whole units of 16 kUnit
+    const int32_t units = (r1 - r0 + 16 * kUnit - 1) / (16 * kUnit);
+    const int32_t f0 = (int32_t)((int64_t)units * t / tiles), f1 = (int32_t)((int64_t)units * (t + 1) / tiles);
     it.e = e;
-    it.run = run;
-    it.row0 = r0 + (int64_t)f0 * 16;
-    it.rows = (int32_t)(min(r1, r0 + (int64_t)f1 * 16) - it.row0);
+    it.run = (int32_t)run;
+    it.row0 = r0 + f0 * 16 * kUnit;
+    it.rows = min(r1, r0 + f1 * 16 * kUnit) - it.row0;
     return it;
 }
 
@@ -213,7 +217,7 @@ __device__ __forceinline__ float swiglu(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
-__device__ __forceinline__ void store_out(const ProductArgs& a, int64_t row, int n, v4f v) {
+__device__ __forceinline__ void store_out(const ProductArgs& a, int32_t row, int n, v4f v) {
     float f[4] = {v[0], v[1], v[2], v[3]};
     store4_any(a.p.out, a.p.dtype, row * a.p.out_stride, n, a.n_out, a.vec_out, f);
 }
@@ -230,11 +234,11 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(ProductArgs a) {
     __shared__ v4f part[kWaves][MF * NF][64];
     const MxProduct& p = a.p;
     make_list<MT>(p, L, wave_sum);
-    const int64_t items = (int64_t)L.pre[p.E] * a.nb;
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, r16 = lane % 16, g = lane / 16;
+    const int64_t items = (int64_t)uniform(L.pre[p.E]) * a.nb;
+    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), r16 = lane % 16, g = lane / 16;
     const int s0 = a.steps * wave / kWaves, s1 = a.steps * (wave + 1) / kWaves;
     for (int64_t u = blockIdx.x; u < items; u += gridDim.x) {
-        const Item it = find_item<MT>(p, L, a.nb, u);
+        const Item it = find_item<MT, 1>(p, L, a.nb, u);
         const uint8_t* wt[NF];
 #pragma unroll
         for (int f = 0; f < NF; ++f)
@@ -264,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(ProductArgs a) {
                 w[f] = *(const v4i*)(wt[f] + at + in_group * kMxStepBytes + lane * 16);
                 ws[f] = *(const int*)(wt[f] + at + of_group * kMxStepBytes + lane * 4) >> (8 * in_group);
             }
-            const int b = s * 4 + g;
+            const int b = group * 16 + of_group * g + in_group;
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
                 x[m] = v4i{0, 0, 0, 0};
@@ -303,6 +307,287 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(ProductArgs a) {
             if (r < it.rows && n < a.n_out) store_out(a, it.row0 + r, n, v);
         }
         __syncthreads();
+    }
+}
+
+// Many rows: the matrix unit bounds it, or the weights' bytes if an expert has a
+// few hundred rows.  A workgroup takes up to 8 tiles of rows (128) and 16 of
+// weights, 4 to a wave.  The rows' codes of 512 reduction values (a group) go to
+// LDS while the group before is multiplied (two buffers); each wave reads its own
+// weights from memory straight into registers, a group ahead.  Row tiles come in
+// pairs: an item of fewer rows leaves out the pairs it lacks.
+constexpr int kRowTiles = 8;
+constexpr int kWaveTiles = 4;
+constexpr int kGroupBytes = 4 * kMxStepBytes + kMxScaleBytes;
+// [row][16 pieces]: 16 bytes a block; piece c of row r lies at c ^ r % 16, so that
+// the 16 rows that a product reads at one c lie in different banks.
+struct Rows {
+    v4i codes[kRowTiles * 16 * 16];
+    int scales[kRowTiles * 64];  // [tile][lane]: the lane's scales of a group, byte s for step s
+};
+
+using Resource = __amdgpu_buffer_rsrc_t;
+__device__ __forceinline__ Resource resource(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+using LdsPtr = void __attribute__((address_space(3)))*;
+
+struct TileLoads {
+    Resource codes, scales, weights;  // x, its scales, the item's expert
+    const uint32_t* first;            // [128] LDS: first block in x of each row of the item
+    uint32_t tile[kWaveTiles];        // byte offsets of the wave's weight tiles
+    int32_t blocks, steps, lane, wave;
+};
+
+// A lane's offset that no array reaches: such a load reads nothing.
+constexpr uint32_t kNowhere = 0xf0000000u;
+
+// Start the loads of group q: 4 rows of 256 bytes an instruction.
+template <int kPairs>
+__device__ __forceinline__ void load_rows(const TileLoads& l, int q, uint32_t off, Rows* __restrict__ to) {
+#pragma unroll
+    for (int i = 0; i < 2 * kPairs; ++i) {
+        const int r4 = (i * kWaves + l.wave) * 4, r = r4 + l.lane / 16;
+        const uint32_t at = l.first[r] * 16 + ((l.lane % 16) ^ (r % 16)) * 16;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(l.codes, (LdsPtr)(to->codes + r4 * 16), 16, at | off, q * 256, 0, 0);
+    }
+}
+
+// The scales of whole group q of tiles wave and wave + 4: a lane's are neighbours.
+template <int kPairs>
+__device__ __forceinline__ void load_row_scales(const TileLoads& l, int q, uint32_t off, int* sc) {
+#pragma unroll
+    for (int i = 0; i < (kPairs > 2 ? 2 : 1); ++i) {
+        const uint32_t at = l.first[(l.wave + 4 * i) * 16 + l.lane % 16] + 4 * (l.lane / 16);
+        sc[i] = __builtin_amdgcn_raw_buffer_load_b32(l.scales, at | off, q * 16, 0);
+    }
+}
+// Those of the last, n steps long and perhaps not whole, byte by byte: a block
+// past the row's end gets scale 2^-127 (its codes are any, and meet weights of 0).
+template <int kPairs>
+__device__ __forceinline__ void load_last_scales(const TileLoads& l, int q, int n, int* sc) {
+    const int g = l.lane / 16;
+#pragma unroll
+    for (int i = 0; i < (kPairs > 2 ? 2 : 1); ++i) {
+        const uint32_t at = l.first[(l.wave + 4 * i) * 16 + l.lane % 16] + n * g;
+        sc[i] = 0;
+        for (int s = 0; s < n; ++s)
+            if (q * 16 + n * g + s < l.blocks)
+                sc[i] |= (int)__builtin_amdgcn_raw_buffer_load_b8(l.scales, at + s, q * 16, 0) << (8 * s);
+    }
+}
+template <int kPairs>
+__device__ __forceinline__ void keep_row_scales(const TileLoads& l, const int* sc, Rows* to) {
+#pragma unroll
+    for (int i = 0; i < (kPairs > 2 ? 2 : 1); ++i) to->scales[(l.wave + 4 * i) * 64 + l.lane] = sc[i];
+}
+
+__device__ __forceinline__ void load_weights(const TileLoads& l, int q, int st, uint32_t off, v4i* w) {
+#pragma unroll
+    for (int f = 0; f < kWaveTiles; ++f)
+        w[f] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                           l.weights, l.lane * 16 | off, l.tile[f] + q * kGroupBytes + st * kMxStepBytes, 0));
+}
+__device__ __forceinline__ void load_weight_scales(const TileLoads& l, int q, int n, uint32_t off, int* sc) {
+#pragma unroll
+    for (int f = 0; f < kWaveTiles; ++f)
+        sc[f] = __builtin_amdgcn_raw_buffer_load_b32(l.weights, l.lane * 4 | off,
+                                                     l.tile[f] + q * kGroupBytes + n * kMxStepBytes, 0);
+}
+
+// Step ST of a group of n: the products of every row tile.
+template <int kPairs, int ST>
+__device__ __forceinline__ void step_products(const Rows* __restrict__ x, const int* xs, const v4i* w, const int* ws,
+                                              int n, int lane, v4f (*acc)[kWaveTiles]) {
+    const int r16 = lane % 16;
+    const v4i* at = x->codes + r16 * 16 + ((n * (lane / 16) + ST) ^ r16);
+#pragma unroll
+    for (int m = 0; m < 2 * kPairs; ++m) {
+        const v8i a = operand(at[m * 256]);
+#pragma unroll
+        for (int f = 0; f < kWaveTiles; ++f)
+            acc[m][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[f]), a, acc[m][f], 4, 4, ST, ws[f], ST,
+                                                                         xs[m]);
+    }
+}
+
+// Everything this wave wrote to or started into LDS is there, for all waves.
+__device__ __forceinline__ void rows_ready() {
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+}
+
+struct WeightRegs {
+    v4i w[2][kWaveTiles];  // steps of the same parity take turns
+    int s[kWaveTiles];
+};
+
+// Whole group q of `groups` from `now`, the loads of group q + 1 into `next` beside
+// it, and those of the weights two steps ahead.
+template <int kPairs>
+__device__ __forceinline__ void group(const TileLoads& l, int q, int groups, Rows* __restrict__ now,
+                                      Rows* __restrict__ next, WeightRegs& r, v4f (*acc)[kWaveTiles]) {
+    // behind the last group: loads of nothing (the scalar offset stays in the arrays,
+    // since the range check subtracts it from their size)
+    const int qn = q + 1 < groups ? q + 1 : q;
+    const uint32_t off = q + 1 < groups ? 0 : kNowhere;
+    int sc[2], ws[kWaveTiles], xs[2 * kPairs];
+    load_rows<kPairs>(l, qn, off, next);
+    load_row_scales<kPairs>(l, qn, off, sc);
+    load_weight_scales(l, qn, 4, off, ws);
+#pragma unroll
+    for (int m = 0; m < 2 * kPairs; ++m) xs[m] = now->scales[m * 64 + l.lane];
+    __builtin_amdgcn_sched_barrier(0);
+    step_products<kPairs, 0>(now, xs, r.w[0], r.s, 4, l.lane, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    load_weights(l, q, 2, 0, r.w[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    step_products<kPairs, 1>(now, xs, r.w[1], r.s, 4, l.lane, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    load_weights(l, q, 3, 0, r.w[1]);
+    __builtin_amdgcn_sched_barrier(0);
+    step_products<kPairs, 2>(now, xs, r.w[0], r.s, 4, l.lane, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    load_weights(l, qn, 0, off, r.w[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    step_products<kPairs, 3>(now, xs, r.w[1], r.s, 4, l.lane, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    load_weights(l, qn, 1, off, r.w[1]);
+    __builtin_amdgcn_sched_barrier(0);
+    keep_row_scales<kPairs>(l, sc, next);
+#pragma unroll
+    for (int f = 0; f < kWaveTiles; ++f) r.s[f] = ws[f];
+    rows_ready();
+}
+
+// The last group, where it is not whole: n steps of four.
+template <int kPairs>
+__device__ __forceinline__ void last_group(const TileLoads& l, int q, Rows* __restrict__ b0, v4f (*acc)[kWaveTiles]) {
+    const int n = l.steps - 4 * q;
+    int sc[2], ws[kWaveTiles], xs[2 * kPairs];
+    v4i w[kWaveTiles];
+    load_rows<kPairs>(l, q, 0, b0);
+    load_weight_scales(l, q, n, 0, ws);
+    load_last_scales<kPairs>(l, q, n, sc);
+    keep_row_scales<kPairs>(l, sc, b0);
+    load_weights(l, q, 0, 0, w);
+    rows_ready();
+#pragma unroll
+    for (int m = 0; m < 2 * kPairs; ++m) xs[m] = b0->scales[m * 64 + l.lane];
+    step_products<kPairs, 0>(b0, xs, w, ws, n, l.lane, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    if (n > 1) {
+        load_weights(l, q, 1, 0, w);
+        step_products<kPairs, 1>(b0, xs, w, ws, n, l.lane, acc);
+    }
+    if (n > 2) {
+        load_weights(l, q, 2, 0, w);
+        step_products<kPairs, 2>(b0, xs, w, ws, n, l.lane, acc);
+    }
+    if (n > 3) {
+        load_weights(l, q, 3, 0, w);
+        step_products<kPairs, 3>(b0, xs, w, ws, n, l.lane, acc);
+    }
+    rows_ready();
+}
+
+template <int kPairs>
+__device__ __forceinline__ void item_sums(const TileLoads& l, Rows* b0, Rows* b1, v4f (*acc)[kWaveTiles]) {
+    const int groups = l.blocks / 16;  // whole ones
+    int sc[2];
+    if (groups) {
+        WeightRegs r;
+        load_rows<kPairs>(l, 0, 0, b0);
+        load_row_scales<kPairs>(l, 0, 0, sc);
+        load_weight_scales(l, 0, 4, 0, r.s);
+        load_weights(l, 0, 0, 0, r.w[0]);
+        load_weights(l, 0, 1, 0, r.w[1]);
+        keep_row_scales<kPairs>(l, sc, b0);
+        rows_ready();
+        for (int q = 0; q < groups; q += 2) {
+            group<kPairs>(l, q, groups, b0, b1, r, acc);
+            if (q + 1 < groups) group<kPairs>(l, q + 1, groups, b1, b0, r, acc);
+        }
+    }
+    if (l.blocks % 16) last_group<kPairs>(l, groups, b0, acc);
+}
+
+__global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
+    constexpr int MT = kRowTiles * 16;
+    __shared__ Rows b0, b1;
+    __shared__ uint32_t first[MT];
+    __shared__ List L;
+    __shared__ int32_t wave_sum[kWaves];
+    const MxProduct& p = a.p;
+    make_list<MT>(p, L, wave_sum);
+    const int64_t items = (int64_t)uniform(L.pre[p.E]) * a.nb;
+    // workgroups of one XCD (every eighth) take one run of the items
+    const int xcd = blockIdx.x % 8, per = gridDim.x / 8;
+    const int64_t u1 = items * (xcd + 1) / 8;
+    TileLoads l;
+    l.codes = resource(p.codes, (uint32_t)(p.x_rows * a.blocks * 16));
+    l.scales = resource(p.scales, (uint32_t)(p.x_rows * a.blocks));
+    l.first = first;
+    l.blocks = a.blocks;
+    l.steps = a.steps;
+    l.lane = threadIdx.x % 64;
+    l.wave = uniform(threadIdx.x / 64);
+    for (int64_t u = items * xcd / 8 + blockIdx.x / 8; u < u1; u += per) {
+        const Item it = find_item<MT, 2>(p, L, a.nb, u);
+        if (threadIdx.x < MT) {
+            int32_t s = it.row0 + min((int)threadIdx.x, it.rows - 1);
+            if (p.src) s = p.src[s];
+            first[threadIdx.x] = s < 0 || s >= p.x_rows ? 0u : (uint32_t)s * (uint32_t)a.blocks;
+        }
+        __syncthreads();
+        const int t0 = it.run * (kWaves * kWaveTiles) + l.wave * kWaveTiles, pairs = (it.rows + 31) / 32;
+        l.weights = resource(p.packed + it.e * p.stride, (uint32_t)(a.tiles * a.tile_bytes));
+#pragma unroll
+        for (int f = 0; f < kWaveTiles; ++f) l.tile[f] = (uint32_t)(min(t0 + f, a.tiles - 1) * a.tile_bytes);
+        v4f acc[kRowTiles][kWaveTiles];
+#pragma unroll
+        for (int m = 0; m < kRowTiles; ++m)
+#pragma unroll
+            for (int f = 0; f < kWaveTiles; ++f) acc[m][f] = v4f{0, 0, 0, 0};
+        if (pairs == 1) item_sums<1>(l, &b0, &b1, acc);
+        else if (pairs == 2) item_sums<2>(l, &b0, &b1, acc);
+        else if (pairs == 3) item_sums<3>(l, &b0, &b1, acc);
+        else item_sums<4>(l, &b0, &b1, acc);
+
+        // Four row tiles at a time through 16 KB of LDS of the wave's own (nobody
+        // reads rows there now), so that a row's outputs are stored side by side.
+        // A row has 16 pieces of 4 outputs, piece c at c ^ row % 16 again.
+        v4f* own = (v4f*)((l.wave & 2 ? b1 : b0).codes) + (l.wave & 1) * 1024;
+        const int r16 = l.lane % 16, g = l.lane / 16;
+        const int width = p.paired ? 8 : 16, n0 = t0 * kMxTileRows / (p.paired ? 2 : 1);  // pieces, first output
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (2 * half >= pairs) break;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int f = 0; f < kWaveTiles; f += 2) {
+                    v4f v = acc[4 * half + m][f], u = acc[4 * half + m][f + 1];
+                    v4f* row = own + (m * 16 + r16) * 16;
+                    if (p.paired) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], u[i]);
+                        row[(f / 2 * 4 + g) ^ r16] = v;
+                    } else {
+                        row[(f * 4 + g) ^ r16] = v;
+                        row[(f * 4 + 4 + g) ^ r16] = u;
+                    }
+                }
+            const int rows = min(64, it.rows - 64 * half), step = 64 / width;
+            for (int r = l.lane / width; r < rows; r += step) {
+                const int c = l.lane % width, to = it.row0 + 64 * half + r;
+                v4f v = own[r * 16 + (c ^ (r % 16))];
+                if (p.src && (uint64_t)(int64_t)p.src[to] >= (uint64_t)p.x_rows) v = v4f{0, 0, 0, 0};
+                if (n0 + 4 * c < a.n_out) store_out(a, to, n0 + 4 * c, v);
+            }
+        }
     }
 }
 
@@ -360,16 +645,15 @@ hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
     const size_t el = dtype_bytes(p.dtype);
     a.vec_out = ((uintptr_t)p.out | (uintptr_t)(p.out_stride * (int64_t)el)) % (4 * el) == 0;
     constexpr int NF = 4;
-    a.nb = (a.tiles + NF - 1) / NF;
     const int64_t hit = p.rows < p.E ? p.rows : p.E;
-    auto items = [&](int mt) { return (p.rows / mt + hit) * a.nb; };
-    const int64_t most = 256 * 4;
     if (p.rows <= 16 * (int64_t)p.E) {
-        const int64_t n = items(16);
+        a.nb = (a.tiles + NF - 1) / NF;
+        const int64_t n = (p.rows / 16 + hit) * a.nb, most = 256 * 4;
         hipLaunchKernelGGL((stream_kernel<1, NF>), dim3((uint32_t)(n < most ? n : most)), dim3(kThreads), 0, st, a);
     } else {
-        const int64_t n = items(64);
-        hipLaunchKernelGGL((stream_kernel<4, NF>), dim3((uint32_t)(n < most ? n : most)), dim3(kThreads), 0, st, a);
+        a.nb = (a.tiles + kWaves * kWaveTiles - 1) / (kWaves * kWaveTiles);
+        const int64_t n = (p.rows / (16 * kRowTiles) + hit) * a.nb, most = 256 * 2;
+        hipLaunchKernelGGL(tile_kernel, dim3((uint32_t)(n < most ? (n + 7) / 8 * 8 : most)), dim3(kThreads), 0, st, a);
     }
     return hipGetLastError();
 }

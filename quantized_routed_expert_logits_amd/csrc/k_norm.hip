@@ -9,9 +9,10 @@
 // One workgroup per token; its row stays in registers between the sums, so
 // every array is read or written once.  A thread holds runs of 4 neighbouring
 // columns, so 8 neighbouring threads hold the 32 columns of one 4-bit block.
-// All arithmetic is in 64 bits: an output is then rounded once, and the 4-bit
-// codes are those of the exact row except where it lies within about 2^-50 of
-// a border.  The memory bounds these kernels, so the wider arithmetic is free.
+// All arithmetic is in 64 bits and an output is rounded to fp32, and from there
+// to 16 bits: the stored stream and the 4-bit codes are those of the exact row
+// except where it lies within about 2^-50 of a border.  The memory bounds these
+// kernels, so the wider arithmetic is free.
 #include "block.h"
 #include "mxfp.h"
 
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
             float o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                h[c][i] = round_once(fma(l.residual_scale, h[c][i], l.block_scale * (g[i] * v[c][i])), l.dtype, &o[i]);
+                h[c][i] = round_to(fma(l.residual_scale, h[c][i], l.block_scale * (g[i] * v[c][i])), l.dtype, &o[i]);
             store4_any(l.out, l.dtype, t * l.out_stride, j, H, a.vec_out, o);
         }
     }

@@ -51,22 +51,11 @@ __device__ __forceinline__ void store4_any(void* base, int dtype, int64_t at, in
     else store4<__bf16, v4b>((__bf16*)base + at, j, H, vec, v);
 }
 
-// v in 64 bits rounded to the type, once: fp32 to nearest, and the 16-bit
-// types from a 32-bit value rounded to odd, which keeps the second rounding
-// from meeting a tie that the first one made.  *o: the value as fp32.
-__device__ __forceinline__ double round_once(double v, int dtype, float* o) {
-    float f = (float)v;
-    if (dtype == kF32) {
-        *o = f;
-        return f;
-    }
-    const double d = (double)f;
-    if (d != v && __builtin_isfinite(f)) {
-        uint32_t u = __float_as_uint(f);
-        if (!(u & 1)) u += fabs(d) < fabs(v) ? 1u : ~0u;  // f even, so its neighbours are odd
-        f = __uint_as_float(u);
-    }
-    *o = dtype == kF16 ? (float)(_Float16)f : (float)(__bf16)f;
+// v rounded to fp32 and from there to the type, as a 16-bit tensor is made of a
+// 64-bit one; *o: the value as fp32.
+__device__ __forceinline__ double round_to(double v, int dtype, float* o) {
+    const float f = (float)v;
+    *o = dtype == kF32 ? f : dtype == kF16 ? (float)(_Float16)f : (float)(__bf16)f;
     return *o;
 }
 

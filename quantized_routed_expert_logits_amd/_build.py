@@ -41,15 +41,9 @@ FLAGS = [
 ]
 
 
-# k_mxfp.hip: the machine sinking pass moves matrix products into the branches
-# around them, and the accumulators of all variants are then live at once (551
-# registers spilled, none without the pass)
-FILE_FLAGS = {"k_mxfp.hip": ["-mllvm", "-disable-machine-sink"]}
-
-
 def _compile(src: str) -> str:
     obj = os.path.join(OUT_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *FLAGS, *FILE_FLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{res.stdout}\n{res.stderr}")

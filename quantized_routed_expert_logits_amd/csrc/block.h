@@ -11,17 +11,22 @@ constexpr int kF32 = 1, kF16 = 2, kBF16 = 3;  // STRATA_MOE_F32, _F16, _BF16
 inline size_t dtype_bytes(int32_t t) { return t == kF32 ? 4 : 2; }
 
 // ---- microscaled 4-bit floating point (k_mxfp.hip)
-// A packed matrix: tiles of 16 rows; a tile is its steps of 128 values of the
-// reduction, four to a group, and each group's scales behind its steps.
+// A packed matrix: tiles of 16 rows, each its groups of 16 blocks of 32 reduction
+// values; a group is the codes of its blocks, 256 bytes each, then its scales.
 constexpr int kMxTileRows = 16;
-constexpr int kMxStep = 128;       // reduction values of one matrix-unit product
-constexpr int kMxStepBytes = 1024; // codes of 16 rows x 128 values
-constexpr int kMxScaleBytes = 256; // scales of 16 rows x 512 values
+constexpr int kMxBlockBytes = 256;  // codes of 16 rows x 32 values
+constexpr int kMxScaleBytes = 256;  // scales of 16 rows x 512 values
+constexpr int kMxGroupBytes = 16 * kMxBlockBytes + kMxScaleBytes;
 constexpr int kMxMaxCols = 65536, kMxMaxRows = 65536;
 
 inline int64_t mx_tile_bytes(int64_t cols) {
-    const int64_t steps = (cols + kMxStep - 1) / kMxStep;
-    return steps * kMxStepBytes + (steps + 3) / 4 * kMxScaleBytes;
+    const int64_t blocks = cols / 32;
+    return blocks * kMxBlockBytes + (blocks + 15) / 16 * kMxScaleBytes;
+}
+// Where step s of a group of `have` blocks begins: step s holds blocks s, 4 + s,
+// 8 + s and 12 + s, as far as they exist.
+__host__ __device__ inline int mx_step_at(int have, int s) {
+    return (s * (have / 4) + (s < have % 4 ? s : have % 4)) * kMxBlockBytes;
 }
 // Tiles of a matrix of `rows` rows; with paired set, the tiles of its first
 // and second half alternate.

@@ -5,6 +5,8 @@
 // Format.  32 consecutive values of a row share a scale 2^(byte - 127); a value
 // is a sign and one of 0, .5, 1, 1.5, 2, 3, 4, 6 (code bit 3 the sign, 2..1 the
 // exponent, 0 the mantissa), two to a byte, the first in the low half.
+#include <algorithm>
+
 #include "block.h"
 #include "mxfp.h"
 
@@ -80,31 +82,31 @@ __device__ __forceinline__ int tile_row(int tile, int r, int rows, int paired) {
     return i < rows / 2 ? i + (tile & 1) * (rows / 2) : -1;
 }
 
-// One wave per (expert, tile, group of n = 4 steps, fewer in the last).  In step s
-// of a group lane l holds row l % 16 and the 32 values of block n (l / 16) + s of
-// the group: what the matrix unit reads.  A lane's blocks of the group are then
-// neighbours, and its scale dword is theirs, byte s for step s.
+// One wave per (expert, tile, group of 16 blocks).  A group is four steps: in step
+// s lane l holds row l % 16 and block 4 (l / 16) + s of the group, what the matrix
+// unit reads, so a lane's blocks are neighbours and its scale dword is theirs, byte
+// s for step s.  The last group keeps only the blocks there are (mx_step_at).
 __global__ __launch_bounds__(64) void pack_kernel(const uint8_t* __restrict__ codes,
                                                   const uint8_t* __restrict__ scales, int rows, int cols, int paired,
                                                   uint8_t* __restrict__ packed, int64_t stride, int64_t tile_bytes) {
     const int lane = threadIdx.x, g = lane / 16, blocks = cols / 32;
-    const int steps = (cols + kMxStep - 1) / kMxStep;
-    const int s0 = blockIdx.x * 4, n = min(4, steps - s0);
+    const int q = blockIdx.x, have = min(16, blocks - q * 16);
     const int row = tile_row(blockIdx.y, lane % 16, rows, paired);
     const int64_t e = blockIdx.z;
-    uint8_t* dst = packed + e * stride + blockIdx.y * tile_bytes + (int64_t)blockIdx.x * (4 * kMxStepBytes + kMxScaleBytes);
+    uint8_t* dst = packed + e * stride + blockIdx.y * tile_bytes + (int64_t)q * kMxGroupBytes;
     uint32_t sc = 0;
-    for (int s = 0; s < n; ++s) {
-        const int b = s0 * 4 + n * g + s;
-        uint4 q = {0, 0, 0, 0};
-        if (row >= 0 && b < blocks) {
-            const int64_t at = (e * rows + row) * blocks + b;
-            q = ((const uint4*)codes)[at];
+    for (int s = 0; s < 4; ++s) {
+        const int b = 4 * g + s;
+        if (b >= have) continue;
+        uint4 v = {0, 0, 0, 0};
+        if (row >= 0) {
+            const int64_t at = (e * rows + row) * blocks + q * 16 + b;
+            v = ((const uint4*)codes)[at];
             sc |= (uint32_t)scales[at] << (8 * s);
         }
-        *(uint4*)(dst + s * kMxStepBytes + lane * 16) = q;
+        *(uint4*)(dst + mx_step_at(have, s) + lane * 16) = v;
     }
-    *(uint32_t*)(dst + n * kMxStepBytes + lane * 4) = sc;
+    *(uint32_t*)(dst + have * kMxBlockBytes + lane * 4) = sc;
 }
 
 // ------------------------------------------------------------------- product
@@ -112,9 +114,11 @@ struct ProductArgs {
     MxProduct p;
     int64_t tile_bytes;
     int32_t tiles, n_out;   // packed tiles of an expert; outputs of a row
-    int32_t steps, blocks;  // of 128 and of 32 reduction values
+    int32_t blocks, groups; // of 32 and of 512 reduction values
+    int32_t steps;          // matrix-unit products along the reduction
     int32_t nb;             // work items along the outputs
-    int32_t vec_out;
+    int32_t vec_out;        // rows of out take 16-byte stores
+    int32_t vec_out4;       // ... stores of four outputs
 };
 
 // The work list.  An item is one tile of MT rows of one expert times one run of
@@ -125,13 +129,18 @@ struct ProductArgs {
 constexpr int kMaxE = 1024;
 struct List {
     int32_t pre[kMaxE + 1];
+    int32_t row[kMaxE + 1];  // the clamped offsets
 };
 __device__ __forceinline__ int32_t clamp_row(int32_t v, int32_t rows) { return v < 0 ? 0 : v > rows ? rows : v; }
 
 template <int MT>
 __device__ __forceinline__ void make_list(const MxProduct& p, List& L, int32_t* wave_sum) {
     if (!p.offsets) {
-        if (threadIdx.x == 0) L.pre[0] = 0, L.pre[1] = (int32_t)((p.rows + MT - 1) / MT);
+        if (threadIdx.x == 0) {
+            L.pre[0] = L.row[0] = 0;
+            L.pre[1] = (int32_t)((p.rows + MT - 1) / MT);
+            L.row[1] = (int32_t)p.rows;
+        }
         __syncthreads();
         return;
     }
@@ -144,6 +153,8 @@ __device__ __forceinline__ void make_list(const MxProduct& p, List& L, int32_t* 
         if (e < p.E) {
             const int32_t a = clamp_row(p.offsets[e], (int32_t)p.rows), b = clamp_row(p.offsets[e + 1], (int32_t)p.rows);
             n[i] = b > a ? (b - a + MT - 1) / MT : 0;
+            L.row[e] = a;
+            if (e == p.E - 1) L.row[p.E] = b;
         }
         s += n[i];
     }
@@ -192,9 +203,7 @@ __device__ __forceinline__ Item find_item(const MxProduct& p, const List& L, int
     const int32_t first = uniform(L.pre[e]), tiles = uniform(L.pre[e + 1]) - first;
     const uint32_t left = (uint32_t)(u - (int64_t)first * nb);  // below tiles * nb < 2^31
     const uint32_t run = left / (uint32_t)tiles, t = left - run * (uint32_t)tiles;
-    const int32_t rows = (int32_t)p.rows;
-    const int32_t r0 = p.offsets ? clamp_row(uniform(p.offsets[e]), rows) : 0;
-    const int32_t r1 = p.offsets ? clamp_row(uniform(p.offsets[e + 1]), rows) : rows;
+    const int32_t r0 = uniform(L.row[e]), r1 = uniform(L.row[e + 1]);
     // rows dealt evenly to the tiles, in whole units of 16 kUnit
     const int32_t units = (r1 - r0 + 16 * kUnit - 1) / (16 * kUnit);
     const int32_t f0 = (int32_t)((int64_t)units * t / tiles), f1 = (int32_t)((int64_t)units * (t + 1) / tiles);
@@ -219,7 +228,7 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 
 __device__ __forceinline__ void store_out(const ProductArgs& a, int32_t row, int n, v4f v) {
     float f[4] = {v[0], v[1], v[2], v[3]};
-    store4_any(a.p.out, a.p.dtype, row * a.p.out_stride, n, a.n_out, a.vec_out, f);
+    store4_any(a.p.out, a.p.dtype, row * a.p.out_stride, n, a.n_out, a.vec_out4, f);
 }
 
 // Few rows: the weights' bytes bound it.  A workgroup's 4 waves share NF tiles
@@ -259,23 +268,25 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(ProductArgs a) {
 #pragma unroll
             for (int f = 0; f < NF; ++f) acc[m][f] = v4f{0, 0, 0, 0};
         for (int s = s0; s < s1; ++s) {
-            const int group = s / 4, in_group = s % 4, of_group = min(4, a.steps - group * 4);
-            const int64_t at = (int64_t)group * (4 * kMxStepBytes + kMxScaleBytes);
+            // step st of group q, which has `have` blocks
+            const int q = s / 4, st = s % 4, have = min(16, a.blocks - q * 16);
+            const int b = 4 * g + st;
             v4i w[NF], x[MF];
             int ws[NF], xs[MF];
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
-                w[f] = *(const v4i*)(wt[f] + at + in_group * kMxStepBytes + lane * 16);
-                ws[f] = *(const int*)(wt[f] + at + of_group * kMxStepBytes + lane * 4) >> (8 * in_group);
+                const uint8_t* at = wt[f] + (int64_t)q * kMxGroupBytes;
+                w[f] = v4i{0, 0, 0, 0};
+                if (b < have) w[f] = *(const v4i*)(at + mx_step_at(have, st) + lane * 16);
+                ws[f] = *(const int*)(at + have * kMxBlockBytes + lane * 4) >> (8 * st);
             }
-            const int b = group * 16 + of_group * g + in_group;
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
                 x[m] = v4i{0, 0, 0, 0};
                 xs[m] = 0;
-                if (src[m] >= 0 && b < a.blocks) {
-                    x[m] = ((const v4i*)p.codes)[src[m] * a.blocks + b];
-                    xs[m] = p.scales[src[m] * a.blocks + b];
+                if (src[m] >= 0 && b < have) {
+                    x[m] = ((const v4i*)p.codes)[src[m] * a.blocks + q * 16 + b];
+                    xs[m] = p.scales[src[m] * a.blocks + q * 16 + b];
                 }
             }
 #pragma unroll
@@ -318,7 +329,6 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(ProductArgs a) {
 // pairs: an item of fewer rows leaves out the pairs it lacks.
 constexpr int kRowTiles = 8;
 constexpr int kWaveTiles = 4;
-constexpr int kGroupBytes = 4 * kMxStepBytes + kMxScaleBytes;
 // [row][16 pieces]: 16 bytes a block; piece c of row r lies at c ^ r % 16, so that
 // the 16 rows that a product reads at one c lie in different banks.
 struct Rows {
@@ -330,93 +340,140 @@ using Resource = __amdgpu_buffer_rsrc_t;
 __device__ __forceinline__ Resource resource(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
 }
+using GlobalPtr = const void __attribute__((address_space(1)))*;
 using LdsPtr = void __attribute__((address_space(3)))*;
 
 struct TileLoads {
-    Resource codes, scales, weights;  // x, its scales, the item's expert
-    const uint32_t* first;            // [128] LDS: first block in x of each row of the item
-    uint32_t tile[kWaveTiles];        // byte offsets of the wave's weight tiles
-    int32_t blocks, steps, lane, wave;
+    const uint8_t* codes;    // x
+    uint32_t last_codes;     // where its last 16 bytes begin
+    Resource scales;
+    uint32_t last_scales;    // where their last four bytes begin
+    int32_t blocks, groups, tiles, tile_bytes;
+    int32_t lane, wave;
 };
-
-// A lane's offset that no array reaches: such a load reads nothing.
+// One group of one item to load: wave-uniform.
+struct Part {
+    Resource weights;       // the item's expert
+    const uint32_t* first;  // [128] LDS: first block in x of each row of the item (and kZeroRow)
+    int32_t t0;             // the wave's first weight tile
+    int32_t pairs;          // of the item's row tiles
+    int32_t q;              // the group
+    uint32_t off;           // 0, or kNowhere: load nothing
+};
+// In the table: the row's src is outside x, its result zeros (it loads row 0; x has
+// less than 2^28 blocks, so the flag leaves the address).
+constexpr uint32_t kZeroRow = 0x80000000u;
+// A lane's offset that no array reaches.  (The scalar offsets always stay in the
+// arrays: the range check subtracts them from the size.)
 constexpr uint32_t kNowhere = 0xf0000000u;
 
-// Start the loads of group q: 4 rows of 256 bytes an instruction.
-template <int kPairs>
-__device__ __forceinline__ void load_rows(const TileLoads& l, int q, uint32_t off, Rows* __restrict__ to) {
+// Start the loads of a group's rows: 4 rows of 256 bytes an instruction.  (All
+// table reads come before the first load: the compiler takes a read of LDS to
+// wait for the loads into it.)
+struct RowAddresses {
+    uint32_t codes[kRowTiles], scales[2];
+};
+__device__ __forceinline__ void row_addresses(const TileLoads& l, const Part& t, RowAddresses& ad) {
 #pragma unroll
-    for (int i = 0; i < 2 * kPairs; ++i) {
-        const int r4 = (i * kWaves + l.wave) * 4, r = r4 + l.lane / 16;
-        const uint32_t at = l.first[r] * 16 + ((l.lane % 16) ^ (r % 16)) * 16;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(l.codes, (LdsPtr)(to->codes + r4 * 16), 16, at | off, q * 256, 0, 0);
+    for (int i = 0; i < kRowTiles; ++i) {
+        const int r = (i * kWaves + l.wave) * 4 + l.lane / 16;
+        // a piece past the row's end is any of x: it meets weights of 0
+        ad.codes[i] = min((t.first[r] + t.q * 16 + ((l.lane % 16) ^ (r % 16))) * 16, l.last_codes);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) ad.scales[i] = t.first[(l.wave + 4 * i) * 16 + l.lane % 16] & ~kZeroRow;
+}
+// 16 bytes a lane from base + its offset to LDS at `to` + 16 lane.  The compiler
+// does not know of the load: its own waits count too few loads in flight, so they
+// wait for more than they need, never for less; the wait for these is at group().
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void load_rows(const TileLoads& l, const RowAddresses& ad, int from, Rows* to) {
+    const uint32_t at = (uint32_t)(uintptr_t)(LdsPtr)to->codes + l.wave * 1024;
+#pragma unroll
+    for (int i = from; i < from + kRowTiles / 2; ++i) load_to_lds(l.codes, ad.codes[i], uniform(at) + i * kWaves * 1024);
+}
+
+// The scales of the rows of tiles wave and wave + 4: a lane's are neighbours, one
+// unaligned dword, read from at most the array's last four bytes.
+__device__ __forceinline__ uint32_t scales_at(const TileLoads& l, const Part& t, uint32_t row) {
+    return row + (uint32_t)(t.q * 16 + 4 * (l.lane / 16));
+}
+__device__ __forceinline__ void load_row_scales(const TileLoads& l, const Part& t, const RowAddresses& ad, int* sc) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        sc[i] = __builtin_amdgcn_raw_buffer_load_b32(l.scales, min(scales_at(l, t, ad.scales[i]), l.last_scales) | t.off,
+                                                     0, 0);
+}
+// Past the row's end a block gets scale 2^-127 (its codes are any, and meet weights
+// of 0).
+__device__ __forceinline__ void keep_row_scales(const TileLoads& l, const Part& t, const RowAddresses& ad, const int* sc,
+                                                Rows* to) {
+    const int have = l.blocks - (t.q * 16 + 4 * (l.lane / 16));  // blocks of the row from the lane's first on
+    const uint32_t mask = have >= 4 ? ~0u : have <= 0 ? 0u : (1u << (8 * have)) - 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t at = scales_at(l, t, ad.scales[i]), past = at - min(at, l.last_scales);
+        const uint32_t v = past < 4 ? (uint32_t)sc[i] >> (8 * past) : 0u;
+        to->scales[(l.wave + 4 * i) * 64 + l.lane] = (int)(v & mask);
     }
 }
 
-// The scales of whole group q of tiles wave and wave + 4: a lane's are neighbours.
-template <int kPairs>
-__device__ __forceinline__ void load_row_scales(const TileLoads& l, int q, uint32_t off, int* sc) {
-#pragma unroll
-    for (int i = 0; i < (kPairs > 2 ? 2 : 1); ++i) {
-        const uint32_t at = l.first[(l.wave + 4 * i) * 16 + l.lane % 16] + 4 * (l.lane / 16);
-        sc[i] = __builtin_amdgcn_raw_buffer_load_b32(l.scales, at | off, q * 16, 0);
-    }
+__device__ __forceinline__ uint32_t weights_at(const TileLoads& l, const Part& t, int f) {
+    return (uint32_t)min(t.t0 + f, l.tiles - 1) * (uint32_t)l.tile_bytes + t.q * kMxGroupBytes;
 }
-// Those of the last, n steps long and perhaps not whole, byte by byte: a block
-// past the row's end gets scale 2^-127 (its codes are any, and meet weights of 0).
-template <int kPairs>
-__device__ __forceinline__ void load_last_scales(const TileLoads& l, int q, int n, int* sc) {
-    const int g = l.lane / 16;
-#pragma unroll
-    for (int i = 0; i < (kPairs > 2 ? 2 : 1); ++i) {
-        const uint32_t at = l.first[(l.wave + 4 * i) * 16 + l.lane % 16] + n * g;
-        sc[i] = 0;
-        for (int s = 0; s < n; ++s)
-            if (q * 16 + n * g + s < l.blocks)
-                sc[i] |= (int)__builtin_amdgcn_raw_buffer_load_b8(l.scales, at + s, q * 16, 0) << (8 * s);
-    }
-}
-template <int kPairs>
-__device__ __forceinline__ void keep_row_scales(const TileLoads& l, const int* sc, Rows* to) {
-#pragma unroll
-    for (int i = 0; i < (kPairs > 2 ? 2 : 1); ++i) to->scales[(l.wave + 4 * i) * 64 + l.lane] = sc[i];
-}
-
-__device__ __forceinline__ void load_weights(const TileLoads& l, int q, int st, uint32_t off, v4i* w) {
+// Step st of the wave's tiles; lanes without a block in it get zeros.
+__device__ __forceinline__ void load_weights(const TileLoads& l, const Part& t, int st, v4i* w) {
+    const int have = min(16, l.blocks - t.q * 16);
+    const uint32_t off = (uint32_t)l.lane * 16 | (4 * (l.lane / 16) + st < have ? t.off : kNowhere);
 #pragma unroll
     for (int f = 0; f < kWaveTiles; ++f)
-        w[f] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
-                                           l.weights, l.lane * 16 | off, l.tile[f] + q * kGroupBytes + st * kMxStepBytes, 0));
+        w[f] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(t.weights, off, weights_at(l, t, f) + mx_step_at(have, st), 0));
 }
-__device__ __forceinline__ void load_weight_scales(const TileLoads& l, int q, int n, uint32_t off, int* sc) {
+__device__ __forceinline__ void load_weight_scales(const TileLoads& l, const Part& t, int* sc) {
+    const int have = min(16, l.blocks - t.q * 16);
 #pragma unroll
     for (int f = 0; f < kWaveTiles; ++f)
-        sc[f] = __builtin_amdgcn_raw_buffer_load_b32(l.weights, l.lane * 4 | off,
-                                                     l.tile[f] + q * kGroupBytes + n * kMxStepBytes, 0);
+        sc[f] = __builtin_amdgcn_raw_buffer_load_b32(t.weights, l.lane * 4 | t.off,
+                                                     weights_at(l, t, f) + have * kMxBlockBytes, 0);
 }
 
-// Step ST of a group of n: the products of every row tile.
+// Keeps the products before it before it: they have no side effects, and the
+// compiler would gather those of a whole group behind the group's loads.
+__device__ __forceinline__ void stay(v4f* a) {
+    static_assert(kWaveTiles == 4, "one operand a tile");
+    asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
+}
+
+// Step ST of a group: the products of every row tile.
 template <int kPairs, int ST>
-__device__ __forceinline__ void step_products(const Rows* __restrict__ x, const int* xs, const v4i* w, const int* ws,
-                                              int n, int lane, v4f (*acc)[kWaveTiles]) {
+__device__ __forceinline__ void step_products(const Rows* __restrict__ from, const int* xs, const v4i* w, const int* ws,
+                                              int lane, v4f (*acc)[kWaveTiles]) {
     const int r16 = lane % 16;
-    const v4i* at = x->codes + r16 * 16 + ((n * (lane / 16) + ST) ^ r16);
+    const v4i* at = from->codes + r16 * 16 + ((4 * (lane / 16) + ST) ^ r16);
+    // each operand read two tiles ahead of its products, in this order
+    v4i x[3] = {at[0], at[256], {}};
 #pragma unroll
     for (int m = 0; m < 2 * kPairs; ++m) {
-        const v8i a = operand(at[m * 256]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (m + 2 < 2 * kPairs) x[(m + 2) % 3] = at[(m + 2) * 256];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int f = 0; f < kWaveTiles; ++f)
-            acc[m][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[f]), a, acc[m][f], 4, 4, ST, ws[f], ST,
-                                                                         xs[m]);
+            acc[m][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[f]), operand(x[m % 3]), acc[m][f], 4, 4,
+                                                                         ST, ws[f], ST, xs[m]);
+        stay(acc[m]);
     }
 }
 
-// Everything this wave wrote to or started into LDS is there, for all waves.
-__device__ __forceinline__ void rows_ready() {
-    __builtin_amdgcn_s_waitcnt(0);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+// What this wave wrote to or read from LDS is done, for all waves.
+__device__ __forceinline__ void meet() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 struct WeightRegs {
@@ -424,100 +481,129 @@ struct WeightRegs {
     int s[kWaveTiles];
 };
 
-// Whole group q of `groups` from `now`, the loads of group q + 1 into `next` beside
-// it, and those of the weights two steps ahead.
+// Group `t` from `now`, the loads of the group after it, `u`, into `next` beside
+// it; the weights come two steps ahead.  Loads return in the order they were
+// issued, so the wait for the row scales, issued last, is the wait for the rows.
+// table: the thread's value for the next item's row table at `entry`, there behind
+// any group.
 template <int kPairs>
-__device__ __forceinline__ void group(const TileLoads& l, int q, int groups, Rows* __restrict__ now,
-                                      Rows* __restrict__ next, WeightRegs& r, v4f (*acc)[kWaveTiles]) {
-    // behind the last group: loads of nothing (the scalar offset stays in the arrays,
-    // since the range check subtracts it from their size)
-    const int qn = q + 1 < groups ? q + 1 : q;
-    const uint32_t off = q + 1 < groups ? 0 : kNowhere;
+__device__ __forceinline__ void group(const TileLoads& l, const Part& t, const Part& u, Rows* now, Rows* next,
+                                      WeightRegs& r, uint32_t* entry, uint32_t table, v4f (*acc)[kWaveTiles]) {
     int sc[2], ws[kWaveTiles], xs[2 * kPairs];
-    load_rows<kPairs>(l, qn, off, next);
-    load_row_scales<kPairs>(l, qn, off, sc);
-    load_weight_scales(l, qn, 4, off, ws);
+    RowAddresses ad;
+    row_addresses(l, u, ad);
 #pragma unroll
     for (int m = 0; m < 2 * kPairs; ++m) xs[m] = now->scales[m * 64 + l.lane];
     __builtin_amdgcn_sched_barrier(0);
-    step_products<kPairs, 0>(now, xs, r.w[0], r.s, 4, l.lane, acc);
+    load_rows(l, ad, 0, next);
+    load_rows(l, ad, 4, next);
+    load_weight_scales(l, u, ws);
     __builtin_amdgcn_sched_barrier(0);
-    load_weights(l, q, 2, 0, r.w[0]);
+    load_row_scales(l, u, ad, sc);
     __builtin_amdgcn_sched_barrier(0);
-    step_products<kPairs, 1>(now, xs, r.w[1], r.s, 4, l.lane, acc);
+    step_products<kPairs, 0>(now, xs, r.w[0], r.s, l.lane, acc);
     __builtin_amdgcn_sched_barrier(0);
-    load_weights(l, q, 3, 0, r.w[1]);
+    load_weights(l, t, 2, r.w[0]);
     __builtin_amdgcn_sched_barrier(0);
-    step_products<kPairs, 2>(now, xs, r.w[0], r.s, 4, l.lane, acc);
+    step_products<kPairs, 1>(now, xs, r.w[1], r.s, l.lane, acc);
     __builtin_amdgcn_sched_barrier(0);
-    load_weights(l, qn, 0, off, r.w[0]);
+    load_weights(l, t, 3, r.w[1]);
     __builtin_amdgcn_sched_barrier(0);
-    step_products<kPairs, 3>(now, xs, r.w[1], r.s, 4, l.lane, acc);
+    step_products<kPairs, 2>(now, xs, r.w[0], r.s, l.lane, acc);
     __builtin_amdgcn_sched_barrier(0);
-    load_weights(l, qn, 1, off, r.w[1]);
+    load_weights(l, u, 0, r.w[0]);
     __builtin_amdgcn_sched_barrier(0);
-    keep_row_scales<kPairs>(l, sc, next);
+    step_products<kPairs, 3>(now, xs, r.w[1], r.s, l.lane, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    load_weights(l, u, 1, r.w[1]);
+    __builtin_amdgcn_sched_barrier(0);
+    if (threadIdx.x < kRowTiles * 16) entry[threadIdx.x] = table;
+    keep_row_scales(l, u, ad, sc, next);
 #pragma unroll
     for (int f = 0; f < kWaveTiles; ++f) r.s[f] = ws[f];
-    rows_ready();
+    meet();
 }
 
-// The last group, where it is not whole: n steps of four.
+// All groups of an item, the last one beside the loads of the first group of the
+// item after it.
 template <int kPairs>
-__device__ __forceinline__ void last_group(const TileLoads& l, int q, Rows* __restrict__ b0, v4f (*acc)[kWaveTiles]) {
-    const int n = l.steps - 4 * q;
-    int sc[2], ws[kWaveTiles], xs[2 * kPairs];
-    v4i w[kWaveTiles];
-    load_rows<kPairs>(l, q, 0, b0);
-    load_weight_scales(l, q, n, 0, ws);
-    load_last_scales<kPairs>(l, q, n, sc);
-    keep_row_scales<kPairs>(l, sc, b0);
-    load_weights(l, q, 0, 0, w);
-    rows_ready();
+__device__ __forceinline__ void item_sums(const TileLoads& l, Part t, const Part& after, Rows* b, int& turn, WeightRegs& r,
+                                          uint32_t* entry, uint32_t table, v4f (*acc)[kWaveTiles]) {
+#pragma unroll 1
+    for (int q = 0; q < l.groups; ++q) {
+        t.q = q;
+        Part u = t;
+        u.q = q + 1;
+        if (q + 1 == l.groups) u = after;
+        group<kPairs>(l, t, u, b + turn, b + (turn ^ 1), r, entry, table, acc);
+        turn ^= 1;
+    }
+}
+
+// An item's results: two row tiles at a time through 8 KB of LDS of the wave's own
+// (`own`), so that neighbouring lanes store 16 bytes each of one row.  A row has
+// kUnits such units; unit c lies at c ^ row, for the banks' sake.
+template <typename T, bool kPaired>
+__device__ __forceinline__ void store_item(const ProductArgs& a, const Item& it, const Part& t, const TileLoads& l, v4f* own,
+                                           v4f (*acc)[kWaveTiles]) {
+    typedef T Piece __attribute__((ext_vector_type(4)));
+    constexpr int kOutputs = kWaveTiles * kMxTileRows / (kPaired ? 2 : 1), kPer = 16 / (int)sizeof(T);
+    constexpr int kUnits = kOutputs / kPer, kRows = 64 / kUnits;  // rows an instruction
+    const int r16 = l.lane % 16, g = l.lane / 16, n0 = t.t0 * kMxTileRows / (kPaired ? 2 : 1);
+    typedef T Unit __attribute__((ext_vector_type(kPer)));
+    const int c = l.lane % kUnits, n = n0 + c * kPer;
+    const bool whole = a.vec_out && n0 + kOutputs <= a.n_out;  // all of the wave's units are 16-byte stores
+    T* out = (T*)a.p.out;
 #pragma unroll
-    for (int m = 0; m < 2 * kPairs; ++m) xs[m] = b0->scales[m * 64 + l.lane];
-    step_products<kPairs, 0>(b0, xs, w, ws, n, l.lane, acc);
-    __builtin_amdgcn_sched_barrier(0);
-    if (n > 1) {
-        load_weights(l, q, 1, 0, w);
-        step_products<kPairs, 1>(b0, xs, w, ws, n, l.lane, acc);
-    }
-    if (n > 2) {
-        load_weights(l, q, 2, 0, w);
-        step_products<kPairs, 2>(b0, xs, w, ws, n, l.lane, acc);
-    }
-    if (n > 3) {
-        load_weights(l, q, 3, 0, w);
-        step_products<kPairs, 3>(b0, xs, w, ws, n, l.lane, acc);
-    }
-    rows_ready();
-}
-
-template <int kPairs>
-__device__ __forceinline__ void item_sums(const TileLoads& l, Rows* b0, Rows* b1, v4f (*acc)[kWaveTiles]) {
-    const int groups = l.blocks / 16;  // whole ones
-    int sc[2];
-    if (groups) {
-        WeightRegs r;
-        load_rows<kPairs>(l, 0, 0, b0);
-        load_row_scales<kPairs>(l, 0, 0, sc);
-        load_weight_scales(l, 0, 4, 0, r.s);
-        load_weights(l, 0, 0, 0, r.w[0]);
-        load_weights(l, 0, 1, 0, r.w[1]);
-        keep_row_scales<kPairs>(l, sc, b0);
-        rows_ready();
-        for (int q = 0; q < groups; q += 2) {
-            group<kPairs>(l, q, groups, b0, b1, r, acc);
-            if (q + 1 < groups) group<kPairs>(l, q + 1, groups, b1, b0, r, acc);
+    for (int h = 0; h < kRowTiles / 2; ++h) {
+        if (h >= t.pairs) continue;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int f = 0; f < kWaveTiles; f += kPaired ? 2 : 1) {
+                v4f v = acc[2 * h + m][f];
+                if (kPaired)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], acc[2 * h + m][f + 1][i]);
+                Piece o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = (T)v[i];
+                const int row = m * 16 + r16, piece = (kPaired ? f / 2 : f) * 4 + g, unit = piece * 4 / kPer;
+                *(Piece*)((char*)(own + row * kUnits + (unit ^ row % kUnits)) + piece * 4 % kPer * sizeof(T)) = o;
+            }
+        const int rows = it.rows - 32 * h, r0 = l.lane / kUnits;
+        T* to = out + (int64_t)(it.row0 + 32 * h + r0) * a.p.out_stride + n;
+        if (whole) {
+            v4f u[32 / kRows];
+#pragma unroll
+            for (int i = 0; i < 32 / kRows; ++i) u[i] = own[(i * kRows + r0) * kUnits + (c ^ (i * kRows + r0) % kUnits)];
+#pragma unroll
+            for (int i = 0; i < 32 / kRows; ++i)
+                if (i * kRows + r0 < rows) *(v4f*)(to + i * kRows * a.p.out_stride) = u[i];
+        } else {
+#pragma unroll 1
+            for (int r = r0; r < min(32, rows); r += kRows, to += kRows * a.p.out_stride) {
+                const Unit u = __builtin_bit_cast(Unit, own[r * kUnits + (c ^ r % kUnits)]);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (n + j < a.n_out) to[j] = u[j];
+            }
         }
     }
-    if (l.blocks % 16) last_group<kPairs>(l, groups, b0, acc);
 }
 
+__device__ __forceinline__ uint32_t first_block(const ProductArgs& a, const Item& it) {
+    if (threadIdx.x >= kRowTiles * 16) return 0;
+    int32_t s = it.row0 + min((int)threadIdx.x, it.rows - 1);
+    if (a.p.src) s = a.p.src[s];
+    return s < 0 || s >= a.p.x_rows ? kZeroRow : (uint32_t)s * (uint32_t)a.blocks;
+}
+
+template <typename T, bool kPaired>
 __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
     constexpr int MT = kRowTiles * 16;
-    __shared__ Rows b0, b1;
-    __shared__ uint32_t first[MT];
+    __shared__ Rows b[2];
+    __shared__ uint32_t first[2][MT];  // of this item and the next, in turn
     __shared__ List L;
     __shared__ int32_t wave_sum[kWaves];
     const MxProduct& p = a.p;
@@ -526,68 +612,85 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
     // workgroups of one XCD (every eighth) take one run of the items
     const int xcd = blockIdx.x % 8, per = gridDim.x / 8;
     const int64_t u1 = items * (xcd + 1) / 8;
+    int64_t u = items * xcd / 8 + blockIdx.x / 8;
+    if (u >= u1) return;
     TileLoads l;
-    l.codes = resource(p.codes, (uint32_t)(p.x_rows * a.blocks * 16));
+    l.codes = p.codes;
+    l.last_codes = (uint32_t)(p.x_rows * a.blocks * 16) - 16;
     l.scales = resource(p.scales, (uint32_t)(p.x_rows * a.blocks));
-    l.first = first;
+    l.last_scales = (uint32_t)(p.x_rows * a.blocks) - 4;
     l.blocks = a.blocks;
-    l.steps = a.steps;
+    l.groups = a.groups;
+    l.tiles = a.tiles;
+    l.tile_bytes = (int32_t)a.tile_bytes;
     l.lane = threadIdx.x % 64;
     l.wave = uniform(threadIdx.x / 64);
-    for (int64_t u = items * xcd / 8 + blockIdx.x / 8; u < u1; u += per) {
-        const Item it = find_item<MT, 2>(p, L, a.nb, u);
-        if (threadIdx.x < MT) {
-            int32_t s = it.row0 + min((int)threadIdx.x, it.rows - 1);
-            if (p.src) s = p.src[s];
-            first[threadIdx.x] = s < 0 || s >= p.x_rows ? 0u : (uint32_t)s * (uint32_t)a.blocks;
-        }
-        __syncthreads();
-        const int t0 = it.run * (kWaves * kWaveTiles) + l.wave * kWaveTiles, pairs = (it.rows + 31) / 32;
-        l.weights = resource(p.packed + it.e * p.stride, (uint32_t)(a.tiles * a.tile_bytes));
-#pragma unroll
-        for (int f = 0; f < kWaveTiles; ++f) l.tile[f] = (uint32_t)(min(t0 + f, a.tiles - 1) * a.tile_bytes);
+    auto part = [&](const Item& it, const uint32_t* table) {
+        Part t;
+        t.weights = resource(p.packed + it.e * p.stride, (uint32_t)(a.tiles * a.tile_bytes));
+        t.first = table;
+        t.t0 = it.run * (kWaves * kWaveTiles) + l.wave * kWaveTiles;
+        t.pairs = (it.rows + 31) / 32;
+        t.q = 0;
+        t.off = 0;
+        return t;
+    };
+
+    // the first item's first group
+    Item it = find_item<MT, 2>(p, L, a.nb, u);
+    if (threadIdx.x < MT) first[0][threadIdx.x] = first_block(a, it);
+    meet();
+    Part t = part(it, first[0]);
+    WeightRegs r;
+    int turn = 0, table = 0;
+    {
+        int sc[2];
+        RowAddresses ad;
+        row_addresses(l, t, ad);
+        load_rows(l, ad, 0, b);
+        load_rows(l, ad, 4, b);
+        load_weight_scales(l, t, r.s);
+        __builtin_amdgcn_sched_barrier(0);
+        load_row_scales(l, t, ad, sc);
+        load_weights(l, t, 0, r.w[0]);
+        load_weights(l, t, 1, r.w[1]);
+        keep_row_scales(l, t, ad, sc, b);
+    }
+    for (;;) {
+        const bool more = u + per < u1;
+        const Item then = more ? find_item<MT, 2>(p, L, a.nb, u + per) : it;
+        Part after = part(then, first[table ^ 1]);
+        if (!more) after.off = kNowhere;
+        uint32_t* entry = first[table ^ 1];
+        const uint32_t block = first_block(a, then);
+        // the only group already loads by the table
+        if (a.groups == 1 && threadIdx.x < MT) entry[threadIdx.x] = block;
+        meet();
         v4f acc[kRowTiles][kWaveTiles];
 #pragma unroll
         for (int m = 0; m < kRowTiles; ++m)
 #pragma unroll
             for (int f = 0; f < kWaveTiles; ++f) acc[m][f] = v4f{0, 0, 0, 0};
-        if (pairs == 1) item_sums<1>(l, &b0, &b1, acc);
-        else if (pairs == 2) item_sums<2>(l, &b0, &b1, acc);
-        else if (pairs == 3) item_sums<3>(l, &b0, &b1, acc);
-        else item_sums<4>(l, &b0, &b1, acc);
+        if (t.pairs == 1) item_sums<1>(l, t, after, b, turn, r, entry, block, acc);
+        else if (t.pairs == 2) item_sums<2>(l, t, after, b, turn, r, entry, block, acc);
+        else if (t.pairs == 3) item_sums<3>(l, t, after, b, turn, r, entry, block, acc);
+        else item_sums<4>(l, t, after, b, turn, r, entry, block, acc);
 
-        // Four row tiles at a time through 16 KB of LDS of the wave's own (nobody
-        // reads rows there now), so that a row's outputs are stored side by side.
-        // A row has 16 pieces of 4 outputs, piece c at c ^ row % 16 again.
-        v4f* own = (v4f*)((l.wave & 2 ? b1 : b0).codes) + (l.wave & 1) * 1024;
-        const int r16 = l.lane % 16, g = l.lane / 16;
-        const int width = p.paired ? 8 : 16, n0 = t0 * kMxTileRows / (p.paired ? 2 : 1);  // pieces, first output
+        v4f* own = (v4f*)b[turn ^ 1].codes + l.wave * 512;  // the buffer that the last group was read from
+        const bool zeros = __any((first[table][l.lane] | first[table][64 + l.lane]) & kZeroRow);
+        if (zeros) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (2 * half >= pairs) break;
+            for (int m = 0; m < kRowTiles; ++m)
+                if (first[table][m * 16 + l.lane % 16] & kZeroRow)
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int f = 0; f < kWaveTiles; f += 2) {
-                    v4f v = acc[4 * half + m][f], u = acc[4 * half + m][f + 1];
-                    v4f* row = own + (m * 16 + r16) * 16;
-                    if (p.paired) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], u[i]);
-                        row[(f / 2 * 4 + g) ^ r16] = v;
-                    } else {
-                        row[(f * 4 + g) ^ r16] = v;
-                        row[(f * 4 + 4 + g) ^ r16] = u;
-                    }
-                }
-            const int rows = min(64, it.rows - 64 * half), step = 64 / width;
-            for (int r = l.lane / width; r < rows; r += step) {
-                const int c = l.lane % width, to = it.row0 + 64 * half + r;
-                v4f v = own[r * 16 + (c ^ (r % 16))];
-                if (p.src && (uint64_t)(int64_t)p.src[to] >= (uint64_t)p.x_rows) v = v4f{0, 0, 0, 0};
-                if (n0 + 4 * c < a.n_out) store_out(a, to, n0 + 4 * c, v);
-            }
+                    for (int f = 0; f < kWaveTiles; ++f) acc[m][f] = v4f{0, 0, 0, 0};
         }
+        store_item<T, kPaired>(a, it, t, l, own, acc);
+        if (!more) return;
+        u += per;
+        it = then;
+        t = after;
+        table ^= 1;
     }
 }
 
@@ -627,8 +730,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 
 hipError_t launch_mx_pack(const uint8_t* codes, const uint8_t* scales, int32_t ne, int32_t rows, int32_t cols,
                           bool paired, uint8_t* packed, int64_t stride, hipStream_t st) {
-    const int groups = (cols + 4 * kMxStep - 1) / (4 * kMxStep);
-    const dim3 grid(groups, (uint32_t)mx_tiles(rows, paired), ne);
+    const dim3 grid((cols + 511) / 512, (uint32_t)mx_tiles(rows, paired), ne);
     hipLaunchKernelGGL(pack_kernel, grid, dim3(64), 0, st, codes, scales, rows, cols, paired ? 1 : 0, packed, stride,
                        mx_tile_bytes(cols));
     return hipGetLastError();
@@ -640,20 +742,27 @@ hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
     a.tile_bytes = mx_tile_bytes(p.cols);
     a.tiles = (int32_t)mx_tiles(p.n, p.paired != 0);
     a.n_out = p.paired ? p.n / 2 : p.n;
-    a.steps = (p.cols + kMxStep - 1) / kMxStep;
     a.blocks = p.cols / 32;
+    a.groups = (a.blocks + 15) / 16;
+    a.steps = a.blocks / 16 * 4 + std::min(4, a.blocks % 16);
     const size_t el = dtype_bytes(p.dtype);
-    a.vec_out = ((uintptr_t)p.out | (uintptr_t)(p.out_stride * (int64_t)el)) % (4 * el) == 0;
+    const uintptr_t align = (uintptr_t)p.out | (uintptr_t)(p.out_stride * (int64_t)el);
+    a.vec_out = align % 16 == 0;
+    a.vec_out4 = align % (4 * el) == 0;
     constexpr int NF = 4;
     const int64_t hit = p.rows < p.E ? p.rows : p.E;
-    if (p.rows <= 16 * (int64_t)p.E) {
+    if (p.rows <= 16 * (int64_t)p.E || p.x_rows * a.blocks < 4) {
         a.nb = (a.tiles + NF - 1) / NF;
         const int64_t n = (p.rows / 16 + hit) * a.nb, most = 256 * 4;
         hipLaunchKernelGGL((stream_kernel<1, NF>), dim3((uint32_t)(n < most ? n : most)), dim3(kThreads), 0, st, a);
     } else {
         a.nb = (a.tiles + kWaves * kWaveTiles - 1) / (kWaves * kWaveTiles);
         const int64_t n = (p.rows / (16 * kRowTiles) + hit) * a.nb, most = 256 * 2;
-        hipLaunchKernelGGL(tile_kernel, dim3((uint32_t)(n < most ? (n + 7) / 8 * 8 : most)), dim3(kThreads), 0, st, a);
+        const dim3 grid((uint32_t)(n < most ? (n + 7) / 8 * 8 : most));
+        auto kernel = p.dtype == kF32   ? (p.paired ? tile_kernel<float, true> : tile_kernel<float, false>)
+                      : p.dtype == kF16 ? (p.paired ? tile_kernel<_Float16, true> : tile_kernel<_Float16, false>)
+                                        : (p.paired ? tile_kernel<__bf16, true> : tile_kernel<__bf16, false>);
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, a);
     }
     return hipGetLastError();
 }

@@ -15,6 +15,7 @@ namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 
@@ -122,11 +123,13 @@ struct ProductArgs {
 };
 
 // The work list.  An item is one tile of MT rows of one expert times one run of
-// its outputs; items are numbered expert by expert, within an expert run by run,
-// and within a run tile by tile, so that the workgroups that read the same
-// weights run at about the same time.  pre[e] = row tiles of the experts below
+// its outputs; items are numbered expert by expert, within an expert kTogether
+// tiles by kTogether tiles, there run by run, and within a run tile by tile, so
+// that the workgroups that read the same weights or rows run at about the same
+// time (in one L2).  pre[e] = row tiles of the experts below
 // e; the caller's offsets are clamped to [0, rows], whatever they hold.
 constexpr int kMaxE = 1024;
+constexpr int kTogether = 8;
 struct List {
     int32_t pre[kMaxE + 1];
     int32_t row[kMaxE + 1];  // the clamped offsets
@@ -201,8 +204,11 @@ __device__ __forceinline__ Item find_item(const MxProduct& p, const List& L, int
     }
     e = uniform(e);
     const int32_t first = uniform(L.pre[e]), tiles = uniform(L.pre[e + 1]) - first;
-    const uint32_t left = (uint32_t)(u - (int64_t)first * nb);  // below tiles * nb < 2^31
-    const uint32_t run = left / (uint32_t)tiles, t = left - run * (uint32_t)tiles;
+    uint32_t left = (uint32_t)(u - (int64_t)first * nb);  // below tiles * nb < 2^31
+    const uint32_t wave = left / (uint32_t)(kTogether * nb);
+    left -= wave * (uint32_t)(kTogether * nb);
+    const uint32_t wide = min((uint32_t)kTogether, (uint32_t)tiles - wave * kTogether);
+    const uint32_t run = left / wide, t = wave * kTogether + left - run * wide;
     const int32_t r0 = uniform(L.row[e]), r1 = uniform(L.row[e + 1]);
     // rows dealt evenly to the tiles, in whole units of 16 kUnit
     const int32_t units = (r1 - r0 + 16 * kUnit - 1) / (16 * kUnit);
@@ -322,25 +328,25 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(ProductArgs a) {
 }
 
 // Many rows: the matrix unit bounds it, or the weights' bytes if an expert has a
-// few hundred rows.  A workgroup takes up to 8 tiles of rows (128) and 16 of
+// few hundred rows.  A workgroup takes up to 6 tiles of rows (96) and 16 of
 // weights, 4 to a wave.  The rows' codes of 512 reduction values (a group) go to
 // LDS while the group before is multiplied (two buffers); each wave reads its own
 // weights from memory straight into registers, a group ahead.  Row tiles come in
 // pairs: an item of fewer rows leaves out the pairs it lacks.
-constexpr int kRowTiles = 8;
+constexpr int kRowTiles = 6;
+constexpr int kTableRows = 128;  // of an item's row table: a multiple of the 64 rows of four scale tiles
 constexpr int kWaveTiles = 4;
 // [row][16 pieces]: 16 bytes a block; piece c of row r lies at c ^ r % 16, so that
 // the 16 rows that a product reads at one c lie in different banks.
 struct Rows {
     v4i codes[kRowTiles * 16 * 16];
-    int scales[kRowTiles * 64];  // [tile][lane]: the lane's scales of a group, byte s for step s
+    int scales[kTableRows / 16 * 64];  // [tile][lane]: the lane's scales of a group, byte s for step s
 };
 
 using Resource = __amdgpu_buffer_rsrc_t;
 __device__ __forceinline__ Resource resource(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
 }
-using GlobalPtr = const void __attribute__((address_space(1)))*;
 using LdsPtr = void __attribute__((address_space(3)))*;
 
 struct TileLoads {
@@ -367,34 +373,37 @@ constexpr uint32_t kZeroRow = 0x80000000u;
 // arrays: the range check subtracts them from the size.)
 constexpr uint32_t kNowhere = 0xf0000000u;
 
-// Start the loads of a group's rows: 4 rows of 256 bytes an instruction.  (All
-// table reads come before the first load: the compiler takes a read of LDS to
-// wait for the loads into it.)
+// A lane's byte offsets in x of an item's rows: of the 16 bytes that it loads in
+// each instruction (4 rows of 256 bytes), and of the scales of its two rows.
 struct RowAddresses {
     uint32_t codes[kRowTiles], scales[2];
 };
-__device__ __forceinline__ void row_addresses(const TileLoads& l, const Part& t, RowAddresses& ad) {
+__device__ __forceinline__ void row_addresses(const TileLoads& l, const uint32_t* first, RowAddresses& ad) {
 #pragma unroll
     for (int i = 0; i < kRowTiles; ++i) {
         const int r = (i * kWaves + l.wave) * 4 + l.lane / 16;
-        // a piece past the row's end is any of x: it meets weights of 0
-        ad.codes[i] = min((t.first[r] + t.q * 16 + ((l.lane % 16) ^ (r % 16))) * 16, l.last_codes);
+        ad.codes[i] = (first[r] + ((l.lane % 16) ^ (r % 16))) * 16;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) ad.scales[i] = t.first[(l.wave + 4 * i) * 16 + l.lane % 16] & ~kZeroRow;
+    for (int i = 0; i < 2; ++i) ad.scales[i] = first[(l.wave + 4 * i) * 16 + l.lane % 16] & ~kZeroRow;
 }
-// 16 bytes a lane from base + its offset to LDS at `to` + 16 lane.  The compiler
-// does not know of the load: its own waits count too few loads in flight, so they
-// wait for more than they need, never for less; the wait for these is at group().
-__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t off, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ void load_rows(const TileLoads& l, const RowAddresses& ad, int from, Rows* to) {
-    const uint32_t at = (uint32_t)(uintptr_t)(LdsPtr)to->codes + l.wave * 1024;
+// Start the loads of a pair of row tiles of group q.  In asm, so that the compiler
+// does not have every read of LDS wait for them: its own waits then count too few
+// loads in flight and wait for more than they need, never for less.  The wait for
+// these is that for the row scales, which are loaded behind them (loads return in
+// the order they were issued).  A piece past the row's end is any of x: it meets
+// weights of 0.
+__device__ __forceinline__ void load_pair(const TileLoads& l, const RowAddresses& ad, int q, int pair, uint32_t to) {
 #pragma unroll
-    for (int i = from; i < from + kRowTiles / 2; ++i) load_to_lds(l.codes, ad.codes[i], uniform(at) + i * kWaves * 1024);
+    for (int i = 2 * pair; i < 2 * pair + 2; ++i) {
+        const uint32_t at = min(ad.codes[i] + q * 256, l.last_codes);
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(to + (i * kWaves + l.wave) * 1024), "v"(at), "s"(l.codes)
+                     : "memory", "m0");
+    }
 }
+__device__ __forceinline__ uint32_t lds(const void* p) { return uniform((uint32_t)(uintptr_t)(LdsPtr)p); }
 
 // The scales of the rows of tiles wave and wave + 4: a lane's are neighbours, one
 // unaligned dword, read from at most the array's last four bytes.
@@ -425,13 +434,11 @@ __device__ __forceinline__ uint32_t weights_at(const TileLoads& l, const Part& t
     return (uint32_t)min(t.t0 + f, l.tiles - 1) * (uint32_t)l.tile_bytes + t.q * kMxGroupBytes;
 }
 // Step st of the wave's tiles; lanes without a block in it get zeros.
-__device__ __forceinline__ void load_weights(const TileLoads& l, const Part& t, int st, v4i* w) {
+__device__ __forceinline__ v4i load_weights(const TileLoads& l, const Part& t, int st, int f) {
     const int have = min(16, l.blocks - t.q * 16);
     const uint32_t off = (uint32_t)l.lane * 16 | (4 * (l.lane / 16) + st < have ? t.off : kNowhere);
-#pragma unroll
-    for (int f = 0; f < kWaveTiles; ++f)
-        w[f] = __builtin_bit_cast(
-            v4i, __builtin_amdgcn_raw_buffer_load_b128(t.weights, off, weights_at(l, t, f) + mx_step_at(have, st), 0));
+    return __builtin_bit_cast(
+        v4i, __builtin_amdgcn_raw_buffer_load_b128(t.weights, off, weights_at(l, t, f) + mx_step_at(have, st), 0));
 }
 __device__ __forceinline__ void load_weight_scales(const TileLoads& l, const Part& t, int* sc) {
     const int have = min(16, l.blocks - t.q * 16);
@@ -442,31 +449,67 @@ __device__ __forceinline__ void load_weight_scales(const TileLoads& l, const Par
 }
 
 // Keeps the products before it before it: they have no side effects, and the
-// compiler would gather those of a whole group behind the group's loads.
-__device__ __forceinline__ void stay(v4f* a) {
-    static_assert(kWaveTiles == 4, "one operand a tile");
-    asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
+// compiler would gather those of a whole group behind its loads.
+__device__ __forceinline__ void stay(v4f& a, v4f& b) { asm volatile("" : "+v"(a), "+v"(b)); }
+
+struct WeightRegs {
+    v4i w[4][kWaveTiles];  // [step]
+    int s[kWaveTiles];
+};
+struct Pair {
+    v4i x[2];
+};
+template <int ST>
+__device__ __forceinline__ Pair read_pair(const Rows* from, int lane, int pair) {
+    const int r16 = lane % 16;
+    const v4i* at = from->codes + r16 * 16 + ((4 * (lane / 16) + ST) ^ r16) + pair * 512;
+    return Pair{{at[0], at[256]}};
 }
 
-// Step ST of a group: the products of every row tile.
-template <int kPairs, int ST>
-__device__ __forceinline__ void step_products(const Rows* __restrict__ from, const int* xs, const v4i* w, const int* ws,
-                                              int lane, v4f (*acc)[kWaveTiles]) {
-    const int r16 = lane % 16;
-    const v4i* at = from->codes + r16 * 16 + ((4 * (lane / 16) + ST) ^ r16);
-    // each operand read two tiles ahead of its products, in this order
-    v4i x[3] = {at[0], at[256], {}};
+template <int ST>
+__device__ __forceinline__ v4f product(v4i w, v4i x, v4f c, int ws, int xs) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(x), c, 4, 4, ST, ws, ST, xs);
+}
+
+// Step ST of a group: the products of the item's pairs of row tiles, of which
+// `first` is read already; returns the first pair of the next step.  Between the
+// first pair's products the weights of step `load` of group u are loaded.
+template <int ST, int LOAD>
+__device__ __forceinline__ Pair step_products(const TileLoads& l, int pairs, const Rows* from, const Pair& first,
+                                              const int* xs, WeightRegs& r, const Part& u, v4f (*acc)[kWaveTiles]) {
+    static_assert(kRowTiles == 6, "three pairs");
+    Pair ahead{}, next = read_pair<ST>(from, l.lane, 1);
+    if (ST < 3) ahead = read_pair<ST + 1>(from, l.lane, 0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int m = 0; m < 2 * kPairs; ++m) {
+    for (int f = 0; f < kWaveTiles; ++f) {
+        acc[0][f] = product<ST>(r.w[ST][f], first.x[0], acc[0][f], r.s[f], xs[0]);
+        acc[1][f] = product<ST>(r.w[ST][f], first.x[1], acc[1][f], r.s[f], xs[1]);
+        stay(acc[0][f], acc[1][f]);
         __builtin_amdgcn_sched_barrier(0);
-        if (m + 2 < 2 * kPairs) x[(m + 2) % 3] = at[(m + 2) * 256];
+        r.w[LOAD][f] = load_weights(l, u, LOAD, f);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int f = 0; f < kWaveTiles; ++f)
-            acc[m][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[f]), operand(x[m % 3]), acc[m][f], 4, 4,
-                                                                         ST, ws[f], ST, xs[m]);
-        stay(acc[m]);
     }
+    if (pairs > 1) {
+        const Pair last = read_pair<ST>(from, l.lane, 2);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < kWaveTiles; ++f) {
+            acc[2][f] = product<ST>(r.w[ST][f], next.x[0], acc[2][f], r.s[f], xs[2]);
+            acc[3][f] = product<ST>(r.w[ST][f], next.x[1], acc[3][f], r.s[f], xs[3]);
+            stay(acc[2][f], acc[3][f]);
+        }
+        if (pairs > 2) {
+#pragma unroll
+            for (int f = 0; f < kWaveTiles; ++f) {
+                acc[4][f] = product<ST>(r.w[ST][f], last.x[0], acc[4][f], r.s[f], xs[4]);
+                acc[5][f] = product<ST>(r.w[ST][f], last.x[1], acc[5][f], r.s[f], xs[5]);
+                stay(acc[4][f], acc[5][f]);
+            }
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    return ahead;
 }
 
 // What this wave wrote to or read from LDS is done, for all waves.
@@ -476,48 +519,28 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-struct WeightRegs {
-    v4i w[2][kWaveTiles];  // steps of the same parity take turns
-    int s[kWaveTiles];
-};
-
 // Group `t` from `now`, the loads of the group after it, `u`, into `next` beside
-// it; the weights come two steps ahead.  Loads return in the order they were
-// issued, so the wait for the row scales, issued last, is the wait for the rows.
-// table: the thread's value for the next item's row table at `entry`, there behind
-// any group.
-template <int kPairs>
-__device__ __forceinline__ void group(const TileLoads& l, const Part& t, const Part& u, Rows* now, Rows* next,
-                                      WeightRegs& r, uint32_t* entry, uint32_t table, v4f (*acc)[kWaveTiles]) {
-    int sc[2], ws[kWaveTiles], xs[2 * kPairs];
-    RowAddresses ad;
-    row_addresses(l, u, ad);
+// it; each step's weights are loaded three steps ahead.  table: the thread's value
+// for the next item's row table at `entry`, there behind any group.
+__device__ __forceinline__ void group(const TileLoads& l, const Part& t, const Part& u, const RowAddresses& ad, Rows* now,
+                                      Rows* next, WeightRegs& r, uint32_t* entry, uint32_t table, v4f (*acc)[kWaveTiles]) {
+    int sc[2], ws[kWaveTiles], xs[kRowTiles];
+    const uint32_t to = lds(next->codes);
+    Pair x = read_pair<0>(now, l.lane, 0);
 #pragma unroll
-    for (int m = 0; m < 2 * kPairs; ++m) xs[m] = now->scales[m * 64 + l.lane];
-    __builtin_amdgcn_sched_barrier(0);
-    load_rows(l, ad, 0, next);
-    load_rows(l, ad, 4, next);
+    for (int m = 0; m < kRowTiles; ++m) xs[m] = now->scales[m * 64 + l.lane];
+    x = step_products<0, 3>(l, t.pairs, now, x, xs, r, t, acc);
+    load_pair(l, ad, u.q, 0, to);
+    x = step_products<1, 0>(l, t.pairs, now, x, xs, r, u, acc);
+    if (u.pairs > 1) load_pair(l, ad, u.q, 1, to);
     load_weight_scales(l, u, ws);
+    x = step_products<2, 1>(l, t.pairs, now, x, xs, r, u, acc);
+    if (u.pairs > 2) load_pair(l, ad, u.q, 2, to);
     __builtin_amdgcn_sched_barrier(0);
     load_row_scales(l, u, ad, sc);
     __builtin_amdgcn_sched_barrier(0);
-    step_products<kPairs, 0>(now, xs, r.w[0], r.s, l.lane, acc);
-    __builtin_amdgcn_sched_barrier(0);
-    load_weights(l, t, 2, r.w[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    step_products<kPairs, 1>(now, xs, r.w[1], r.s, l.lane, acc);
-    __builtin_amdgcn_sched_barrier(0);
-    load_weights(l, t, 3, r.w[1]);
-    __builtin_amdgcn_sched_barrier(0);
-    step_products<kPairs, 2>(now, xs, r.w[0], r.s, l.lane, acc);
-    __builtin_amdgcn_sched_barrier(0);
-    load_weights(l, u, 0, r.w[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    step_products<kPairs, 3>(now, xs, r.w[1], r.s, l.lane, acc);
-    __builtin_amdgcn_sched_barrier(0);
-    load_weights(l, u, 1, r.w[1]);
-    __builtin_amdgcn_sched_barrier(0);
-    if (threadIdx.x < kRowTiles * 16) entry[threadIdx.x] = table;
+    step_products<3, 2>(l, t.pairs, now, x, xs, r, u, acc);
+    if (threadIdx.x < kTableRows) entry[threadIdx.x] = table;
     keep_row_scales(l, u, ad, sc, next);
 #pragma unroll
     for (int f = 0; f < kWaveTiles; ++f) r.s[f] = ws[f];
@@ -526,21 +549,23 @@ __device__ __forceinline__ void group(const TileLoads& l, const Part& t, const P
 
 // All groups of an item, the last one beside the loads of the first group of the
 // item after it.
-template <int kPairs>
-__device__ __forceinline__ void item_sums(const TileLoads& l, Part t, const Part& after, Rows* b, int& turn, WeightRegs& r,
-                                          uint32_t* entry, uint32_t table, v4f (*acc)[kWaveTiles]) {
+__device__ __forceinline__ void item_sums(const TileLoads& l, Part t, const Part& after, RowAddresses& ad, Rows* b, int& turn,
+                                          WeightRegs& r, uint32_t* entry, uint32_t table, v4f (*acc)[kWaveTiles]) {
 #pragma unroll 1
     for (int q = 0; q < l.groups; ++q) {
         t.q = q;
         Part u = t;
         u.q = q + 1;
-        if (q + 1 == l.groups) u = after;
-        group<kPairs>(l, t, u, b + turn, b + (turn ^ 1), r, entry, table, acc);
+        if (q + 1 == l.groups) {
+            u = after;
+            if (!after.off) row_addresses(l, after.first, ad);
+        }
+        group(l, t, u, ad, b + turn, b + (turn ^ 1), r, entry, table, acc);
         turn ^= 1;
     }
 }
 
-// An item's results: two row tiles at a time through 8 KB of LDS of the wave's own
+// An item's results: a row tile at a time through 4 KB of LDS of the wave's own
 // (`own`), so that neighbouring lanes store 16 bytes each of one row.  A row has
 // kUnits such units; unit c lies at c ^ row, for the banks' sake.
 template <typename T, bool kPaired>
@@ -549,51 +574,49 @@ __device__ __forceinline__ void store_item(const ProductArgs& a, const Item& it,
     typedef T Piece __attribute__((ext_vector_type(4)));
     constexpr int kOutputs = kWaveTiles * kMxTileRows / (kPaired ? 2 : 1), kPer = 16 / (int)sizeof(T);
     constexpr int kUnits = kOutputs / kPer, kRows = 64 / kUnits;  // rows an instruction
-    const int r16 = l.lane % 16, g = l.lane / 16, n0 = t.t0 * kMxTileRows / (kPaired ? 2 : 1);
     typedef T Unit __attribute__((ext_vector_type(kPer)));
-    const int c = l.lane % kUnits, n = n0 + c * kPer;
+    const int r16 = l.lane % 16, g = l.lane / 16, n0 = t.t0 * kMxTileRows / (kPaired ? 2 : 1);
+    const int c = l.lane % kUnits, n = n0 + c * kPer, r0 = l.lane / kUnits;
     const bool whole = a.vec_out && n0 + kOutputs <= a.n_out;  // all of the wave's units are 16-byte stores
-    T* out = (T*)a.p.out;
+    T* out = (T*)a.p.out + (int64_t)(it.row0 + r0) * a.p.out_stride + n;
 #pragma unroll
-    for (int h = 0; h < kRowTiles / 2; ++h) {
-        if (h >= t.pairs) continue;
+    for (int m = 0; m < kRowTiles; ++m) {
+        if (m / 2 >= t.pairs) continue;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int f = 0; f < kWaveTiles; f += kPaired ? 2 : 1) {
+            v4f v = acc[m][f];
+            if (kPaired)
 #pragma unroll
-            for (int f = 0; f < kWaveTiles; f += kPaired ? 2 : 1) {
-                v4f v = acc[2 * h + m][f];
-                if (kPaired)
+                for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], acc[m][f + 1][i]);
+            Piece o;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], acc[2 * h + m][f + 1][i]);
-                Piece o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = (T)v[i];
-                const int row = m * 16 + r16, piece = (kPaired ? f / 2 : f) * 4 + g, unit = piece * 4 / kPer;
-                *(Piece*)((char*)(own + row * kUnits + (unit ^ row % kUnits)) + piece * 4 % kPer * sizeof(T)) = o;
-            }
-        const int rows = it.rows - 32 * h, r0 = l.lane / kUnits;
-        T* to = out + (int64_t)(it.row0 + 32 * h + r0) * a.p.out_stride + n;
+            for (int i = 0; i < 4; ++i) o[i] = (T)v[i];
+            const int piece = (kPaired ? f / 2 : f) * 4 + g, unit = piece * 4 / kPer;
+            *(Piece*)((char*)(own + r16 * kUnits + (unit ^ r16 % kUnits)) + piece * 4 % kPer * sizeof(T)) = o;
+        }
+        const int rows = it.rows - 16 * m;
         if (whole) {
-            v4f u[32 / kRows];
+            v4f u[16 / kRows];
 #pragma unroll
-            for (int i = 0; i < 32 / kRows; ++i) u[i] = own[(i * kRows + r0) * kUnits + (c ^ (i * kRows + r0) % kUnits)];
+            for (int i = 0; i < 16 / kRows; ++i) u[i] = own[(i * kRows + r0) * kUnits + (c ^ (i * kRows + r0) % kUnits)];
 #pragma unroll
-            for (int i = 0; i < 32 / kRows; ++i)
-                if (i * kRows + r0 < rows) *(v4f*)(to + i * kRows * a.p.out_stride) = u[i];
+            for (int i = 0; i < 16 / kRows; ++i)
+                if (i * kRows + r0 < rows) *(v4f*)(out + (16 * m + i * kRows) * a.p.out_stride) = u[i];
         } else {
 #pragma unroll 1
-            for (int r = r0; r < min(32, rows); r += kRows, to += kRows * a.p.out_stride) {
+            for (int r = r0; r < min(16, rows); r += kRows) {
                 const Unit u = __builtin_bit_cast(Unit, own[r * kUnits + (c ^ r % kUnits)]);
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    if (n + j < a.n_out) to[j] = u[j];
+                    if (n + j < a.n_out) out[(16 * m + r - r0) * a.p.out_stride + j] = u[j];
             }
         }
     }
 }
 
 __device__ __forceinline__ uint32_t first_block(const ProductArgs& a, const Item& it) {
-    if (threadIdx.x >= kRowTiles * 16) return 0;
+    if (threadIdx.x >= kTableRows) return 0;
     int32_t s = it.row0 + min((int)threadIdx.x, it.rows - 1);
     if (a.p.src) s = a.p.src[s];
     return s < 0 || s >= a.p.x_rows ? kZeroRow : (uint32_t)s * (uint32_t)a.blocks;
@@ -603,7 +626,7 @@ template <typename T, bool kPaired>
 __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
     constexpr int MT = kRowTiles * 16;
     __shared__ Rows b[2];
-    __shared__ uint32_t first[2][MT];  // of this item and the next, in turn
+    __shared__ uint32_t first[2][kTableRows];  // of this item and the next, in turn
     __shared__ List L;
     __shared__ int32_t wave_sum[kWaves];
     const MxProduct& p = a.p;
@@ -638,22 +661,25 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
 
     // the first item's first group
     Item it = find_item<MT, 2>(p, L, a.nb, u);
-    if (threadIdx.x < MT) first[0][threadIdx.x] = first_block(a, it);
+    if (threadIdx.x < kTableRows) first[0][threadIdx.x] = first_block(a, it);
     meet();
     Part t = part(it, first[0]);
     WeightRegs r;
+    RowAddresses ad;
     int turn = 0, table = 0;
     {
         int sc[2];
-        RowAddresses ad;
-        row_addresses(l, t, ad);
-        load_rows(l, ad, 0, b);
-        load_rows(l, ad, 4, b);
+        row_addresses(l, t.first, ad);
+#pragma unroll
+        for (int h = 0; h < kRowTiles / 2; ++h)
+            if (h < t.pairs) load_pair(l, ad, 0, h, lds(b[0].codes));
         load_weight_scales(l, t, r.s);
         __builtin_amdgcn_sched_barrier(0);
         load_row_scales(l, t, ad, sc);
-        load_weights(l, t, 0, r.w[0]);
-        load_weights(l, t, 1, r.w[1]);
+#pragma unroll
+        for (int f = 0; f < kWaveTiles; ++f)
+#pragma unroll
+            for (int st = 0; st < 3; ++st) r.w[st][f] = load_weights(l, t, st, f);
         keep_row_scales(l, t, ad, sc, b);
     }
     for (;;) {
@@ -664,19 +690,16 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
         uint32_t* entry = first[table ^ 1];
         const uint32_t block = first_block(a, then);
         // the only group already loads by the table
-        if (a.groups == 1 && threadIdx.x < MT) entry[threadIdx.x] = block;
+        if (a.groups == 1 && threadIdx.x < kTableRows) entry[threadIdx.x] = block;
         meet();
         v4f acc[kRowTiles][kWaveTiles];
 #pragma unroll
         for (int m = 0; m < kRowTiles; ++m)
 #pragma unroll
             for (int f = 0; f < kWaveTiles; ++f) acc[m][f] = v4f{0, 0, 0, 0};
-        if (t.pairs == 1) item_sums<1>(l, t, after, b, turn, r, entry, block, acc);
-        else if (t.pairs == 2) item_sums<2>(l, t, after, b, turn, r, entry, block, acc);
-        else if (t.pairs == 3) item_sums<3>(l, t, after, b, turn, r, entry, block, acc);
-        else item_sums<4>(l, t, after, b, turn, r, entry, block, acc);
+        item_sums(l, t, after, ad, b, turn, r, entry, block, acc);
 
-        v4f* own = (v4f*)b[turn ^ 1].codes + l.wave * 512;  // the buffer that the last group was read from
+        v4f* own = (v4f*)b[turn ^ 1].codes + l.wave * 256;  // the buffer that the last group was read from
         const bool zeros = __any((first[table][l.lane] | first[table][64 + l.lane]) & kZeroRow);
         if (zeros) {
 #pragma unroll

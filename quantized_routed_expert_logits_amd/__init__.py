@@ -656,41 +656,71 @@ def strata_moe_decode(x: torch.Tensor, router_w: torch.Tensor, experts: Experts,
 
 
 # ------------------------------------- 4-bit floating point, norms of a block
+# These calls take the GPU a few microseconds for a token, so their checks read
+# each tensor's properties once and go past torch's context managers.
+_Tensor = torch.Tensor
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _float_rows(t, name: str, rows: int | None = None, width: int | None = None) -> int:
     """A [rows][width] fp32, fp16 or bf16 tensor with contiguous rows that do not overlap -> its row stride."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in ROW_DTYPES:
         raise TypeError(f"{name} must be one of {sorted(str(d) for d in ROW_DTYPES)}, got {t.dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (width is not None and t.shape[1] != width):
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (width is not None and shape[1] != width):
         want = "2-D" if rows is None and width is None else (rows, width)
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
-    if (t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {want}")
+    n, w = shape
+    if t.is_contiguous():
+        return w
+    stride, col = t.stride()
+    if (w > 1 and n > 0 and col != 1) or (n > 1 and stride < w):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return stride if n > 1 else w
 
 
-def _mxfp_arrays(codes, scales, rows: int, cols: int) -> None:
-    for name, t, n in (("codes", codes, cols // 2), ("scales", scales, cols // 32)):
-        _expect(t, name, (rows, n), torch.uint8)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _array(t, name: str, shape: tuple, dt, dev: int):
+    """A contiguous tensor of this shape and type on device `dev`, or None -> its pointer."""
+    if t is None:
+        return None
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    return t.data_ptr()
 
 
-def _on_device(device, stream, call):
-    """call(stream) with `device` current; the stream is the device's current one if none is given."""
-    index = device.index
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(device):
-            return _on_device(device, stream, call)
-    return call(torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+def _same_device(t, name: str, dev: int):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
 
 
-def _made_on(device, stream):
-    """Where an output that a call allocates is allocated: the call's own stream."""
-    if stream is None:
-        return torch.cuda.device(device)
-    return torch.cuda.stream(stream)
+def _run_on(dev: int, stream, what: str, fn, *args) -> None:
+    """fn(*args, stream) with device `dev` current, on its current stream if none is given."""
+    if dev < 0:
+        raise TypeError(f"{what} takes CUDA (HIP) tensors")
+    st = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if _get_device() == dev:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, st)
+    if rc:
+        _check(rc, what)
+
+
+def _new_bytes(shape: tuple, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output that the call allocates, on the stream that it runs on."""
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=torch.uint8, device=like.device)
 
 
 def strata_moe_mxfp_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
@@ -699,29 +729,30 @@ def strata_moe_mxfp_quantize(x: torch.Tensor, codes: torch.Tensor | None = None,
     byte, and scales uint8 [rows][cols/32], powers of two."""
     xs = _float_rows(x, "x")
     rows, cols = x.shape
-    _one_device(x=x, codes=codes, scales=scales)
-    if codes is None or scales is None:
-        with _made_on(x.device, stream):
-            if codes is None:
-                codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
-            if scales is None:
-                scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
-    _mxfp_arrays(codes, scales, rows, cols)
-    _on_device(x.device, stream, lambda st: _check(
-        _lib.strata_moe_mxfp_quantize(x.data_ptr(), ROW_DTYPES[x.dtype], xs, rows, cols, codes.data_ptr(),
-                                      scales.data_ptr(), st), "strata_moe_mxfp_quantize"))
+    dev = x.get_device()
+    if dev < 0:
+        raise TypeError("x must be a CUDA (HIP) tensor")
+    if codes is None:
+        codes = _new_bytes((rows, cols // 2), x, stream)
+    if scales is None:
+        scales = _new_bytes((rows, cols // 32), x, stream)
+    _run_on(dev, stream, "strata_moe_mxfp_quantize", _lib.strata_moe_mxfp_quantize, x.data_ptr(), ROW_DTYPES[x.dtype], xs,
+            rows, cols, _array(codes, "codes", (rows, cols // 2), torch.uint8, dev),
+            _array(scales, "scales", (rows, cols // 32), torch.uint8, dev))
     return codes, scales
 
 
 def strata_moe_mxfp_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> torch.Tensor:
-    """The values that codes and scales stand for, into out [rows][cols] (fp32, fp16 or bf16)."""
+    """The values that codes and scales stand for, into out [rows][cols] (fp32, fp16 or bf16; rows may be padded)."""
     os_ = _float_rows(out, "out")
     rows, cols = out.shape
-    _mxfp_arrays(codes, scales, rows, cols)
-    _one_device(codes=codes, scales=scales, out=out)
-    _on_device(out.device, stream, lambda st: _check(
-        _lib.strata_moe_mxfp_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
-                                        ROW_DTYPES[out.dtype], os_, st), "strata_moe_mxfp_dequantize"))
+    dev = out.get_device()
+    if codes is None or scales is None:
+        raise TypeError("codes and scales must be torch tensors")
+    _run_on(dev, stream, "strata_moe_mxfp_dequantize", _lib.strata_moe_mxfp_dequantize,
+            _array(codes, "codes", (rows, cols // 2), torch.uint8, dev),
+            _array(scales, "scales", (rows, cols // 32), torch.uint8, dev), rows, cols, out.data_ptr(),
+            ROW_DTYPES[out.dtype], os_)
     return out
 
 
@@ -752,20 +783,18 @@ class MxfpWeights:
 
 
 def strata_moe_mxfp_pack(codes: torch.Tensor, scales: torch.Tensor, e0: int, weights: MxfpWeights, stream=None) -> None:
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
+    if not isinstance(codes, _Tensor) or codes.dim() != 3:
         raise ValueError("codes must be [n][rows][cols/2]")
-    n = codes.shape[0]
-    _expect(codes, "codes", (n, weights.rows, weights.cols // 2), torch.uint8)
-    _expect(scales, "scales", (n, weights.rows, weights.cols // 32), torch.uint8)
-    _one_device(codes=codes, scales=scales, packed=weights.packed)
+    if scales is None:
+        raise TypeError("scales must be a torch tensor")
+    n, dev = codes.shape[0], codes.get_device()
     if e0 < 0 or e0 + n > weights.n_expert:
         raise ValueError(f"experts [{e0}, {e0 + n}) outside [0, {weights.n_expert})")
-    if not codes.is_contiguous() or not scales.is_contiguous():
-        raise ValueError("codes and scales must be contiguous")
-    _on_device(codes.device, stream, lambda st: _check(
-        _lib.strata_moe_mxfp_pack(codes.data_ptr(), scales.data_ptr(), e0, e0 + n, weights.rows, weights.cols,
-                                  int(weights.swiglu), weights.packed.data_ptr(), weights.stride, st),
-        "strata_moe_mxfp_pack"))
+    args = (_array(codes, "codes", (n, weights.rows, weights.cols // 2), torch.uint8, dev),
+            _array(scales, "scales", (n, weights.rows, weights.cols // 32), torch.uint8, dev))
+    _same_device(weights.packed, "weights", dev)
+    _run_on(dev, stream, "strata_moe_mxfp_pack", _lib.strata_moe_mxfp_pack, *args, e0, e0 + n, weights.rows, weights.cols,
+            int(weights.swiglu), weights.packed.data_ptr(), weights.stride)
 
 
 def strata_moe_mxfp_product(codes: torch.Tensor, scales: torch.Tensor, weights: MxfpWeights, out: torch.Tensor,
@@ -776,25 +805,20 @@ def strata_moe_mxfp_product(codes: torch.Tensor, scales: torch.Tensor, weights: 
     x's row r."""
     if not isinstance(weights, MxfpWeights):
         raise TypeError("weights must be an MxfpWeights object")
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+    if not isinstance(codes, _Tensor) or codes.dim() != 2:
         raise ValueError("codes must be [x_rows][cols/2]")
+    if scales is None:
+        raise TypeError("scales must be a torch tensor")
     x_rows = codes.shape[0]
-    _mxfp_arrays(codes, scales, x_rows, weights.cols)
-    os_ = _float_rows(out, "out", width=weights.n_out)
-    rows = out.shape[0]
-    if offsets is not None:
-        _expect(offsets, "offsets", (weights.n_expert + 1,), torch.int32)
-    if src is not None:
-        _expect(src, "src", (rows,), torch.int32)
-    _one_device(codes=codes, scales=scales, packed=weights.packed, out=out, offsets=offsets, src=src)
-    for name, t in (("offsets", offsets), ("src", src)):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    _on_device(out.device, stream, lambda st: _check(
-        _lib.strata_moe_mxfp_product(codes.data_ptr(), scales.data_ptr(), x_rows, ctypes.byref(weights.struct),
-                                     None if offsets is None else offsets.data_ptr(),
-                                     None if src is None else src.data_ptr(), rows, out.data_ptr(),
-                                     ROW_DTYPES[out.dtype], os_, st), "strata_moe_mxfp_product"))
+    os_ = _float_rows(out, "out", None, weights.n_out)
+    rows, dev = out.shape[0], out.get_device()
+    args = (_array(codes, "codes", (x_rows, weights.cols // 2), torch.uint8, dev),
+            _array(scales, "scales", (x_rows, weights.cols // 32), torch.uint8, dev), x_rows,
+            ctypes.byref(weights.struct), _array(offsets, "offsets", (weights.n_expert + 1,), torch.int32, dev),
+            _array(src, "src", (rows,), torch.int32, dev))
+    _same_device(weights.packed, "weights", dev)
+    _run_on(dev, stream, "strata_moe_mxfp_product", _lib.strata_moe_mxfp_product, *args, rows, out.data_ptr(),
+            ROW_DTYPES[out.dtype], os_)
     return out
 
 
@@ -802,51 +826,53 @@ class Norm:
     """A root mean square norm: v / sqrt(mean(v^2) + eps) * (weight_offset + weight); weight [H] float32 or None."""
 
     def __init__(self, weight: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0):
+        self.width = self.device = None
         if weight is not None:
-            if not isinstance(weight, torch.Tensor) or weight.dim() != 1:
+            if not isinstance(weight, _Tensor) or weight.dim() != 1:
                 raise ValueError("weight must be a 1-D [H] tensor")
             _dtype(weight, torch.float32, "weight")
             if not weight.is_contiguous():
                 raise ValueError("weight must be contiguous")
+            self.width, self.device = weight.shape[0], weight.get_device()
         self.weight, self.eps, self.weight_offset = weight, eps, weight_offset
         self.struct = NormStruct(None if weight is None else weight.data_ptr(), weight_offset, eps)
+        self.pointer = ctypes.pointer(self.struct)
 
 
-def _check_norm(norm, name: str, H: int):
+def _norm(norm, name: str, H: int, dev: int):
+    """A Norm for rows of H, or None -> the pointer to its struct."""
+    if norm is None:
+        return None
     if not isinstance(norm, Norm):
         raise TypeError(f"{name} must be a Norm object")
     if norm.weight is not None:
-        _expect(norm.weight, f"{name}'s weight", (H,), torch.float32)
-    return norm.weight
+        if norm.width != H:
+            raise ValueError(f"{name} has a weight of {norm.width} values for rows of {H}")
+        if norm.device != dev:
+            raise ValueError(f"{name} is on another device")
+    return norm.pointer
 
 
-def _norm_outputs(x, codes, scales, T: int, H: int) -> None:
-    if x is not None:
-        _expect(x, "x", (T, H), torch.float32)
-        if not x.is_contiguous():
-            raise ValueError("x must be contiguous")
-    if (codes is None) != (scales is None):
+def _norm_outputs(x, codes, scales, T: int, H: int, dev: int) -> tuple:
+    if codes is None and scales is None:
+        return _array(x, "x", (T, H), torch.float32, dev), None, None
+    if codes is None or scales is None:
         raise ValueError("codes and scales come together")
-    if codes is not None:
-        _mxfp_arrays(codes, scales, T, H)
-
-
-def _opt(t):
-    return None if t is None else t.data_ptr()
+    return (_array(x, "x", (T, H), torch.float32, dev), _array(codes, "codes", (T, H // 2), torch.uint8, dev),
+            _array(scales, "scales", (T, H // 32), torch.uint8, dev))
 
 
 def strata_moe_norm_before(h: torch.Tensor, norm: Norm, x: torch.Tensor | None = None,
                            codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None) -> None:
     """x = norm(h): the layer's fp32 input from the residual stream h [T][H] (fp32, fp16 or bf16; rows may be
     padded), and with codes and scales (uint8, as strata_moe_mxfp_quantize) x in 4 bits."""
+    if norm is None:
+        raise TypeError("norm must be a Norm object")
     hs = _float_rows(h, "h")
     T, H = h.shape
-    weight = _check_norm(norm, "norm", H)
-    _norm_outputs(x, codes, scales, T, H)
-    _one_device(h=h, weight=weight, x=x, codes=codes, scales=scales)
-    _on_device(h.device, stream, lambda st: _check(
-        _lib.strata_moe_norm_before(h.data_ptr(), ROW_DTYPES[h.dtype], hs, T, H, ctypes.byref(norm.struct), _opt(x),
-                                    _opt(codes), _opt(scales), st), "strata_moe_norm_before"))
+    dev = h.get_device()
+    _run_on(dev, stream, "strata_moe_norm_before", _lib.strata_moe_norm_before, h.data_ptr(), ROW_DTYPES[h.dtype], hs, T, H,
+            _norm(norm, "norm", H, dev), *_norm_outputs(x, codes, scales, T, H, dev))
 
 
 def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, norm: Norm | None = None,
@@ -860,45 +886,47 @@ def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, n
     input x = next_norm(out) (x, codes and scales as in strata_moe_norm_before)."""
     hs = _float_rows(h, "h")
     T, H = h.shape
-    os_ = _float_rows(out, "out", T, H)
-    _dtype(out, h.dtype, "out")
-    ys = _float_rows(y, "y", width=H)
-    K = 0
+    dev = h.get_device()
+    if out is h:
+        os_ = hs
+    else:
+        os_ = _float_rows(out, "out", T, H)
+        if out.dtype is not h.dtype:
+            raise TypeError(f"out must be {h.dtype}, got {out.dtype}")
+        _same_device(out, "out", dev)
+    ys = _float_rows(y, "y", None, H)
+    _same_device(y, "y", dev)
+    K, slots, weights = 0, None, None
     if (slot is None) != (p is None):
         raise ValueError("slot and p come together")
     if slot is not None:
-        if not isinstance(slot, torch.Tensor) or slot.dim() != 2:
+        if not isinstance(slot, _Tensor) or slot.dim() != 2:
             raise ValueError("slot must be [T][K]")
         K = slot.shape[1]
-        _expect(slot, "slot", (T, K), torch.int32)
-        _expect(p, "p", (T, K), torch.float32)
-        if not slot.is_contiguous() or not p.is_contiguous():
-            raise ValueError("slot and p must be contiguous")
+        slots, weights = _array(slot, "slot", (T, K), torch.int32, dev), _array(p, "p", (T, K), torch.float32, dev)
     elif y.shape[0] != T:
         raise ValueError(f"y has {y.shape[0]} rows for {T} tokens")
-    grow = gcol = 0
+    gates, grow, gcol = None, 0, 0
     if gate is not None:
-        if not isinstance(gate, torch.Tensor):
+        if not isinstance(gate, _Tensor):
             raise TypeError("gate must be a torch tensor")
-        _dtype(gate, torch.float32, "gate")
-        if tuple(gate.shape) not in ((H,), (T, 1), (T, H)):
-            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {(H,)}, {(T, 1)} or {(T, H)}")
-        grow = gate.stride(0) if gate.dim() == 2 and T > 1 else 0
-        gcol = gate.stride(-1) if gate.shape[-1] > 1 else 0
+        if gate.dtype is not torch.float32:
+            raise TypeError(f"gate must be {torch.float32}, got {gate.dtype}")
+        shape = gate.shape
+        if shape != (H,) and shape != (T, 1) and shape != (T, H):
+            raise ValueError(f"gate has shape {tuple(shape)}, expected {(H,)}, {(T, 1)} or {(T, H)}")
+        stride = gate.stride()
+        grow = stride[0] if len(shape) == 2 and T > 1 else 0
+        gcol = stride[-1] if shape[-1] > 1 else 0
         if gcol not in (0, 1) or grow < 0:
             raise ValueError("gate must have contiguous or broadcast rows")
-    weight = None if norm is None else _check_norm(norm, "norm", H)
-    next_weight = None if next_norm is None else _check_norm(next_norm, "next_norm", H)
-    _norm_outputs(x, codes, scales, T, H)
-    _one_device(h=h, y=y, out=out, slot=slot, p=p, gate=gate, weight=weight, next_weight=next_weight, x=x,
-                codes=codes, scales=scales)
-    branch = BranchStruct(y.data_ptr(), ys, y.shape[0], ROW_DTYPES[y.dtype], K, _opt(slot), _opt(p),
-                          None if norm is None else ctypes.pointer(norm.struct), _opt(gate), grow, gcol,
-                          residual_scale, block_scale)
-    _on_device(h.device, stream, lambda st: _check(
-        _lib.strata_moe_norm_after(h.data_ptr(), ROW_DTYPES[h.dtype], hs, T, H, ctypes.byref(branch), out.data_ptr(),
-                                   os_, None if next_norm is None else ctypes.byref(next_norm.struct), _opt(x),
-                                   _opt(codes), _opt(scales), st), "strata_moe_norm_after"))
+        _same_device(gate, "gate", dev)
+        gates = gate.data_ptr()
+    branch = BranchStruct(y.data_ptr(), ys, y.shape[0], ROW_DTYPES[y.dtype], K, slots, weights,
+                          _norm(norm, "norm", H, dev), gates, grow, gcol, residual_scale, block_scale)
+    _run_on(dev, stream, "strata_moe_norm_after", _lib.strata_moe_norm_after, h.data_ptr(), ROW_DTYPES[h.dtype], hs, T, H,
+            ctypes.byref(branch), out.data_ptr(), os_, _norm(next_norm, "next_norm", H, dev),
+            *_norm_outputs(x, codes, scales, T, H, dev))
     return out
 
 

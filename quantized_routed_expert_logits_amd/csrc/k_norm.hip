@@ -7,8 +7,18 @@
 // A call has the part up to h', the part from h' (h' = h then), or both.
 //
 // One workgroup per token; its row stays in registers between the sums, so
-// every array is read or written once.  A thread holds runs of 4 neighbouring
-// columns, so 8 neighbouring threads hold the 32 columns of one 4-bit block.
+// every array is read or written once.  A thread holds runs of 8 neighbouring
+// columns, so 4 neighbouring threads hold the 32 columns of one 4-bit block; where
+// an array's rows do not take wide accesses (and no codes are written) it holds
+// single columns, neighbouring threads neighbouring ones.
+//
+// What bounds it: with few tokens the latency of a chain of loads (slots, rows,
+// the norms' sums), with many the memory, as far as enough tokens are in flight
+// per CU to cover that chain.  So a token has few waves with few registers: 8192
+// tokens of 2560, K = 10 bf16 rows, with the next norm and codes, take 160 us (671
+// MB, 4.2 TB/s); runs of 4 columns (twice the waves) took 213, and 5 or 10 rows
+// loaded before the first is used, which costs registers, 183 and 280.
+//
 // All arithmetic is in 64 bits and an output is rounded to fp32, and from there
 // to 16 bits: the stored stream and the 4-bit codes are those of the exact row
 // except where it lies within about 2^-50 of a border.  The memory bounds these
@@ -20,146 +30,223 @@ namespace strata_moe {
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr int kRun = 8;  // columns of a thread's run
 
 struct NormArgs {
     NormLaunch l;
-    int32_t vec_h, vec_y, vec_out, vec_x, vec_gate, vec_w, vec_u;  // rows of this array take 4-wide accesses
+    int32_t vec_h, vec_y, vec_out, vec_x, vec_gate, vec_w, vec_u;  // rows of this array take 16-byte accesses
 };
 
-// 4 columns from j on (columns at and past H: 0).
-template <typename T>
-__device__ __forceinline__ void load4(const T* row, int j, int H, bool vec, double* v) {
-    if (vec && j + 4 <= H) {
-        float f[4];
-        load4_vec(row + j, f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = f[i];
+// Column i of a thread's run c.
+template <bool kSingle>
+__device__ __forceinline__ int column(int c, int i) {
+    return kSingle ? (c * kRun + i) * (int)blockDim.x + (int)threadIdx.x : (c * (int)blockDim.x + (int)threadIdx.x) * kRun + i;
+}
+
+// A thread's run c of a row (columns at and past H: 0).
+template <bool kSingle, typename T>
+__device__ __forceinline__ void load_run(const T* row, int c, int H, bool vec, float* v) {
+    const int j = column<kSingle>(c, 0);
+    if (!kSingle && vec && j + kRun <= H) {
+        load8_vec(row + j, v);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = j + i < H ? (double)widen(row[j + i]) : 0.0;
+    for (int i = 0; i < kRun; ++i) v[i] = column<kSingle>(c, i) < H ? widen(row[column<kSingle>(c, i)]) : 0.0f;
+}
+template <bool kSingle>
+__device__ __forceinline__ void load_run(const void* base, int dtype, int64_t at, int c, int H, bool vec, float* v) {
+    if (dtype == kF32) load_run<kSingle>((const float*)base + at, c, H, vec, v);
+    else if (dtype == kF16) load_run<kSingle>((const _Float16*)base + at, c, H, vec, v);
+    else load_run<kSingle>((const __bf16*)base + at, c, H, vec, v);
+}
+template <bool kSingle>
+__device__ __forceinline__ void store_run(void* base, int dtype, int64_t at, int c, int H, bool vec, const float* v) {
+    if (!kSingle) {
+        const int j = column<kSingle>(c, 0);
+        if (dtype == kF32) store8<float, v4f>((float*)base + at, j, H, vec, v);
+        else if (dtype == kF16) store8<_Float16, v8h>((_Float16*)base + at, j, H, vec, v);
+        else store8<__bf16, v8b>((__bf16*)base + at, j, H, vec, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+        const int j = column<kSingle>(c, i);
+        if (j >= H) continue;
+        if (dtype == kF32) ((float*)base)[at + j] = v[i];
+        else if (dtype == kF16) ((_Float16*)base)[at + j] = (_Float16)v[i];
+        else ((__bf16*)base)[at + j] = (__bf16)v[i];
+    }
 }
 
-__device__ __forceinline__ void load4_any(const void* base, int dtype, int64_t at, int j, int H, bool vec, double* v) {
-    if (dtype == kF32) load4((const float*)base + at, j, H, vec, v);
-    else if (dtype == kF16) load4((const _Float16*)base + at, j, H, vec, v);
-    else load4((const __bf16*)base + at, j, H, vec, v);
+// v = sum_k p[t][k] y[slot[t][k]], k ascending.
+template <int NC, bool kSingle, typename T>
+__device__ __forceinline__ void gather(const NormArgs& a, int64_t t, double (*v)[kRun]) {
+    const NormLaunch& l = a.l;
+    constexpr int kBatch = 2;
+    for (int k0 = 0; k0 < l.K; k0 += kBatch) {
+        int row[kBatch];
+        float p[kBatch], y[kBatch][NC][kRun];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            row[b] = k0 + b < l.K ? l.slot[t * l.K + k0 + b] : -1;
+            p[b] = k0 + b < l.K ? l.p[t * l.K + k0 + b] : 0.0f;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t at = row[b] < 0 || row[b] >= l.y_rows ? 0 : row[b];  // a row to read; used if it is the slot's
+#pragma unroll
+            for (int c = 0; c < NC; ++c) load_run<kSingle>((const T*)l.y + at * l.y_stride, c, l.H, a.vec_y, y[b][c]);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (row[b] < 0 || row[b] >= l.y_rows) continue;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) v[c][i] = fma((double)p[b], (double)y[b][c][i], v[c][i]);
+        }
+    }
 }
 
 // The sum over the workgroup, in a fixed order, in every thread.  red: one
-// double per wave, not used by an earlier sum of the same kernel.
+// double per possible wave, not used by an earlier sum of the same kernel.
+constexpr int kMaxWaves = kMaxThreads / 64;
 __device__ __forceinline__ double block_sum(double s, double* red) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
     const int waves = blockDim.x / 64;
     if (waves == 1) return s;
     if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = s;
+    if ((int)threadIdx.x >= waves && threadIdx.x < kMaxWaves) red[threadIdx.x] = 0.0;
     __syncthreads();
-    s = 0.0;
-    for (int w = 0; w < waves; ++w) s += red[w];
+    s = red[0];
+#pragma unroll
+    for (int w = 1; w < kMaxWaves; ++w) s += red[w];
     return s;
 }
 
-template <int NC>
-__device__ __forceinline__ void apply_norm(double (*v)[4], const NormScale& n, bool vec, int H, double* red) {
+// 1 / sqrt(v): the unit's estimate and two Newton steps, which square its error
+// (2^-25 or less) twice; at 0 and infinity the estimate is the result.
+__device__ __forceinline__ double inverse_root(double v) {
+    const double e = __builtin_amdgcn_rsq(v);
+    double r = e;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = r * fma(-0.5 * v * r, r, 1.5);
+    return __builtin_isfinite(r) ? r : e;
+}
+
+template <int NC, bool kSingle>
+__device__ __forceinline__ void apply_norm(double (*v)[kRun], const NormScale& n, bool vec, int H, double* red) {
+    float w[NC][kRun];
+    if (n.weight)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) load_run<kSingle>(n.weight, c, H, vec, w[c]);
     double s = 0.0;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s = fma(v[c][i], v[c][i], s);
+        for (int i = 0; i < kRun; ++i) s = fma(v[c][i], v[c][i], s);
     s = block_sum(s, red);
-    const double r = 1.0 / sqrt(s / H + n.eps);
+    const double r = inverse_root(s / H + n.eps);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        double w[4] = {1.0, 1.0, 1.0, 1.0};
-        const int j = (c * blockDim.x + threadIdx.x) * 4;
-        if (n.weight) {
-            load4(n.weight, j, H, vec, w);
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] += n.offset;
+        for (int i = 0; i < kRun; ++i) {
+            v[c][i] *= r;
+            if (n.weight) v[c][i] *= n.offset + (double)w[c][i];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[c][i] = v[c][i] * r * w[i];
-    }
 }
 
-template <int NC>
+template <int NC, bool kSingle>
 __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
-    __shared__ double red[2][kMaxThreads / 64];
+    __shared__ double red[2][kMaxWaves];
     const NormLaunch& l = a.l;
     const int H = l.H;
     const int64_t t = blockIdx.x;
-    double v[NC][4], h[NC][4];
+    double v[NC][kRun], h[NC][kRun];
+    float in[NC][kRun];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) load_run<kSingle>(l.h, l.dtype, t * l.h_stride, c, H, a.vec_h, in[c]);
     if (l.y) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[c][i] = 0.0;
         if (l.slot) {
-            for (int k = 0; k < l.K; ++k) {
-                const int row = l.slot[t * l.K + k];
-                if (row < 0 || row >= l.y_rows) continue;
-                const double p = l.p[t * l.K + k];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    double y[4];
-                    load4_any(l.y, l.y_dtype, row * l.y_stride, (c * blockDim.x + threadIdx.x) * 4, H, a.vec_y, y);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[c][i] = fma(p, y[i], v[c][i]);
-                }
-            }
-        } else {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                load4_any(l.y, l.y_dtype, t * l.y_stride, (c * blockDim.x + threadIdx.x) * 4, H, a.vec_y, v[c]);
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) v[c][i] = 0.0;
+            if (l.y_dtype == kF32) gather<NC, kSingle, float>(a, t, v);
+            else if (l.y_dtype == kF16) gather<NC, kSingle, _Float16>(a, t, v);
+            else gather<NC, kSingle, __bf16>(a, t, v);
+        } else {
+            float y[NC][kRun];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) load_run<kSingle>(l.y, l.y_dtype, t * l.y_stride, c, H, a.vec_y, y[c]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) v[c][i] = y[c][i];
         }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-        load4_any(l.h, l.dtype, t * l.h_stride, (c * blockDim.x + threadIdx.x) * 4, H, a.vec_h, h[c]);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) h[c][i] = in[c][i];
     if (l.y) {
-        if (l.after.on) apply_norm<NC>(v, l.after, a.vec_w, H, red[0]);
+        if (l.after.on) apply_norm<NC, kSingle>(v, l.after, a.vec_w, H, red[0]);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int j = (c * blockDim.x + threadIdx.x) * 4;
-            double g[4] = {1.0, 1.0, 1.0, 1.0};
+            float g[kRun], o[kRun];
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) g[i] = 1.0f;
             if (l.gate) {
                 const float* gr = l.gate + t * l.gate_row_stride;
-                if (l.gate_col_stride) load4(gr, j, H, a.vec_gate, g);
-                else g[0] = g[1] = g[2] = g[3] = *gr;
-            }
-            float o[4];
+                if (l.gate_col_stride) load_run<kSingle>(gr, c, H, a.vec_gate, g);
+                else
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kRun; ++i) g[i] = *gr;
+            }
+#pragma unroll
+            for (int i = 0; i < kRun; ++i)
                 h[c][i] = round_to(fma(l.residual_scale, h[c][i], l.block_scale * (g[i] * v[c][i])), l.dtype, &o[i]);
-            store4_any(l.out, l.dtype, t * l.out_stride, j, H, a.vec_out, o);
+            store_run<kSingle>(l.out, l.dtype, t * l.out_stride, c, H, a.vec_out, o);
         }
     }
     if (!l.before.on) return;
-    apply_norm<NC>(h, l.before, a.vec_u, H, red[1]);
+    apply_norm<NC, kSingle>(h, l.before, a.vec_u, H, red[1]);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int j = (c * blockDim.x + threadIdx.x) * 4;
-        float o[4];
+        float o[kRun];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = (float)h[c][i];
-        if (l.x) store4_any(l.x, kF32, t * H, j, H, a.vec_x, o);
-        if (l.codes) {  // H is a multiple of 32, so a block's 8 threads are all inside or all outside
+        for (int i = 0; i < kRun; ++i) o[i] = (float)h[c][i];
+        if (l.x) store_run<kSingle>(l.x, kF32, t * H, c, H, a.vec_x, o);
+        if (!kSingle && l.codes) {  // H is a multiple of 32, so a block's 4 threads are all inside or all outside
+            const int j = column<kSingle>(c, 0);
             uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(o[i]) & 0x7fffffffu);
+            for (int i = 0; i < kRun; ++i) top = max(top, __float_as_uint(o[i]) & 0x7fffffffu);
             top = max(top, (uint32_t)__shfl_xor((int)top, 1));
             top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-            top = max(top, (uint32_t)__shfl_xor((int)top, 4));
             const uint32_t byte = mx_scale_byte(top);
             if (j < H) {
                 uint32_t q = mx_code_pair<0>(0, o[0], o[1], byte);
                 q = mx_code_pair<1>(q, o[2], o[3], byte);
-                *(uint16_t*)(l.codes + (t * H + j) / 2) = byte == 255 ? 0 : (uint16_t)q;
-                if (threadIdx.x % 8 == 0) l.scales[(t * H + j) / 32] = (uint8_t)byte;
+                q = mx_code_pair<2>(q, o[4], o[5], byte);
+                q = mx_code_pair<3>(q, o[6], o[7], byte);
+                *(uint32_t*)(l.codes + (t * H + j) / 2) = byte == 255 ? 0 : q;
+                if (threadIdx.x % 4 == 0) l.scales[(t * H + j) / 32] = (uint8_t)byte;
             }
         }
     }
+}
+
+template <bool kSingle>
+hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
+    const int runs = (a.l.H + kRun - 1) / kRun;
+    const int threads = runs >= kMaxThreads ? kMaxThreads : (runs + 63) / 64 * 64;
+    const dim3 grid((uint32_t)a.l.T), block(threads);
+    if (runs <= threads) hipLaunchKernelGGL((norm_kernel<1, kSingle>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((norm_kernel<2, kSingle>), grid, block, 0, st, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -168,8 +255,9 @@ hipError_t launch_norm(const NormLaunch& l, hipStream_t st) {
     NormArgs a{};
     a.l = l;
     auto vec = [](const void* p, int64_t stride, size_t el) {
-        return ((uintptr_t)p | (uintptr_t)(stride * (int64_t)el)) % (4 * el) == 0 ? 1 : 0;
+        return ((uintptr_t)p | (uintptr_t)(stride * (int64_t)el)) % 16 == 0 ? 1 : 0;
     };
+    static_assert(kNormMaxH <= 2 * kMaxThreads * kRun, "two runs a thread");
     a.vec_h = vec(l.h, l.h_stride, dtype_bytes(l.dtype));
     a.vec_out = vec(l.out, l.out_stride, dtype_bytes(l.dtype));
     a.vec_y = vec(l.y, l.y_stride, dtype_bytes(l.y_dtype));
@@ -177,13 +265,8 @@ hipError_t launch_norm(const NormLaunch& l, hipStream_t st) {
     a.vec_gate = vec(l.gate, l.gate_row_stride, 4);
     a.vec_w = vec(l.after.weight, 0, 4);
     a.vec_u = vec(l.before.weight, 0, 4);
-    const int chunks = (l.H + 3) / 4;
-    const int threads = chunks >= kMaxThreads ? kMaxThreads : (chunks + 63) / 64 * 64;
-    const dim3 grid((uint32_t)l.T), block(threads);
-    if (chunks <= threads) hipLaunchKernelGGL(norm_kernel<1>, grid, block, 0, st, a);
-    else if (chunks <= 2 * threads) hipLaunchKernelGGL(norm_kernel<2>, grid, block, 0, st, a);
-    else hipLaunchKernelGGL(norm_kernel<4>, grid, block, 0, st, a);
-    return hipGetLastError();
+    const bool wide = l.H % kRun == 0 && a.vec_h && a.vec_out && a.vec_y && a.vec_x && a.vec_gate && a.vec_w && a.vec_u;
+    return wide || l.codes ? launch_rows<false>(a, st) : launch_rows<true>(a, st);
 }
 
 }  // namespace strata_moe

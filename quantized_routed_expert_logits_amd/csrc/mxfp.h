@@ -9,6 +9,8 @@ namespace strata_moe {
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(_Float16 v) { return (float)v; }
@@ -29,6 +31,23 @@ __device__ __forceinline__ void load4_vec(const __bf16* p, float* v) {
     v[2] = __uint_as_float(f.y << 16), v[3] = __uint_as_float(f.y & 0xffff0000u);
 }
 
+// 8 values from a 16-byte aligned row.
+__device__ __forceinline__ void load8_vec(const float* p, float* v) {
+    load4_vec(p, v);
+    load4_vec(p + 4, v + 4);
+}
+__device__ __forceinline__ void load8_vec(const _Float16* p, float* v) {
+    const v8h f = *(const v8h*)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)f[i];
+}
+__device__ __forceinline__ void load8_vec(const __bf16* p, float* v) {
+    const uint4 f = *(const uint4*)p;
+    const uint32_t u[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+}
+
 // v (4 values that are exact in type T) to columns j..j+3 of a row of H.
 template <typename T, typename V>
 __device__ __forceinline__ void store4(T* row, int j, int H, bool vec, const float* v) {
@@ -44,6 +63,25 @@ __device__ __forceinline__ void store4(T* row, int j, int H, bool vec, const flo
         if (j + i < H) row[j + i] = (T)v[i];
 }
 typedef float v4f __attribute__((ext_vector_type(4)));
+
+// v (8 values) to columns j..j+7 of a row of H, 16 bytes a store.
+template <typename T, typename V>
+__device__ __forceinline__ void store8(T* row, int j, int H, bool vec, const float* v) {
+    constexpr int n = 16 / (int)sizeof(T);
+    if (vec && j + 8 <= H) {
+#pragma unroll
+        for (int k = 0; k < 8; k += n) {
+            V o;
+#pragma unroll
+            for (int i = 0; i < n; ++i) o[i] = (T)v[k + i];
+            *(V*)(row + j + k) = o;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (j + i < H) row[j + i] = (T)v[i];
+}
 
 __device__ __forceinline__ void store4_any(void* base, int dtype, int64_t at, int j, int H, bool vec, const float* v) {
     if (dtype == kF32) store4<float, v4f>((float*)base + at, j, H, vec, v);

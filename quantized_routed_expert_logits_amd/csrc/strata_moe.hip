@@ -16,6 +16,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -852,14 +853,13 @@ int check_norm_rows(const void* h, int32_t dtype, int64_t h_stride, int64_t T, i
 
 // No two of the written arrays, and none of them and a read one, share an
 // element (a null array never does).
-int check_apart(const std::vector<RowSet>& written, const std::vector<RowSet>& read) {
-    for (size_t i = 0; i < written.size(); ++i) {
-        if (!written[i].base) continue;
-        for (size_t j = i + 1; j < written.size(); ++j)
-            if (written[j].base && overlap(written[i], written[j]))
-                return fail(STRATA_MOE_EINVAL, "two of the call's outputs overlap");
+int check_apart(std::initializer_list<RowSet> written, std::initializer_list<RowSet> read) {
+    for (const RowSet* w = written.begin(); w != written.end(); ++w) {
+        if (!w->base) continue;
+        for (const RowSet* o = w + 1; o != written.end(); ++o)
+            if (o->base && overlap(*w, *o)) return fail(STRATA_MOE_EINVAL, "two of the call's outputs overlap");
         for (const RowSet& r : read)
-            if (r.base && overlap(written[i], r)) return fail(STRATA_MOE_EINVAL, "an output overlaps an input");
+            if (r.base && overlap(*w, r)) return fail(STRATA_MOE_EINVAL, "an output overlaps an input");
     }
     return 0;
 }

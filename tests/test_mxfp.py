@@ -367,12 +367,13 @@ def test_packed_bytes_refuses(qm, rows, cols, swiglu):
 def test_packed_bytes(qm):
     # a multiple of 16 rows and 512 columns is held in 4.25 bits a value
     assert qm.strata_moe_mxfp_packed_bytes(2048, 2560, True) == 2048 * 2560 * 17 // 32
-    assert qm.strata_moe_mxfp_packed_bytes(1, 32) == 1024 + 256
+    # 16 rows of 32 values: 256 bytes of codes, and a group's scales
+    assert qm.strata_moe_mxfp_packed_bytes(1, 32) == 256 + 256
     _refused(qm, qm.library().strata_moe_mxfp_packed_bytes(8, 64, 0, None), -1)
 
 
 @pytest.mark.parametrize("change", [
-    dict(e0=-1), dict(e0=3, e1=2), dict(e1=1025), dict(stride=1024), dict(stride=1300), dict(codes=None), dict(scales=None),
+    dict(e0=-1), dict(e0=3, e1=2), dict(e1=1025), dict(stride=512), dict(stride=1300), dict(codes=None), dict(scales=None),
     dict(packed=None), dict(codes=PTR + 8), dict(packed=(8 << 20) + 128), dict(codes=8 << 20), dict(scales=(8 << 20) + 2600),
     dict(rows=0), dict(cols=33),
 ], ids=str)
@@ -384,7 +385,7 @@ def test_pack_refuses(qm, change):
 
 @pytest.mark.parametrize("change,code", [
     (dict(weights=None), -1), (dict(E=0), -1), (dict(E=1025), -1), (dict(n=0), -1), (dict(cols=72), -1), (dict(swiglu=3), -1),
-    (dict(n=7, swiglu=1), -1), (dict(stride=1024), -1), (dict(stride=1281), -1), (dict(rows=-1), -1),
+    (dict(n=7, swiglu=1), -1), (dict(stride=512), -1), (dict(stride=1281), -1), (dict(rows=-1), -1),
     (dict(rows=(1 << 24) + 1), -1), (dict(x_rows=-1), -1), (dict(x_rows=(1 << 24) + 1, src=7 << 20), -1),
     (dict(dtype=9), -2), (dict(out_stride=7), -1), (dict(offsets=None), -1), (dict(rows=21), -1), (dict(x_rows=0, src=7 << 20), -1),
     (dict(x_rows=1 << 24, cols=512, stride=5120, src=7 << 20), -1), (dict(codes=None), -1), (dict(scales=None), -1),

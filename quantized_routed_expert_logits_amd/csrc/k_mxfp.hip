@@ -118,11 +118,12 @@ struct ProductArgs {
     int32_t blocks, groups; // of 32 and of 512 reduction values
     int32_t steps;          // matrix-unit products along the reduction
     int32_t nb;             // work items along the outputs
+    int32_t item_rows;      // rows of a work item, at most
     int32_t vec_out;        // rows of out take 16-byte stores
     int32_t vec_out4;       // ... stores of four outputs
 };
 
-// The work list.  An item is one tile of MT rows of one expert times one run of
+// The work list.  An item is one tile of at most mt rows of one expert times one run of
 // its outputs; items are numbered expert by expert, within an expert kTogether
 // tiles by kTogether tiles, there run by run, and within a run tile by tile, so
 // that the workgroups that read the same weights or rows run at about the same
@@ -136,31 +137,27 @@ struct List {
 };
 __device__ __forceinline__ int32_t clamp_row(int32_t v, int32_t rows) { return v < 0 ? 0 : v > rows ? rows : v; }
 
-template <int MT>
-__device__ __forceinline__ void make_list(const MxProduct& p, List& L, int32_t* wave_sum) {
+__device__ __forceinline__ void make_list(const MxProduct& p, int mt, List& L, int32_t* wave_sum) {
     if (!p.offsets) {
         if (threadIdx.x == 0) {
             L.pre[0] = L.row[0] = 0;
-            L.pre[1] = (int32_t)((p.rows + MT - 1) / MT);
+            L.pre[1] = ((int32_t)p.rows + mt - 1) / mt;
             L.row[1] = (int32_t)p.rows;
         }
         __syncthreads();
         return;
     }
-    constexpr int kPer = kMaxE / kThreads;
-    int32_t n[kPer], s = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
-        n[i] = 0;
-        if (e < p.E) {
-            const int32_t a = clamp_row(p.offsets[e], (int32_t)p.rows), b = clamp_row(p.offsets[e + 1], (int32_t)p.rows);
-            n[i] = b > a ? (b - a + MT - 1) / MT : 0;
-            L.row[e] = a;
-            if (e == p.E - 1) L.row[p.E] = b;
-        }
-        s += n[i];
-    }
+    // a thread takes a run of experts, its first sum the scan's
+    const int per = (p.E + (int)blockDim.x - 1) / (int)blockDim.x, rows = (int)p.rows;
+    const int e0 = threadIdx.x * per, e1 = min(p.E, e0 + per);
+    auto tiles = [&](int e, int32_t* first) {
+        const int32_t a = clamp_row(p.offsets[e], rows), b = clamp_row(p.offsets[e + 1], rows);
+        *first = a;
+        if (e == p.E - 1) L.row[p.E] = b;
+        return b > a ? (b - a + mt - 1) / mt : 0;
+    };
+    int32_t s = 0, row;
+    for (int e = e0; e < e1; ++e) s += tiles(e, &row);
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     int32_t inc = s;
 #pragma unroll
@@ -172,25 +169,23 @@ __device__ __forceinline__ void make_list(const MxProduct& p, List& L, int32_t* 
     __syncthreads();
     int32_t at = inc - s;
     for (int w = 0; w < wave; ++w) at += wave_sum[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
-        if (e <= p.E) L.pre[e] = at;
-        at += n[i];
+    for (int e = e0; e < e1; ++e) {
+        L.pre[e] = at;
+        at += tiles(e, &row);
+        L.row[e] = row;
     }
-    // E = 1024: the last entry has no thread of its own
-    if (threadIdx.x == kThreads - 1 && p.E == kMaxE) L.pre[kMaxE] = at;
+    if (e1 == p.E && e0 < e1) L.pre[p.E] = at;
     __syncthreads();
 }
 
 // Wave-uniform, in scalar registers.
 struct Item {
     int32_t e, run, row0;
-    int32_t rows;  // 1 .. MT
+    int32_t rows;
 };
 __device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <int MT, int kUnit>
+template <int kUnit>
 __device__ __forceinline__ Item find_item(const MxProduct& p, const List& L, int nb, int64_t u) {
     const int lane = threadIdx.x % 64;
     Item it;
@@ -237,94 +232,131 @@ __device__ __forceinline__ void store_out(const ProductArgs& a, int32_t row, int
     store4_any(a.p.out, a.p.dtype, row * a.p.out_stride, n, a.n_out, a.vec_out4, f);
 }
 
-// Few rows: the weights' bytes bound it.  A workgroup's 4 waves share NF tiles
-// of weights (16 NF rows) and MF tiles of rows, each a quarter of the steps; the
-// quarters are added in wave order through LDS.
-constexpr int kWaves = 4;
-template <int MF, int NF>
-__global__ __launch_bounds__(kThreads) void stream_kernel(ProductArgs a) {
-    constexpr int MT = MF * 16;
-    __shared__ List L;
-    __shared__ int32_t wave_sum[kWaves];
-    __shared__ v4f part[kWaves][MF * NF][64];
+// Few rows: latency bounds it.  An item is up to 16 rows of an expert times kFewTiles
+// tiles of its weights.  A wave takes up to four steps at a time, so with a wave
+// for every four of them all loads of an item are in flight together; the waves'
+// sums are added in wave order through LDS.
+// kList: the items of the work list, shared out.  Otherwise a workgroup per row
+// and run, which looks the row's expert up and works if the row begins one of the
+// expert's tiles: no list, no scan, the offsets and the rows' sources in one
+// round of loads.
+constexpr int kFewWaves = 8;
+constexpr int kFewTiles = 4;
+
+__device__ __forceinline__ void few_item(const ProductArgs& a, int e, int run, int row, int rows, int src, int wave,
+                                         int waves, v4f (*part)[kFewTiles][64]) {
     const MxProduct& p = a.p;
-    make_list<MT>(p, L, wave_sum);
-    const int64_t items = (int64_t)uniform(L.pre[p.E]) * a.nb;
-    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), r16 = lane % 16, g = lane / 16;
-    const int s0 = a.steps * wave / kWaves, s1 = a.steps * (wave + 1) / kWaves;
-    for (int64_t u = blockIdx.x; u < items; u += gridDim.x) {
-        const Item it = find_item<MT, 1>(p, L, a.nb, u);
-        const uint8_t* wt[NF];
+    const int lane = threadIdx.x % 64, r16 = lane % 16, g = lane / 16;
+    const uint8_t* wt[kFewTiles];
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
-            wt[f] = p.packed + it.e * p.stride + min(it.run * NF + f, a.tiles - 1) * a.tile_bytes;
-        int64_t src[MF];
+    for (int f = 0; f < kFewTiles; ++f)
+        wt[f] = p.packed + e * p.stride + min(run * kFewTiles + f, a.tiles - 1) * a.tile_bytes;
+    v4f acc[kFewTiles];
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            src[m] = -1;
-            const int r = m * 16 + r16;
-            if (r < it.rows) {
-                src[m] = p.src ? p.src[it.row0 + r] : it.row0 + r;
-                if (src[m] >= p.x_rows) src[m] = -1;
-            }
-        }
-        v4f acc[MF][NF];
+    for (int f = 0; f < kFewTiles; ++f) acc[f] = v4f{0, 0, 0, 0};
+    const int s1 = a.steps * (wave + 1) / waves;
+    constexpr int kAtOnce = 4;
+    for (int s0 = a.steps * wave / waves; s0 < s1; s0 += kAtOnce) {
+        v4i w[kAtOnce][kFewTiles], x[kAtOnce];
+        int ws[kAtOnce][kFewTiles], xs[kAtOnce];
 #pragma unroll
-        for (int m = 0; m < MF; ++m)
+        for (int i = 0; i < kAtOnce; ++i) {
+            // step st of group q, which has `have` blocks (for a step past the wave's, its last again)
+            const int s = min(s0 + i, s1 - 1), q = s / 4, st = s % 4, have = min(16, a.blocks - q * 16);
+            const bool mine = 4 * g + st < have;
 #pragma unroll
-            for (int f = 0; f < NF; ++f) acc[m][f] = v4f{0, 0, 0, 0};
-        for (int s = s0; s < s1; ++s) {
-            // step st of group q, which has `have` blocks
-            const int q = s / 4, st = s % 4, have = min(16, a.blocks - q * 16);
-            const int b = 4 * g + st;
-            v4i w[NF], x[MF];
-            int ws[NF], xs[MF];
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
+            for (int f = 0; f < kFewTiles; ++f) {
                 const uint8_t* at = wt[f] + (int64_t)q * kMxGroupBytes;
-                w[f] = v4i{0, 0, 0, 0};
-                if (b < have) w[f] = *(const v4i*)(at + mx_step_at(have, st) + lane * 16);
-                ws[f] = *(const int*)(at + have * kMxBlockBytes + lane * 4) >> (8 * st);
+                w[i][f] = v4i{0, 0, 0, 0};
+                if (mine) w[i][f] = *(const v4i*)(at + mx_step_at(have, st) + lane * 16);
+                ws[i][f] = *(const int*)(at + have * kMxBlockBytes + lane * 4) >> (8 * st);
             }
-#pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                x[m] = v4i{0, 0, 0, 0};
-                xs[m] = 0;
-                if (src[m] >= 0 && b < have) {
-                    x[m] = ((const v4i*)p.codes)[src[m] * a.blocks + q * 16 + b];
-                    xs[m] = p.scales[src[m] * a.blocks + q * 16 + b];
-                }
+            x[i] = v4i{0, 0, 0, 0};
+            xs[i] = 0;
+            if (src >= 0 && r16 < rows && mine && s0 + i < s1) {
+                const int64_t b = (int64_t)src * a.blocks + q * 16 + 4 * g + st;
+                x[i] = ((const v4i*)p.codes)[b];
+                xs[i] = p.scales[b];
             }
-#pragma unroll
-            for (int m = 0; m < MF; ++m)
-#pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    acc[m][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[f]), operand(x[m]), acc[m][f],
-                                                                                 4, 4, 0, ws[f], 0, xs[m]);
         }
 #pragma unroll
-        for (int m = 0; m < MF; ++m)
+        for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-            for (int f = 0; f < NF; ++f) part[wave][m * NF + f][lane] = acc[m][f];
-        __syncthreads();
-        // outputs: lane holds row lane % 16 and 4 consecutive outputs of a tile
-        const int per = p.paired ? 2 : 1;
-        for (int o = wave; o < MF * NF / per; o += kWaves) {
-            const int m = o / (NF / per), f = o % (NF / per) * per;
-            v4f v = part[0][m * NF + f][lane];
-            for (int w = 1; w < kWaves; ++w) v += part[w][m * NF + f][lane];
-            if (p.paired) {
-                v4f up = part[0][m * NF + f + 1][lane];
-                for (int w = 1; w < kWaves; ++w) up += part[w][m * NF + f + 1][lane];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], up[i]);
-            }
-            const int r = m * 16 + r16;
-            const int n = (it.run * NF + f) / per * kMxTileRows + 4 * g;
-            if (r < it.rows && n < a.n_out) store_out(a, it.row0 + r, n, v);
-        }
-        __syncthreads();
+            for (int f = 0; f < kFewTiles; ++f)
+                if (s0 + i < s1)
+                    acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[i][f]), operand(x[i]), acc[f], 4, 4, 0,
+                                                                              ws[i][f], 0, xs[i]);
     }
+#pragma unroll
+    for (int f = 0; f < kFewTiles; ++f) part[wave][f][lane] = acc[f];
+    __syncthreads();
+    // outputs: lane holds row lane % 16 and 4 consecutive outputs of a tile
+    const int per = p.paired ? 2 : 1;
+    for (int f = wave * per; f < kFewTiles; f += waves * per) {
+        v4f v = part[0][f][lane];
+        for (int w = 1; w < waves; ++w) v += part[w][f][lane];
+        if (p.paired) {
+            v4f up = part[0][f + 1][lane];
+            for (int w = 1; w < waves; ++w) up += part[w][f + 1][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], up[i]);
+        }
+        const int n = (run * kFewTiles + f) / per * kMxTileRows + 4 * g;
+        if (r16 < rows && n < a.n_out) store_out(a, row + r16, n, v);
+    }
+}
+
+// The lane's row of x for row `row` + lane % 16 of the output, or -1.
+__device__ __forceinline__ int few_source(const MxProduct& p, int row) {
+    int src = row + (int)(threadIdx.x % 16);
+    if (src >= p.rows) return -1;
+    if (p.src) src = p.src[src];
+    return src >= p.x_rows ? -1 : src;
+}
+
+template <bool kList>
+__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(ProductArgs a) {
+    __shared__ v4f part[kFewWaves][kFewTiles][64];
+    const MxProduct& p = a.p;
+    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), waves = blockDim.x / 64, rows = (int)p.rows;
+    if constexpr (kList) {
+        __shared__ List L;
+        __shared__ int32_t wave_sum[kFewWaves];
+        make_list(p, kMxTileRows, L, wave_sum);
+        const int64_t items = (int64_t)uniform(L.pre[p.E]) * a.nb;
+        for (int64_t u = blockIdx.x; u < items; u += gridDim.x) {
+            const Item it = find_item<1>(p, L, a.nb, u);
+            few_item(a, it.e, it.run, it.row0, it.rows, few_source(p, it.row0), wave, waves, part);
+            __syncthreads();
+        }
+        return;
+    }
+    const int row = p.offsets ? blockIdx.y : blockIdx.y * kMxTileRows;
+    const int src = few_source(p, row);
+    int e = 0, end = rows;
+    if (p.offsets) {
+        e = -1;
+        for (int e0 = 0; e0 < p.E && e < 0; e0 += 256) {
+            int lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = e0 + i * 64 + lane;
+                lo[i] = k < p.E ? p.offsets[k] : 0;
+                hi[i] = k < p.E ? p.offsets[k + 1] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = row - clamp_row(lo[i], rows);
+                const uint64_t has = __ballot(at >= 0 && at % kMxTileRows == 0 && row < clamp_row(hi[i], rows));
+                if (!has || e >= 0) continue;
+                const int k = __builtin_ctzll(has);
+                e = e0 + i * 64 + k;
+                end = clamp_row(__builtin_amdgcn_readlane(hi[i], k), rows);
+            }
+        }
+        if (e < 0) return;
+    }
+    few_item(a, e, blockIdx.x, row, min(kMxTileRows, end - row), src, wave, waves, part);
 }
 
 // Many rows: the matrix unit bounds it, or the weights' bytes if an expert has a
@@ -333,6 +365,7 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(ProductArgs a) {
 // LDS while the group before is multiplied (two buffers); each wave reads its own
 // weights from memory straight into registers, a group ahead.  Row tiles come in
 // pairs: an item of fewer rows leaves out the pairs it lacks.
+constexpr int kWaves = 4;
 constexpr int kRowTiles = 6;
 constexpr int kTableRows = 128;  // of an item's row table: a multiple of the 64 rows of four scale tiles
 constexpr int kWaveTiles = 4;
@@ -400,7 +433,7 @@ __device__ __forceinline__ void load_pair(const TileLoads& l, const RowAddresses
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                      :
                      : "s"(to + (i * kWaves + l.wave) * 1024), "v"(at), "s"(l.codes)
-                     : "memory", "m0");
+                     : "memory");
     }
 }
 __device__ __forceinline__ uint32_t lds(const void* p) { return uniform((uint32_t)(uintptr_t)(LdsPtr)p); }
@@ -624,13 +657,12 @@ __device__ __forceinline__ uint32_t first_block(const ProductArgs& a, const Item
 
 template <typename T, bool kPaired>
 __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
-    constexpr int MT = kRowTiles * 16;
     __shared__ Rows b[2];
     __shared__ uint32_t first[2][kTableRows];  // of this item and the next, in turn
     __shared__ List L;
     __shared__ int32_t wave_sum[kWaves];
     const MxProduct& p = a.p;
-    make_list<MT>(p, L, wave_sum);
+    make_list(p, a.item_rows, L, wave_sum);
     const int64_t items = (int64_t)uniform(L.pre[p.E]) * a.nb;
     // workgroups of one XCD (every eighth) take one run of the items
     const int xcd = blockIdx.x % 8, per = gridDim.x / 8;
@@ -660,7 +692,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
     };
 
     // the first item's first group
-    Item it = find_item<MT, 2>(p, L, a.nb, u);
+    Item it = find_item<2>(p, L, a.nb, u);
     if (threadIdx.x < kTableRows) first[0][threadIdx.x] = first_block(a, it);
     meet();
     Part t = part(it, first[0]);
@@ -684,7 +716,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
     }
     for (;;) {
         const bool more = u + per < u1;
-        const Item then = more ? find_item<MT, 2>(p, L, a.nb, u + per) : it;
+        const Item then = more ? find_item<2>(p, L, a.nb, u + per) : it;
         Part after = part(then, first[table ^ 1]);
         if (!more) after.off = kNowhere;
         uint32_t* entry = first[table ^ 1];
@@ -772,15 +804,37 @@ hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
     const uintptr_t align = (uintptr_t)p.out | (uintptr_t)(p.out_stride * (int64_t)el);
     a.vec_out = align % 16 == 0;
     a.vec_out4 = align % (4 * el) == 0;
-    constexpr int NF = 4;
-    const int64_t hit = p.rows < p.E ? p.rows : p.E;
-    if (p.rows <= 16 * (int64_t)p.E || p.x_rows * a.blocks < 4) {
-        a.nb = (a.tiles + NF - 1) / NF;
-        const int64_t n = (p.rows / 16 + hit) * a.nb, most = 256 * 4;
-        hipLaunchKernelGGL((stream_kernel<1, NF>), dim3((uint32_t)(n < most ? n : most)), dim3(kThreads), 0, st, a);
+    // The kernel by the number of its items, at most (us, MI355X; few: a workgroup
+    // per row and run / the list / the tiles of many rows):
+    //   one token, ten experts, 2560 -> 2 x 1024 (320 lookups)   7.8 / 12.9 / 11.0
+    //   two tokens (640)                                        14.8 / 21.1 / 15.3
+    //   128 rows, 2560 -> 2560, one matrix (320)                 6.9 /  9.9 /  8.9
+    //   256 rows (640)                                           9.7 / 13.4 /  9.1
+    //   406 rows, six experts, 544 -> 333 (2436; 930 steps)      7.4 /  5.9 /  8.5
+    //   2000 rows, the same (786 items of 5 steps)              25.2 /  7.5 /  9.1
+    //   2048 rows, 16 experts, 512 -> 2 x 640 (2880 of 4)       47.8 / 22.9 /  8.2
+    const int64_t hit = p.rows < p.E ? p.rows : p.E, few_runs = (a.tiles + kFewTiles - 1) / kFewTiles;
+    auto tiles = [&](int mt) { return p.offsets ? p.rows / mt + hit : (p.rows + mt - 1) / mt; };
+    const int64_t lookups = p.offsets ? p.rows : tiles(kMxTileRows), listed = tiles(kMxTileRows) * few_runs;
+    const dim3 few(64 * std::min(kFewWaves, (a.steps + 3) / 4));
+    if (lookups * few_runs <= 512) {
+        a.nb = (int32_t)few_runs;
+        hipLaunchKernelGGL(few_kernel<false>, dim3((uint32_t)few_runs, (uint32_t)lookups), few, 0, st, a);
+    } else if (listed * a.steps <= 6000 || p.x_rows * a.blocks < 4) {  // (tile_kernel reads scales by four)
+        a.nb = (int32_t)few_runs;
+        const int64_t most = 256 * 4;
+        hipLaunchKernelGGL(few_kernel<true>, dim3((uint32_t)(listed < most ? listed : most)), few, 0, st, a);
     } else {
+        // As few rows an item as still leave every CU at most one (512 rows, 2560 ->
+        // 2560: 9.5 us with 32, 12.5 with 96), or the most (8192 rows: 54 and 39).
         a.nb = (a.tiles + kWaves * kWaveTiles - 1) / (kWaves * kWaveTiles);
-        const int64_t n = (p.rows / (16 * kRowTiles) + hit) * a.nb, most = 256 * 2;
+        a.item_rows = 16 * kRowTiles;
+        for (int mt = 32; mt < 16 * kRowTiles; mt += 32)
+            if (tiles(mt) * a.nb <= 256) {
+                a.item_rows = mt;
+                break;
+            }
+        const int64_t n = tiles(a.item_rows) * a.nb, most = 256 * 2;
         const dim3 grid((uint32_t)(n < most ? (n + 7) / 8 * 8 : most));
         auto kernel = p.dtype == kF32   ? (p.paired ? tile_kernel<float, true> : tile_kernel<float, false>)
                       : p.dtype == kF16 ? (p.paired ? tile_kernel<_Float16, true> : tile_kernel<_Float16, false>)

@@ -721,8 +721,10 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(ProductArgs a) {
         if (!more) after.off = kNowhere;
         uint32_t* entry = first[table ^ 1];
         const uint32_t block = first_block(a, then);
-        // the only group already loads by the table
-        if (a.groups == 1 && threadIdx.x < kTableRows) entry[threadIdx.x] = block;
+        if (a.groups == 1) {  // the only group already loads by the table
+            meet();           // which other waves read to store the item before
+            if (threadIdx.x < kTableRows) entry[threadIdx.x] = block;
+        }
         meet();
         v4f acc[kRowTiles][kWaveTiles];
 #pragma unroll

@@ -190,6 +190,98 @@ def test_product_by_expert(qm, size):
         _check_product(qm, xc, xs, wc, ws, out, swiglu=swiglu, offsets=_offsets(E, rows, rows, how), src=src)
 
 
+# On both sides of each border between the product's kernels (by rows and runs of
+# 64 weight rows, then by 16-row tiles, runs and steps) and between the item sizes
+# of the kernel of many rows.
+BORDERS = [  # rows, cols, n, E (0: no offsets)
+    (512, 64, 60, 7), (513, 64, 60, 7), (512, 96, 1024, 0), (513, 96, 1024, 0),
+    (592, 512, 2560, 0), (593, 512, 2560, 0), (6000, 32, 1024, 0), (6001, 32, 1024, 0),
+    (2048, 512, 1024, 0), (2049, 512, 1024, 0), (4096, 512, 1000, 0), (4097, 512, 1000, 0),
+    (1984, 1024, 700, 8), (2048, 1024, 700, 3), (9000, 512, 700, 8),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", BORDERS, ids=lambda s: "-".join(map(str, s)))
+def test_borders_between_kernels(qm, size):
+    rows, cols, n, E = size
+    xc, xs, wc, ws = _operands(rows, cols, n, E or 1, seed=rows + n)
+    out = torch.full((rows, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    _check_product(qm, xc, xs, wc, ws, out, offsets=_offsets(E, rows, rows) if E else None)
+
+
+MANY = [  # rows, x rows (0: no src), cols, n, E, how, swiglu: all taken by the kernel of many rows
+    (3600, 0, 544, 334, 0, "", True), (1500, 0, 640, 2047, 0, "", False), (1300, 0, 4128, 515, 0, "", False),
+    (4000, 400, 512, 256, 1024, "random", True), (4000, 0, 672, 250, 1024, "hot", False), (4000, 203, 544, 334, 6, "random", True),
+    (2600, 7, 1056, 400, 5, "one", False), (5000, 4, 32, 2048, 4, "random", False), (7000, 11, 96, 1024, 3, "hot", True),
+    (1800, 257, 2560, 96, 64, "random", True), (3000, 3001, 480, 512, 2, "random", False), (1000, 0, 1536, 1100, 1, "one", True),
+    (20000, 0, 512, 640, 3, "random", False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("size", MANY, ids=lambda s: "-".join(map(str, s)))
+def test_product_of_many_rows(qm, size, dtype):
+    """With rows that src names twice or not at all, or that lie outside x, with
+    output rows that do and do not take 16-byte stores, and with scales that begin
+    at an odd byte."""
+    rows, x_rows, cols, n, E, how, swiglu = size
+    xc, xs, wc, ws = _operands(x_rows or rows, cols, n, E or 1, seed=rows)
+    odd = torch.full((xs.numel() + 1,), 255, dtype=torch.uint8, device="cuda")[1:].view(xs.shape)
+    odd.copy_(xs)
+    src = None
+    if x_rows:
+        g = torch.Generator().manual_seed(3)
+        src = torch.randint(0, x_rows, (rows,), generator=g).int()
+        src[torch.randint(0, rows, (9,), generator=g)] = -1
+        src[torch.randint(0, rows, (9,), generator=g)] = x_rows
+        src = src.cuda()
+    n_out = n // 2 if swiglu else n
+    offsets = _offsets(E, rows, rows, how) if E else None
+    weights = qm.MxfpWeights(max(E, 1), n, cols, swiglu=swiglu).pack(0, wc, ws)
+    outs = []
+    for pad in (3, 16 + -n_out % 16):
+        buf = torch.full((rows, n_out + pad), 7.0, dtype=dtype, device="cuda")
+        _check_product(qm, xc, odd, wc, ws, buf[:, :n_out], swiglu=swiglu, offsets=offsets, src=src, weights=weights)
+        assert torch.all(buf[:, n_out:] == 7.0)
+        outs.append(buf[:, :n_out])
+    assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [512, 544])
+def test_runs_of_rows_outside_x(qm, cols):
+    """Several items in turn per workgroup, of which every other one has rows that
+    count as zeros, and the ones between have none."""
+    rows, n = 24000, 1024
+    xc, xs, wc, ws = _operands(300, cols, n, 1, seed=12)
+    r = torch.arange(rows)
+    src = torch.where(r // 96 % 2 == 1, (r % 5 - 1) * 1000, r % 300).int()  # outside x but for 0
+    out = torch.full((rows, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    _check_product(qm, xc, xs, wc, ws, out, src=src.cuda())
+
+
+@pytest.mark.gpu
+def test_two_products_at_once(qm):
+    """The same weights and rows on two streams, and one of few rows beside them."""
+    xc, xs, wc, ws = _operands(2000, 640, 400, 6, seed=13)
+    w = qm.MxfpWeights(6, 400, 640).pack(0, wc, ws)
+    off = _offsets(6, 2000, 4)
+    want = qm.strata_moe_mxfp_product(xc, xs, w, torch.empty((2000, 400), device="cuda"), offsets=off)
+    small = torch.tensor([0, 2, 2, 3, 3, 3, 4], dtype=torch.int32, device="cuda")
+    few = qm.strata_moe_mxfp_product(xc[:4], xs[:4], w, torch.empty((4, 400), device="cuda"), offsets=small)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [torch.zeros((2000, 400), device="cuda") for _ in range(2)] + [torch.zeros((4, 400), device="cuda")]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, o in zip(streams, outs):
+            k = o.shape[0]
+            qm.strata_moe_mxfp_product(xc[:k], xs[:k], w, o, offsets=off if k > 4 else small, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want) and torch.equal(outs[2], few)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows", [40, 900])
 def test_rows_of_no_expert_are_left(qm, rows):

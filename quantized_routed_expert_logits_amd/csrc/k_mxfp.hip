@@ -635,7 +635,8 @@ __device__ __forceinline__ void store_item(const ProductArgs& a, const Item& it,
             for (int i = 0; i < 16 / kRows; ++i) u[i] = own[(i * kRows + r0) * kUnits + (c ^ (i * kRows + r0) % kUnits)];
 #pragma unroll
             for (int i = 0; i < 16 / kRows; ++i)
-                if (i * kRows + r0 < rows) *(v4f*)(out + (16 * m + i * kRows) * a.p.out_stride) = u[i];
+                if (i * kRows + r0 < rows)  // past the caches: nobody reads them in this call
+                    __builtin_nontemporal_store(u[i], (v4f*)(out + (16 * m + i * kRows) * a.p.out_stride));
         } else {
 #pragma unroll 1
             for (int r = r0; r < min(16, rows); r += kRows) {

@@ -23,6 +23,8 @@
 // to 16 bits: the stored stream and the 4-bit codes are those of the exact row
 // except where it lies within about 2^-50 of a border.  The memory bounds these
 // kernels, so the wider arithmetic is free.
+#include <algorithm>
+
 #include "block.h"
 #include "mxfp.h"
 
@@ -163,7 +165,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
     __shared__ double red[2][kMaxWaves];
     const NormLaunch& l = a.l;
     const int H = l.H;
-    const int64_t t = blockIdx.x;
+    const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (t >= l.T) return;
     double v[NC][kRun], h[NC][kRun];
     float in[NC][kRun];
 #pragma unroll
@@ -243,7 +246,9 @@ template <bool kSingle>
 hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
     const int runs = (a.l.H + kRun - 1) / kRun;
     const int threads = runs >= kMaxThreads ? kMaxThreads : (runs + 63) / 64 * 64;
-    const dim3 grid((uint32_t)a.l.T), block(threads);
+    // less than 2^32 threads along x
+    const int64_t most = (int64_t)1 << 21;
+    const dim3 grid((uint32_t)std::min(a.l.T, most), (uint32_t)((a.l.T + most - 1) / most)), block(threads);
     if (runs <= threads) hipLaunchKernelGGL((norm_kernel<1, kSingle>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((norm_kernel<2, kSingle>), grid, block, 0, st, a);
     return hipGetLastError();

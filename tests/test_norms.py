@@ -295,6 +295,28 @@ def test_a_block_with_4_bit_experts(qm, T, H, I, E, K):
             assert torch.equal(kept[n], s[n]), n
 
 
+@pytest.mark.gpu
+def test_more_than_2_to_32_threads(qm):
+    """4.2 million rows of 8192, a workgroup of 1024 each, a pattern of 1000 over and over."""
+    T, H, part = (1 << 22) + 3, 8192, 1000
+    torch.cuda.empty_cache()
+    h = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")  # 69 GB
+    few = torch.randn((part, H), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    for t in range(0, T, part):
+        h[t:t + part] = few[:min(part, T - t)]
+    codes = torch.empty((T, H // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((T, H // 32), dtype=torch.uint8, device="cuda")
+    norm = qm.Norm(torch.rand(H, generator=torch.Generator().manual_seed(2)).cuda())
+    qm.strata_moe_norm_before(h, norm, codes=codes, scales=scales)
+    c, s = torch.empty_like(codes[:part]), torch.empty_like(scales[:part])
+    qm.strata_moe_norm_before(few, norm, codes=c, scales=s)
+    for t in list(range(0, T, part * 61)) + [T // part * part]:
+        k = min(part, T - t)
+        assert torch.equal(codes[t:t + k], c[:k]) and torch.equal(scales[t:t + k], s[:k])
+    del h, codes, scales
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ refusals
 P = [(i + 1) << 24 for i in range(12)]
 

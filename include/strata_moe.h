@@ -444,7 +444,7 @@ int strata_moe_decode(const float* x, const float* router_w, const strata_moe_ex
  * goes to the nearest magnitude, ties to the even code, above 6 to 6.  A block
  * of zeros has scale byte 0; one that holds an infinity or NaN has byte 255
  * and codes 0, so all its values are NaN.  Errors: EINVAL for sizes (also rows
- * * cols >= 2^35), NULL pointers, alignment, strides or overlap, EUNSUPPORTED
+ * * cols >= 2^34), NULL pointers, alignment, strides or overlap, EUNSUPPORTED
  * for an unknown dtype. */
 int strata_moe_mxfp_quantize(const void* x, int32_t dtype, int64_t x_stride, int64_t rows, int32_t cols,
                              uint8_t* codes, uint8_t* scales, void* stream);
@@ -460,7 +460,9 @@ int strata_moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int6
  *   rows, cols: of one matrix (rows in [1, 65536]; the reduction is over cols)
  *   swiglu: 1 if a matrix is [gate; up] (rows even) and the product's output
  *           silu(gate x) (up x) of rows / 2 values, silu(v) = v / (1 + exp(-v))
- *   stride: a multiple of 256, at least strata_moe_mxfp_packed_bytes(). */
+ *           (0 from some v below -87 on, where it is under 2^-118)
+ *   stride: a multiple of 256, at least strata_moe_mxfp_packed_bytes(), at
+ *           most 2^32 */
 typedef struct strata_moe_mxfp_weights {
     int32_t n_expert;
     int32_t rows;
@@ -514,9 +516,9 @@ typedef struct strata_moe_norm {
  *   codes, scales: x rounded as strata_moe_mxfp_quantize does (H a multiple of
  *       32), or both NULL
  * 0 <= T <= 2^24, 1 <= H <= 16384.  The arithmetic is in fp64, each output is
- * rounded to fp32 (norm_after's out from there to its type).  Outputs overlap neither each other nor an input.  Errors:
- * EINVAL for sizes, NULL pointers, alignment, strides or overlap, EUNSUPPORTED
- * for an unknown dtype. */
+ * rounded to fp32 (norm_after's out from there to its type).  Outputs overlap
+ * neither each other nor an input.  Errors: EINVAL for sizes, NULL pointers,
+ * alignment, strides or overlap, EUNSUPPORTED for an unknown dtype. */
 int strata_moe_norm_before(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H,
                            const strata_moe_norm* norm, float* x, uint8_t* codes, uint8_t* scales, void* stream);
 

@@ -794,14 +794,21 @@ int64_t mxfp_packed_bytes(int32_t rows, int32_t cols, int32_t swiglu) {
     return round_up(mx_tiles(rows, swiglu != 0) * mx_tile_bytes(cols), 256);
 }
 
+int check_mxfp_stride(int64_t stride, int64_t need) {
+    if (stride < need || stride % 256 || stride > kMaxRowStride)
+        return fail(STRATA_MOE_EINVAL, "stride %lld below %lld, above 2^32 or not a multiple of 256", (long long)stride,
+                    (long long)need);
+    return 0;
+}
+
 // The size checks of a rounding call, and its arrays: float rows, codes, scales.
 int check_mxfp_rows(const void* v, int32_t dtype, int64_t stride, int64_t rows, int32_t cols, const uint8_t* codes,
                     const uint8_t* scales) {
     TRY(check_dtype(dtype));
     TRY(check_mxfp_cols(cols));
     TRY(check_rows("rows", rows));
-    if (rows * cols >= (int64_t)1 << 35)
-        return fail(STRATA_MOE_EINVAL, "rows * cols = %lld at or above 2^35", (long long)(rows * cols));
+    if (rows * cols >= (int64_t)1 << 34)
+        return fail(STRATA_MOE_EINVAL, "rows * cols = %lld at or above 2^34", (long long)(rows * cols));
     TRY(check_stride("row stride", stride, cols));
     if (rows == 0) return 0;
     if (!v || !codes || !scales) return fail(STRATA_MOE_EINVAL, "null rows / codes / scales");
@@ -1487,9 +1494,7 @@ int strata_moe_mxfp_pack(const uint8_t* codes, const uint8_t* scales, int32_t e0
     if (e0 < 0 || e1 < e0 || e1 > kMaxExperts)
         return fail(STRATA_MOE_EINVAL, "experts [%d, %d) outside [0, %d)", e0, e1, kMaxExperts);
     const int64_t need = mxfp_packed_bytes(rows, cols, swiglu);
-    if (stride < need || stride % 256)
-        return fail(STRATA_MOE_EINVAL, "stride %lld below %lld or not a multiple of 256", (long long)stride,
-                    (long long)need);
+    TRY(check_mxfp_stride(stride, need));
     if (e0 == e1) return 0;
     if (!codes || !scales || !packed) return fail(STRATA_MOE_EINVAL, "null codes / scales / packed");
     if (!aligned(codes, 16) || !aligned(packed, 256))
@@ -1517,9 +1522,7 @@ int strata_moe_mxfp_product(const uint8_t* codes, const uint8_t* scales, int64_t
     if (w.n_expert < 1 || w.n_expert > kMaxExperts)
         return fail(STRATA_MOE_EINVAL, "n_expert %d outside [1, %d]", w.n_expert, kMaxExperts);
     const int64_t need = mxfp_packed_bytes(w.rows, w.cols, w.swiglu);
-    if (w.stride < need || w.stride % 256)
-        return fail(STRATA_MOE_EINVAL, "stride %lld below %lld or not a multiple of 256", (long long)w.stride,
-                    (long long)need);
+    TRY(check_mxfp_stride(w.stride, need));
     TRY(check_rows("rows", rows));
     TRY(check_rows("x_rows", x_rows));
     const int32_t n_out = w.swiglu ? w.rows / 2 : w.rows;

@@ -417,6 +417,46 @@ def test_weights_and_outputs_past_32_bits(qm):
     assert torch.equal(out[rows - rows % 64:], first[:rows % 64])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [9, 6200])
+def test_rows_of_x_past_32_bits(qm, rows):
+    """Rows all over an x whose codes fill 4 GB, against the same rows by themselves."""
+    x_rows, cols, n = (1 << 24) - 1, 512, 256
+    g = torch.Generator(device="cuda").manual_seed(14)
+    xc = torch.randint(0, 256, (x_rows, cols // 2), generator=g, device="cuda", dtype=torch.uint8)
+    xs = torch.randint(120, 130, (x_rows, cols // 32), generator=g, device="cuda", dtype=torch.uint8)
+    _, _, wc, ws = _operands(1, cols, n, 1, seed=15)
+    w = qm.MxfpWeights(1, n, cols).pack(0, wc, ws)
+    src = torch.randint(0, x_rows, (rows,), generator=g, device="cuda").int()
+    src[:4] = torch.tensor([x_rows - 1, 0, x_rows - 2, 1 << 23], dtype=torch.int32)
+    out = qm.strata_moe_mxfp_product(xc, xs, w, torch.empty((rows, n), device="cuda"), src=src)
+    alone = torch.empty((rows, n), device="cuda")
+    _check_product(qm, xc[src.long()], xs[src.long()], wc, ws, alone, weights=w)
+    assert torch.equal(out, alone)
+
+
+@pytest.mark.gpu
+def test_rounding_past_32_bits(qm):
+    rows, cols = (1 << 24) - 1, 1000 // 32 * 32  # 1.7e10 values, 33 GB
+    part = _float_part(4099, cols)
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    for r in range(0, rows, 4099):
+        x[r:r + 4099] = part[:min(4099, rows - r)]
+    codes, scales = qm.strata_moe_mxfp_quantize(x)
+    want = _check_quantize(qm, part)
+    back = qm.strata_moe_mxfp_dequantize(codes, scales, x)
+    values = qm.strata_moe_mxfp_dequantize(*want, torch.empty_like(part))
+    for r in list(range(0, rows, 4099 * 97)) + [rows // 4099 * 4099]:
+        k = min(4099, rows - r)
+        assert torch.equal(codes[r:r + k], want[0][:k]) and torch.equal(scales[r:r + k], want[1][:k])
+        assert torch.equal(back[r:r + k], values[:k])
+
+
+def _float_part(rows, cols):
+    g = torch.Generator().manual_seed(rows)
+    return torch.randn((rows, cols), generator=g).to(torch.bfloat16).cuda()
+
+
 # ------------------------------------------------------------------ refusals
 PTR = 1 << 20
 
@@ -429,7 +469,8 @@ def _refused(qm, rc, code):
     (dict(rows=-1), -1), (dict(rows=(1 << 24) + 1), -1), (dict(cols=0), -1), (dict(cols=48), -1), (dict(cols=65568), -1),
     (dict(dtype=0), -2), (dict(dtype=4), -2), (dict(x_stride=63), -1), (dict(x_stride=(1 << 32) + 1), -1),
     (dict(x=None), -1), (dict(codes=None), -1), (dict(scales=None), -1), (dict(x=PTR + 2), -1), (dict(codes=(2 << 20) + 8), -1),
-    (dict(rows=1 << 24, cols=65536, x_stride=65536), -1), (dict(codes=PTR + 256), -1), (dict(scales=PTR + 1), -1),
+    (dict(rows=1 << 24, cols=65536, x_stride=65536), -1), (dict(rows=1 << 24, cols=1024, x_stride=1024), -1),
+    (dict(codes=PTR + 256), -1), (dict(scales=PTR + 1), -1),
     (dict(scales=(2 << 20) + 5), -1),
 ], ids=str)
 def test_rounding_refuses(qm, change, code):
@@ -465,7 +506,7 @@ def test_packed_bytes(qm):
 
 
 @pytest.mark.parametrize("change", [
-    dict(e0=-1), dict(e0=3, e1=2), dict(e1=1025), dict(stride=512), dict(stride=1300), dict(codes=None), dict(scales=None),
+    dict(e0=-1), dict(e0=3, e1=2), dict(e1=1025), dict(stride=512), dict(stride=1300), dict(stride=1 << 60), dict(codes=None), dict(scales=None),
     dict(packed=None), dict(codes=PTR + 8), dict(packed=(8 << 20) + 128), dict(codes=8 << 20), dict(scales=(8 << 20) + 2600),
     dict(rows=0), dict(cols=33),
 ], ids=str)
@@ -477,7 +518,7 @@ def test_pack_refuses(qm, change):
 
 @pytest.mark.parametrize("change,code", [
     (dict(weights=None), -1), (dict(E=0), -1), (dict(E=1025), -1), (dict(n=0), -1), (dict(cols=72), -1), (dict(swiglu=3), -1),
-    (dict(n=7, swiglu=1), -1), (dict(stride=512), -1), (dict(stride=1281), -1), (dict(rows=-1), -1),
+    (dict(n=7, swiglu=1), -1), (dict(stride=512), -1), (dict(stride=1281), -1), (dict(stride=1 << 60), -1), (dict(rows=-1), -1),
     (dict(rows=(1 << 24) + 1), -1), (dict(x_rows=-1), -1), (dict(x_rows=(1 << 24) + 1, src=7 << 20), -1),
     (dict(dtype=9), -2), (dict(out_stride=7), -1), (dict(offsets=None), -1), (dict(rows=21), -1), (dict(x_rows=0, src=7 << 20), -1),
     (dict(x_rows=1 << 24, cols=512, stride=5120, src=7 << 20), -1), (dict(codes=None), -1), (dict(scales=None), -1),

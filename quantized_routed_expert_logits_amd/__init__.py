@@ -736,13 +736,14 @@ def strata_moe_mxfp_quantize(x: torch.Tensor, codes: torch.Tensor | None = None,
         codes = _new_bytes((rows, cols // 2), x, stream)
     if scales is None:
         scales = _new_bytes((rows, cols // 32), x, stream)
-    _run_on(dev, stream, "strata_moe_mxfp_quantize", _lib.strata_moe_mxfp_quantize, x.data_ptr(), ROW_DTYPES[x.dtype], xs,
-            rows, cols, _array(codes, "codes", (rows, cols // 2), torch.uint8, dev),
+    _run_on(dev, stream, "strata_moe_mxfp_quantize", _lib.strata_moe_mxfp_quantize, x.data_ptr(), ROW_DTYPES[x.dtype],
+            xs, rows, cols, _array(codes, "codes", (rows, cols // 2), torch.uint8, dev),
             _array(scales, "scales", (rows, cols // 32), torch.uint8, dev))
     return codes, scales
 
 
-def strata_moe_mxfp_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> torch.Tensor:
+def strata_moe_mxfp_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor,
+                               stream=None) -> torch.Tensor:
     """The values that codes and scales stand for, into out [rows][cols] (fp32, fp16 or bf16; rows may be padded)."""
     os_ = _float_rows(out, "out")
     rows, cols = out.shape
@@ -793,8 +794,8 @@ def strata_moe_mxfp_pack(codes: torch.Tensor, scales: torch.Tensor, e0: int, wei
     args = (_array(codes, "codes", (n, weights.rows, weights.cols // 2), torch.uint8, dev),
             _array(scales, "scales", (n, weights.rows, weights.cols // 32), torch.uint8, dev))
     _same_device(weights.packed, "weights", dev)
-    _run_on(dev, stream, "strata_moe_mxfp_pack", _lib.strata_moe_mxfp_pack, *args, e0, e0 + n, weights.rows, weights.cols,
-            int(weights.swiglu), weights.packed.data_ptr(), weights.stride)
+    _run_on(dev, stream, "strata_moe_mxfp_pack", _lib.strata_moe_mxfp_pack, *args, e0, e0 + n, weights.rows,
+            weights.cols, int(weights.swiglu), weights.packed.data_ptr(), weights.stride)
 
 
 def strata_moe_mxfp_product(codes: torch.Tensor, scales: torch.Tensor, weights: MxfpWeights, out: torch.Tensor,
@@ -871,8 +872,8 @@ def strata_moe_norm_before(h: torch.Tensor, norm: Norm, x: torch.Tensor | None =
     hs = _float_rows(h, "h")
     T, H = h.shape
     dev = h.get_device()
-    _run_on(dev, stream, "strata_moe_norm_before", _lib.strata_moe_norm_before, h.data_ptr(), ROW_DTYPES[h.dtype], hs, T, H,
-            _norm(norm, "norm", H, dev), *_norm_outputs(x, codes, scales, T, H, dev))
+    _run_on(dev, stream, "strata_moe_norm_before", _lib.strata_moe_norm_before, h.data_ptr(), ROW_DTYPES[h.dtype], hs,
+            T, H, _norm(norm, "norm", H, dev), *_norm_outputs(x, codes, scales, T, H, dev))
 
 
 def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, norm: Norm | None = None,
@@ -924,8 +925,8 @@ def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, n
         gates = gate.data_ptr()
     branch = BranchStruct(y.data_ptr(), ys, y.shape[0], ROW_DTYPES[y.dtype], K, slots, weights,
                           _norm(norm, "norm", H, dev), gates, grow, gcol, residual_scale, block_scale)
-    _run_on(dev, stream, "strata_moe_norm_after", _lib.strata_moe_norm_after, h.data_ptr(), ROW_DTYPES[h.dtype], hs, T, H,
-            ctypes.byref(branch), out.data_ptr(), os_, _norm(next_norm, "next_norm", H, dev),
+    _run_on(dev, stream, "strata_moe_norm_after", _lib.strata_moe_norm_after, h.data_ptr(), ROW_DTYPES[h.dtype], hs, T,
+            H, ctypes.byref(branch), out.data_ptr(), os_, _norm(next_norm, "next_norm", H, dev),
             *_norm_outputs(x, codes, scales, T, H, dev))
     return out
 

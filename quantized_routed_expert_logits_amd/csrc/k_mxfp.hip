@@ -284,8 +284,8 @@ __device__ __forceinline__ void few_item(const ProductArgs& a, int e, int run, i
 #pragma unroll
             for (int f = 0; f < kFewTiles; ++f)
                 if (s0 + i < s1)
-                    acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[i][f]), operand(x[i]), acc[f], 4, 4, 0,
-                                                                              ws[i][f], 0, xs[i]);
+                    acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[i][f]), operand(x[i]), acc[f],
+                                                                              4, 4, 0, ws[i][f], 0, xs[i]);
     }
 #pragma unroll
     for (int f = 0; f < kFewTiles; ++f) part[wave][f][lane] = acc[f];
@@ -359,12 +359,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(ProductArgs a) {
     few_item(a, e, blockIdx.x, row, min(kMxTileRows, end - row), src, wave, waves, part);
 }
 
-// Many rows: the matrix unit bounds it, or the weights' bytes if an expert has a
-// few hundred rows.  A workgroup takes up to 6 tiles of rows (96) and 16 of
+// Many rows.  A workgroup (two to a CU) takes up to 6 tiles of rows (96) and 16 of
 // weights, 4 to a wave.  The rows' codes of 512 reduction values (a group) go to
 // LDS while the group before is multiplied (two buffers); each wave reads its own
-// weights from memory straight into registers, a group ahead.  Row tiles come in
-// pairs: an item of fewer rows leaves out the pairs it lacks.
+// weights from memory straight into registers, three steps of 128 ahead.  Row
+// tiles come in pairs: an item of fewer rows leaves out the pairs it lacks.
+//
+// What bounds it: where an expert has a few hundred rows, the memory (8192 tokens,
+// ten of 512 experts, 2560 -> 2 x 1024 SwiGLU: 395 us; it moves 1.97 GB, 4.9 TB/s of a
+// copy's 5.1, of which 1.6 it cannot do without: the rest is rows read again past an
+// L2, 0.26 GB, and weights, 0.09; down 1024 -> 2560: 245 us, 1.18 GB).  With one
+// matrix, the matrix unit and what feeds it (8192 rows, 4096 -> 4096: 75 us, 3.7
+// PFLOP/s; the unit alone reaches 6.7 to 7.3 on random values; without weight loads
+// 63, without rows' 74, without both and the stores 54).
+//
+// What was measured against it (us, the three calls above, 405 / 258 / 77): items of
+// 128 rows with weights two steps ahead 411 / 278 / 77; weights through the compiler's
+// own waits and LDS loads it sees 413 / 255 / 85; weights read past the caches 534 / 317
+// / 107; runs of one item after the other without kTogether 408 / 262 / 84; stores
+// through the caches 408 / 263 / 78; workgroups that change places to even out odd
+// row counts 413 against 414.
 constexpr int kWaves = 4;
 constexpr int kRowTiles = 6;
 constexpr int kTableRows = 128;  // of an item's row table: a multiple of the 64 rows of four scale tiles
@@ -445,14 +459,15 @@ __device__ __forceinline__ uint32_t scales_at(const TileLoads& l, const Part& t,
 }
 __device__ __forceinline__ void load_row_scales(const TileLoads& l, const Part& t, const RowAddresses& ad, int* sc) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        sc[i] = __builtin_amdgcn_raw_buffer_load_b32(l.scales, min(scales_at(l, t, ad.scales[i]), l.last_scales) | t.off,
-                                                     0, 0);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t at = min(scales_at(l, t, ad.scales[i]), l.last_scales);
+        sc[i] = __builtin_amdgcn_raw_buffer_load_b32(l.scales, at | t.off, 0, 0);
+    }
 }
 // Past the row's end a block gets scale 2^-127 (its codes are any, and meet weights
 // of 0).
-__device__ __forceinline__ void keep_row_scales(const TileLoads& l, const Part& t, const RowAddresses& ad, const int* sc,
-                                                Rows* to) {
+__device__ __forceinline__ void keep_row_scales(const TileLoads& l, const Part& t, const RowAddresses& ad,
+                                                const int* sc, Rows* to) {
     const int have = l.blocks - (t.q * 16 + 4 * (l.lane / 16));  // blocks of the row from the lane's first on
     const uint32_t mask = have >= 4 ? ~0u : have <= 0 ? 0u : (1u << (8 * have)) - 1;
 #pragma unroll
@@ -555,8 +570,9 @@ __device__ __forceinline__ void meet() {
 // Group `t` from `now`, the loads of the group after it, `u`, into `next` beside
 // it; each step's weights are loaded three steps ahead.  table: the thread's value
 // for the next item's row table at `entry`, there behind any group.
-__device__ __forceinline__ void group(const TileLoads& l, const Part& t, const Part& u, const RowAddresses& ad, Rows* now,
-                                      Rows* next, WeightRegs& r, uint32_t* entry, uint32_t table, v4f (*acc)[kWaveTiles]) {
+__device__ __forceinline__ void group(const TileLoads& l, const Part& t, const Part& u, const RowAddresses& ad,
+                                      Rows* now, Rows* next, WeightRegs& r, uint32_t* entry, uint32_t table,
+                                      v4f (*acc)[kWaveTiles]) {
     int sc[2], ws[kWaveTiles], xs[kRowTiles];
     const uint32_t to = lds(next->codes);
     Pair x = read_pair<0>(now, l.lane, 0);
@@ -582,8 +598,9 @@ __device__ __forceinline__ void group(const TileLoads& l, const Part& t, const P
 
 // All groups of an item, the last one beside the loads of the first group of the
 // item after it.
-__device__ __forceinline__ void item_sums(const TileLoads& l, Part t, const Part& after, RowAddresses& ad, Rows* b, int& turn,
-                                          WeightRegs& r, uint32_t* entry, uint32_t table, v4f (*acc)[kWaveTiles]) {
+__device__ __forceinline__ void item_sums(const TileLoads& l, Part t, const Part& after, RowAddresses& ad, Rows* b,
+                                          int& turn, WeightRegs& r, uint32_t* entry, uint32_t table,
+                                          v4f (*acc)[kWaveTiles]) {
 #pragma unroll 1
     for (int q = 0; q < l.groups; ++q) {
         t.q = q;
@@ -602,8 +619,8 @@ __device__ __forceinline__ void item_sums(const TileLoads& l, Part t, const Part
 // (`own`), so that neighbouring lanes store 16 bytes each of one row.  A row has
 // kUnits such units; unit c lies at c ^ row, for the banks' sake.
 template <typename T, bool kPaired>
-__device__ __forceinline__ void store_item(const ProductArgs& a, const Item& it, const Part& t, const TileLoads& l, v4f* own,
-                                           v4f (*acc)[kWaveTiles]) {
+__device__ __forceinline__ void store_item(const ProductArgs& a, const Item& it, const Part& t, const TileLoads& l,
+                                           v4f* own, v4f (*acc)[kWaveTiles]) {
     typedef T Piece __attribute__((ext_vector_type(4)));
     constexpr int kOutputs = kWaveTiles * kMxTileRows / (kPaired ? 2 : 1), kPer = 16 / (int)sizeof(T);
     constexpr int kUnits = kOutputs / kPer, kRows = 64 / kUnits;  // rows an instruction
@@ -632,7 +649,8 @@ __device__ __forceinline__ void store_item(const ProductArgs& a, const Item& it,
         if (whole) {
             v4f u[16 / kRows];
 #pragma unroll
-            for (int i = 0; i < 16 / kRows; ++i) u[i] = own[(i * kRows + r0) * kUnits + (c ^ (i * kRows + r0) % kUnits)];
+            for (int i = 0; i < 16 / kRows; ++i)
+                u[i] = own[(i * kRows + r0) * kUnits + (c ^ (i * kRows + r0) % kUnits)];
 #pragma unroll
             for (int i = 0; i < 16 / kRows; ++i)
                 if (i * kRows + r0 < rows)  // past the caches: nobody reads them in this call

@@ -42,7 +42,8 @@ struct NormArgs {
 // Column i of a thread's run c.
 template <bool kSingle>
 __device__ __forceinline__ int column(int c, int i) {
-    return kSingle ? (c * kRun + i) * (int)blockDim.x + (int)threadIdx.x : (c * (int)blockDim.x + (int)threadIdx.x) * kRun + i;
+    const int n = blockDim.x, t = threadIdx.x;
+    return kSingle ? (c * kRun + i) * n + t : (c * n + t) * kRun + i;
 }
 
 // A thread's run c of a row (columns at and past H: 0).
@@ -96,7 +97,8 @@ __device__ __forceinline__ void gather(const NormArgs& a, int64_t t, double (*v)
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int64_t at = row[b] < 0 || row[b] >= l.y_rows ? 0 : row[b];  // a row to read; used if it is the slot's
+            // a row to read; used if it is the slot's
+            const int64_t at = row[b] < 0 || row[b] >= l.y_rows ? 0 : row[b];
 #pragma unroll
             for (int c = 0; c < NC; ++c) load_run<kSingle>((const T*)l.y + at * l.y_stride, c, l.H, a.vec_y, y[b][c]);
         }

@@ -45,7 +45,10 @@ __device__ __forceinline__ void load8_vec(const __bf16* p, float* v) {
     const uint4 f = *(const uint4*)p;
     const uint32_t u[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
 }
 
 // v (4 values that are exact in type T) to columns j..j+3 of a row of H.

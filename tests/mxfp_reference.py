@@ -60,7 +60,8 @@ def product(x, w, swiglu):
     with np.errstate(over="ignore"):
         silu = g / (1.0 + np.exp(-g))
     out = silu * u
-    return out, 1.1 * dg * (np.abs(u) + du) + np.abs(silu) * du + 12 * 2.0 ** -23 * np.abs(out) + 2.0 ** -118 * np.abs(u)
+    tol = 1.1 * dg * (np.abs(u) + du) + np.abs(silu) * du
+    return out, tol + 12 * 2.0 ** -23 * np.abs(out) + 2.0 ** -118 * np.abs(u)
 
 
 def norm(v, weight, offset, eps):

@@ -33,7 +33,8 @@ def _check_quantize(qm, x):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
-@pytest.mark.parametrize("rows,cols,pad", [(1, 32, 0), (1, 2560, 0), (3, 64, 1), (7, 96, 8), (33, 1056, 3), (130, 544, 0),
+@pytest.mark.parametrize("rows,cols,pad",
+                         [(1, 32, 0), (1, 2560, 0), (3, 64, 1), (7, 96, 8), (33, 1056, 3), (130, 544, 0),
                                            (1025, 32, 5), (2, 65536, 0), (600, 2560, 0)])
 def test_quantize(qm, rows, cols, pad, dtype):
     g = torch.Generator().manual_seed(rows + cols)
@@ -140,9 +141,9 @@ def _check_product(qm, xc, xs, wc, ws, out, swiglu=False, offsets=None, src=None
 
 
 DENSE = [  # rows, cols, n
-    (1, 32, 1), (1, 2560, 2560), (2, 64, 15), (5, 96, 17), (16, 128, 64), (17, 544, 333), (31, 640, 65), (64, 1024, 100),
-    (65, 512, 256), (128, 160, 257), (129, 1056, 128), (200, 2560, 320), (300, 4096, 96), (3, 65536, 20),
-    (2, 32, 65536), (1000, 96, 70), (2049, 512, 130),
+    (1, 32, 1), (1, 2560, 2560), (2, 64, 15), (5, 96, 17), (16, 128, 64), (17, 544, 333), (31, 640, 65),
+    (64, 1024, 100), (65, 512, 256), (128, 160, 257), (129, 1056, 128), (200, 2560, 320), (300, 4096, 96),
+    (3, 65536, 20), (2, 32, 65536), (1000, 96, 70), (2049, 512, 130),
 ]
 
 
@@ -159,7 +160,8 @@ def test_product_of_one_matrix(qm, size, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
-@pytest.mark.parametrize("size", [(1, 32, 2), (1, 2560, 2048), (9, 96, 30), (17, 544, 34), (130, 640, 512), (257, 512, 666)],
+@pytest.mark.parametrize("size",
+                         [(1, 32, 2), (1, 2560, 2048), (9, 96, 30), (17, 544, 34), (130, 640, 512), (257, 512, 666)],
                          ids=lambda s: "-".join(map(str, s)))
 def test_swiglu_of_one_matrix(qm, size, dtype):
     rows, cols, n = size
@@ -171,11 +173,12 @@ def test_swiglu_of_one_matrix(qm, size, dtype):
 
 
 GROUPED = [  # rows, x rows (0: no src), cols, n, E, how, swiglu
-    (1, 1, 96, 32, 512, "random", True), (10, 1, 2560, 128, 512, "random", True), (10, 0, 1024, 80, 512, "random", False),
-    (64, 20, 160, 33, 7, "random", False), (406, 203, 544, 333, 6, "random", False), (300, 30, 640, 64, 1024, "random", True),
+    (1, 1, 96, 32, 512, "random", True), (10, 1, 2560, 128, 512, "random", True),
+    (10, 0, 1024, 80, 512, "random", False), (64, 20, 160, 33, 7, "random", False),
+    (406, 203, 544, 333, 6, "random", False), (300, 30, 640, 64, 1024, "random", True),
     (320, 32, 256, 96, 512, "random", False), (1000, 100, 128, 48, 40, "hot", True), (777, 0, 96, 20, 5, "one", False),
-    (2000, 500, 512, 260, 16, "random", True), (1500, 0, 672, 300, 9, "hot", False), (4000, 400, 96, 16, 1024, "hot", False),
-    (520, 52, 64, 40, 3, "one", True), (33, 33, 2560, 64, 2, "random", False),
+    (2000, 500, 512, 260, 16, "random", True), (1500, 0, 672, 300, 9, "hot", False),
+    (4000, 400, 96, 16, 1024, "hot", False), (520, 52, 64, 40, 3, "one", True), (33, 33, 2560, 64, 2, "random", False),
 ]
 
 
@@ -212,10 +215,11 @@ def test_borders_between_kernels(qm, size):
 
 MANY = [  # rows, x rows (0: no src), cols, n, E, how, swiglu: all taken by the kernel of many rows
     (3600, 0, 544, 334, 0, "", True), (1500, 0, 640, 2047, 0, "", False), (1300, 0, 4128, 515, 0, "", False),
-    (4000, 400, 512, 256, 1024, "random", True), (4000, 0, 672, 250, 1024, "hot", False), (4000, 203, 544, 334, 6, "random", True),
-    (2600, 7, 1056, 400, 5, "one", False), (5000, 4, 32, 2048, 4, "random", False), (7000, 11, 96, 1024, 3, "hot", True),
-    (1800, 257, 2560, 96, 64, "random", True), (3000, 3001, 480, 512, 2, "random", False), (1000, 0, 1536, 1100, 1, "one", True),
-    (20000, 0, 512, 640, 3, "random", False),
+    (4000, 400, 512, 256, 1024, "random", True), (4000, 0, 672, 250, 1024, "hot", False),
+    (4000, 203, 544, 334, 6, "random", True), (2600, 7, 1056, 400, 5, "one", False),
+    (5000, 4, 32, 2048, 4, "random", False), (7000, 11, 96, 1024, 3, "hot", True),
+    (1800, 257, 2560, 96, 64, "random", True), (3000, 3001, 480, 512, 2, "random", False),
+    (1000, 0, 1536, 1100, 1, "one", True), (20000, 0, 512, 640, 3, "random", False),
 ]
 
 
@@ -312,7 +316,8 @@ def test_offsets_of_any_value_stay_in_the_arrays(qm, rows):
     qm.strata_moe_mxfp_product(xc, xs, w, buf[:rows], offsets=off)
     assert torch.all(buf[rows:] == 7.0)
     x = ref.values(ref.unpack(_np(xc)), _np(xs))
-    want, tol = ref.product(x[5:], ref.values(ref.unpack(_np(wc[2])), _np(ws[2])), False)  # rows 5.. are expert 2's alone
+    want, tol = ref.product(x[5:], ref.values(ref.unpack(_np(wc[2])), _np(ws[2])),
+                            False)  # rows 5.. are expert 2's alone
     assert np.all(np.abs(_np(buf[5:rows]) - want) <= tol + 2.0 ** -24 * np.abs(want))
 
 
@@ -348,7 +353,8 @@ def test_repeated_calls_give_the_same_bits(qm, rows, n_e):
     xc, xs, wc, ws = _operands(rows, 640, 200, n_e, seed=6)
     w = qm.MxfpWeights(n_e, 200, 640, swiglu=True).pack(0, wc, ws)
     off = None if n_e == 1 else _offsets(n_e, rows, 1)
-    outs = [qm.strata_moe_mxfp_product(xc, xs, w, torch.empty((rows, 100), device="cuda"), offsets=off) for _ in range(3)]
+    outs = [qm.strata_moe_mxfp_product(xc, xs, w, torch.empty((rows, 100), device="cuda"),
+                                       offsets=off) for _ in range(3)]
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
@@ -466,11 +472,11 @@ def _refused(qm, rc, code):
 
 
 @pytest.mark.parametrize("change,code", [
-    (dict(rows=-1), -1), (dict(rows=(1 << 24) + 1), -1), (dict(cols=0), -1), (dict(cols=48), -1), (dict(cols=65568), -1),
-    (dict(dtype=0), -2), (dict(dtype=4), -2), (dict(x_stride=63), -1), (dict(x_stride=(1 << 32) + 1), -1),
-    (dict(x=None), -1), (dict(codes=None), -1), (dict(scales=None), -1), (dict(x=PTR + 2), -1), (dict(codes=(2 << 20) + 8), -1),
-    (dict(rows=1 << 24, cols=65536, x_stride=65536), -1), (dict(rows=1 << 24, cols=1024, x_stride=1024), -1),
-    (dict(codes=PTR + 256), -1), (dict(scales=PTR + 1), -1),
+    (dict(rows=-1), -1), (dict(rows=(1 << 24) + 1), -1), (dict(cols=0), -1), (dict(cols=48), -1),
+    (dict(cols=65568), -1), (dict(dtype=0), -2), (dict(dtype=4), -2), (dict(x_stride=63), -1),
+    (dict(x_stride=(1 << 32) + 1), -1), (dict(x=None), -1), (dict(codes=None), -1), (dict(scales=None), -1),
+    (dict(x=PTR + 2), -1), (dict(codes=(2 << 20) + 8), -1), (dict(rows=1 << 24, cols=65536, x_stride=65536), -1),
+    (dict(rows=1 << 24, cols=1024, x_stride=1024), -1), (dict(codes=PTR + 256), -1), (dict(scales=PTR + 1), -1),
     (dict(scales=(2 << 20) + 5), -1),
 ], ids=str)
 def test_rounding_refuses(qm, change, code):
@@ -491,7 +497,8 @@ def test_no_rows_is_a_no_op(qm):
     assert lib.strata_moe_mxfp_product(None, None, 0, ctypes.byref(st), None, None, 0, None, 1, 8, None) == 0
 
 
-@pytest.mark.parametrize("rows,cols,swiglu", [(0, 64, 0), (65537, 64, 0), (7, 64, 1), (8, 40, 0), (8, 0, 0), (8, 64, 2)])
+@pytest.mark.parametrize("rows,cols,swiglu",
+                         [(0, 64, 0), (65537, 64, 0), (7, 64, 1), (8, 40, 0), (8, 0, 0), (8, 64, 2)])
 def test_packed_bytes_refuses(qm, rows, cols, swiglu):
     b = ctypes.c_int64()
     _refused(qm, qm.library().strata_moe_mxfp_packed_bytes(rows, cols, swiglu, ctypes.byref(b)), -1)
@@ -506,9 +513,9 @@ def test_packed_bytes(qm):
 
 
 @pytest.mark.parametrize("change", [
-    dict(e0=-1), dict(e0=3, e1=2), dict(e1=1025), dict(stride=512), dict(stride=1300), dict(stride=1 << 60), dict(codes=None), dict(scales=None),
-    dict(packed=None), dict(codes=PTR + 8), dict(packed=(8 << 20) + 128), dict(codes=8 << 20), dict(scales=(8 << 20) + 2600),
-    dict(rows=0), dict(cols=33),
+    dict(e0=-1), dict(e0=3, e1=2), dict(e1=1025), dict(stride=512), dict(stride=1300), dict(stride=1 << 60),
+    dict(codes=None), dict(scales=None), dict(packed=None), dict(codes=PTR + 8), dict(packed=(8 << 20) + 128),
+    dict(codes=8 << 20), dict(scales=(8 << 20) + 2600), dict(rows=0), dict(cols=33),
 ], ids=str)
 def test_pack_refuses(qm, change):
     a = dict(codes=PTR, scales=2 << 20, e0=0, e1=4, rows=8, cols=64, swiglu=0, packed=8 << 20, stride=1280)
@@ -517,23 +524,25 @@ def test_pack_refuses(qm, change):
 
 
 @pytest.mark.parametrize("change,code", [
-    (dict(weights=None), -1), (dict(E=0), -1), (dict(E=1025), -1), (dict(n=0), -1), (dict(cols=72), -1), (dict(swiglu=3), -1),
-    (dict(n=7, swiglu=1), -1), (dict(stride=512), -1), (dict(stride=1281), -1), (dict(stride=1 << 60), -1), (dict(rows=-1), -1),
-    (dict(rows=(1 << 24) + 1), -1), (dict(x_rows=-1), -1), (dict(x_rows=(1 << 24) + 1, src=7 << 20), -1),
-    (dict(dtype=9), -2), (dict(out_stride=7), -1), (dict(offsets=None), -1), (dict(rows=21), -1), (dict(x_rows=0, src=7 << 20), -1),
+    (dict(weights=None), -1), (dict(E=0), -1), (dict(E=1025), -1), (dict(n=0), -1), (dict(cols=72), -1),
+    (dict(swiglu=3), -1), (dict(n=7, swiglu=1), -1), (dict(stride=512), -1), (dict(stride=1281), -1),
+    (dict(stride=1 << 60), -1), (dict(rows=-1), -1), (dict(rows=(1 << 24) + 1), -1), (dict(x_rows=-1), -1),
+    (dict(x_rows=(1 << 24) + 1, src=7 << 20), -1), (dict(dtype=9), -2), (dict(out_stride=7), -1),
+    (dict(offsets=None), -1), (dict(rows=21), -1), (dict(x_rows=0, src=7 << 20), -1),
     (dict(x_rows=1 << 24, cols=512, stride=5120, src=7 << 20), -1), (dict(codes=None), -1), (dict(scales=None), -1),
     (dict(packed=None), -1), (dict(out=None), -1), (dict(codes=PTR + 4), -1), (dict(packed=(3 << 20) + 64), -1),
-    (dict(offsets=(5 << 20) + 2), -1), (dict(src=(7 << 20) + 1), -1), (dict(out=(6 << 20) + 2), -1), (dict(out=PTR + 32), -1),
-    (dict(out=3 << 20), -1), (dict(out=(5 << 20) - 4), -1), (dict(out=(2 << 20) + 4), -1), (dict(src=6 << 20), -1),
+    (dict(offsets=(5 << 20) + 2), -1), (dict(src=(7 << 20) + 1), -1), (dict(out=(6 << 20) + 2), -1),
+    (dict(out=PTR + 32), -1), (dict(out=3 << 20), -1), (dict(out=(5 << 20) - 4), -1), (dict(out=(2 << 20) + 4), -1),
+    (dict(src=6 << 20), -1),
 ], ids=str)
 def test_product_refuses(qm, change, code):
-    a = dict(codes=PTR, scales=2 << 20, x_rows=20, E=4, n=8, cols=64, swiglu=0, packed=3 << 20, stride=1280, offsets=5 << 20,
-             src=None, rows=20, out=6 << 20, dtype=1, out_stride=8, weights=True)
+    a = dict(codes=PTR, scales=2 << 20, x_rows=20, E=4, n=8, cols=64, swiglu=0, packed=3 << 20, stride=1280,
+             offsets=5 << 20, src=None, rows=20, out=6 << 20, dtype=1, out_stride=8, weights=True)
     a.update(change)
     st = qm.MxfpWeightsStruct(a["E"], a["n"], a["cols"], a["swiglu"], a["packed"], a["stride"])
     _refused(qm, qm.library().strata_moe_mxfp_product(
-        a["codes"], a["scales"], a["x_rows"], ctypes.byref(st) if a["weights"] else None, a["offsets"], a["src"], a["rows"],
-        a["out"], a["dtype"], a["out_stride"], None), code)
+        a["codes"], a["scales"], a["x_rows"], ctypes.byref(st) if a["weights"] else None, a["offsets"], a["src"],
+        a["rows"], a["out"], a["dtype"], a["out_stride"], None), code)
 
 
 def test_the_binding_checks_its_tensors(qm):

@@ -4,7 +4,8 @@ definition in 64 bits.
 Tolerance: the kernels work in fp64 and round an output to fp32, and from there
 to a 16-bit type.  Their sums have at most H + K + 40 roundings of 2^-53 relative
 to the absolute terms (H <= 16384), below 2^-38, so an output is off by half a
-step of its type, half a step of fp32 and 2^-37 of the absolute terms.  The stream that the next norm reads is the stored one.
+step of its type, half a step of fp32 and 2^-37 of the absolute terms.  The
+stream that the next norm reads is the stored one.
 4-bit codes: those of the fp32 x that the same call wrote, bit for bit.
 """
 import ctypes
@@ -45,8 +46,8 @@ def _rows(T, H, pad, dtype, g, scale=1.0):
     return (torch.randn((T, H + pad), generator=g) * scale).to(dtype).cuda()[:, :H]
 
 
-BEFORE = [(1, 1, 0), (1, 2560, 0), (2, 3, 1), (5, 33, 0), (7, 64, 1), (33, 255, 2), (64, 256, 8), (100, 1001, 3), (40, 2560, 0),
-          (3, 4096, 4), (3, 4100, 0), (2, 8192, 1), (2, 16384, 0), (2, 12001, 0), (1025, 96, 0)]
+BEFORE = [(1, 1, 0), (1, 2560, 0), (2, 3, 1), (5, 33, 0), (7, 64, 1), (33, 255, 2), (64, 256, 8), (100, 1001, 3),
+          (40, 2560, 0), (3, 4096, 4), (3, 4100, 0), (2, 8192, 1), (2, 16384, 0), (2, 12001, 0), (1025, 96, 0)]
 
 
 @pytest.mark.gpu
@@ -57,7 +58,8 @@ def test_before(qm, size, dtype):
     g = torch.Generator().manual_seed(T + H)
     h = _rows(T, H, pad, dtype, g, 3.0)
     w = torch.randn(H, generator=g).cuda()
-    for weight, offset, eps in ((w, 0.0, 1e-6), (w, 1.0, 1e-5), (None, 0.0, 0.0), (w[:0].new_ones(H + 1)[1:], 0.0, 0.5)):
+    for weight, offset, eps in ((w, 0.0, 1e-6), (w, 1.0, 1e-5), (None, 0.0, 0.0),
+                                (w[:0].new_ones(H + 1)[1:], 0.0, 0.5)):
         x = torch.empty((T, H), device="cuda")
         codes = scales = None
         if H % 32 == 0:
@@ -74,16 +76,19 @@ def test_before(qm, size, dtype):
 
 
 AFTER = [  # T, H, pad, K, y dtype, gate, norm, next
-    (1, 1, 0, 0, 0, "none", True, True), (1, 2560, 0, 10, 0, "channel", True, True), (3, 64, 1, 0, 1, "token", False, True),
-    (7, 33, 0, 1, 2, "full", True, False), (32, 2560, 0, 10, 2, "token", True, True), (65, 1001, 3, 4, 1, "channel", True, True),
-    (200, 96, 0, 16, 0, "full", False, True), (4, 4100, 0, 3, 2, "none", True, True), (2, 16384, 0, 2, 0, "token", True, True),
-    (500, 256, 8, 0, 2, "none", True, True), (9, 640, 2, 2, 1, "wide", True, True),
+    (1, 1, 0, 0, 0, "none", True, True), (1, 2560, 0, 10, 0, "channel", True, True),
+    (3, 64, 1, 0, 1, "token", False, True), (7, 33, 0, 1, 2, "full", True, False),
+    (32, 2560, 0, 10, 2, "token", True, True), (65, 1001, 3, 4, 1, "channel", True, True),
+    (200, 96, 0, 16, 0, "full", False, True), (4, 4100, 0, 3, 2, "none", True, True),
+    (2, 16384, 0, 2, 0, "token", True, True), (500, 256, 8, 0, 2, "none", True, True),
+    (9, 640, 2, 2, 1, "wide", True, True),
 ]
 
 
 def _after_case(T, H, pad, K, ydt, gate, dtype, seed):
     g = torch.Generator().manual_seed(seed)
-    s = dict(h=_rows(T, H, pad, dtype, g, 2.0), y=_rows(T * max(K, 1), H, pad, DTYPES[ydt], g), slot=None, p=None, gate=None)
+    s = dict(h=_rows(T, H, pad, dtype, g, 2.0), y=_rows(T * max(K, 1), H, pad, DTYPES[ydt], g), slot=None, p=None,
+             gate=None)
     if K:
         s["slot"] = torch.randperm(T * K, generator=g).int().view(T, K).cuda()
         s["p"] = torch.rand((T, K), generator=g).cuda()
@@ -180,7 +185,8 @@ def test_extremes(qm, dtype):
     h[3] = torch.finfo(dtype).max
     h[4] = torch.finfo(dtype).smallest_normal
     x = torch.empty((6, H), device="cuda")
-    codes, scales = torch.empty((6, 48), dtype=torch.uint8, device="cuda"), torch.empty((6, 3), dtype=torch.uint8, device="cuda")
+    codes = torch.empty((6, 48), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((6, 3), dtype=torch.uint8, device="cuda")
     qm.strata_moe_norm_before(h, qm.Norm(None, 1e-12), x, codes, scales)
     assert torch.all(x[0] == 0) and torch.isnan(x[1]).all()
     # an infinite value: 0 where the others are finite, NaN at its own place
@@ -248,8 +254,8 @@ def test_a_block_with_4_bit_experts(qm, T, H, I, E, K):
     wc1, ws1, wc2, ws2 = (t.view(E, -1, t.shape[1]) for t in (wc1, ws1, wc2, ws2))
     h0 = rnd(T, H).to(torch.bfloat16)
     s = dict(h=h0.clone(), n1=qm.Norm(rnd(H), 1e-6), n2=qm.Norm(rnd(H), 1e-6), n3=qm.Norm(rnd(H), 1e-6, 1.0),
-             x=torch.empty((T, H), device="cuda"), x2=torch.empty((T, H), device="cuda"), xc=u8(T, H // 2), xs=u8(T, H // 32),
-             hid=torch.empty((T * K, I), device="cuda"), hc=u8(T * K, I // 2), hs=u8(T * K, I // 32),
+             x=torch.empty((T, H), device="cuda"), x2=torch.empty((T, H), device="cuda"), xc=u8(T, H // 2),
+             xs=u8(T, H // 32), hid=torch.empty((T * K, I), device="cuda"), hc=u8(T * K, I // 2), hs=u8(T * K, I // 32),
              y=torch.empty((T * K, H), dtype=torch.bfloat16, device="cuda"),
              gate_up=qm.MxfpWeights(E, 2 * I, H, swiglu=True).pack(0, wc1, ws1),
              down=qm.MxfpWeights(E, H, I).pack(0, wc2, ws2))
@@ -326,44 +332,45 @@ def _refused(qm, rc, code):
 
 
 @pytest.mark.parametrize("change,code", [
-    (dict(T=-1), -1), (dict(T=(1 << 24) + 1), -1), (dict(H=0), -1), (dict(H=16385, h_stride=16385), -1), (dict(dtype=5), -2),
-    (dict(h_stride=63), -1), (dict(h=None), -1), (dict(h=P[0] + 2), -1), (dict(x=P[1] + 2), -1), (dict(x=None, codes=None, scales=None), -1),
-    (dict(codes=None), -1), (dict(scales=None), -1), (dict(codes=P[2] + 8), -1), (dict(H=40), -1), (dict(x=P[0]), -1),
-    (dict(codes=P[0] + 16), -1), (dict(scales=P[1] + 9), -1), (dict(x=P[4]), -1), (dict(eps=-1.0), -1),
-    (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1), (dict(offset=float("inf")), -1), (dict(weight=P[4] + 1), -1),
-    (dict(norm=False), -1),
+    (dict(T=-1), -1), (dict(T=(1 << 24) + 1), -1), (dict(H=0), -1), (dict(H=16385, h_stride=16385), -1),
+    (dict(dtype=5), -2), (dict(h_stride=63), -1), (dict(h=None), -1), (dict(h=P[0] + 2), -1), (dict(x=P[1] + 2), -1),
+    (dict(x=None, codes=None, scales=None), -1), (dict(codes=None), -1), (dict(scales=None), -1),
+    (dict(codes=P[2] + 8), -1), (dict(H=40), -1), (dict(x=P[0]), -1), (dict(codes=P[0] + 16), -1),
+    (dict(scales=P[1] + 9), -1), (dict(x=P[4]), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1),
+    (dict(eps=float("inf")), -1), (dict(offset=float("inf")), -1), (dict(weight=P[4] + 1), -1), (dict(norm=False), -1),
 ], ids=str)
 def test_before_refuses(qm, change, code):
-    a = dict(h=P[0], dtype=1, h_stride=64, T=8, H=64, x=P[1], codes=P[2], scales=P[3], weight=P[4], offset=0.0, eps=1e-6,
-             norm=True)
+    a = dict(h=P[0], dtype=1, h_stride=64, T=8, H=64, x=P[1], codes=P[2], scales=P[3], weight=P[4], offset=0.0,
+             eps=1e-6, norm=True)
     a.update(change)
     n = qm.NormStruct(a["weight"], a["offset"], a["eps"])
     _refused(qm, qm.library().strata_moe_norm_before(a["h"], a["dtype"], a["h_stride"], a["T"], a["H"],
-                                                     ctypes.byref(n) if a["norm"] else None, a["x"], a["codes"], a["scales"],
-                                                     None), code)
+                                                     ctypes.byref(n) if a["norm"] else None, a["x"], a["codes"],
+                                                     a["scales"], None), code)
 
 
 @pytest.mark.parametrize("change,code", [
     (dict(branch=False), -1), (dict(T=-1), -1), (dict(dtype=0), -2), (dict(y_dtype=0), -2), (dict(y_stride=63), -1),
     (dict(out_stride=63), -1), (dict(y_rows=-1), -1), (dict(y_rows=0), -1), (dict(slot=None), -1), (dict(p=None), -1),
     (dict(K=0), -1), (dict(K=17), -1), (dict(slot=None, p=None), -1), (dict(slot=None, p=None, K=0, y_rows=7), -1),
-    (dict(rs=float("inf")), -1), (dict(bs=float("nan")), -1), (dict(gcol=2), -1), (dict(grow=-1), -1), (dict(out=None), -1),
-    (dict(y=None), -1), (dict(out=P[5] + 2), -1), (dict(y=P[6] + 1), -1), (dict(slot=P[7] + 2), -1), (dict(p=P[8] + 2), -1),
-    (dict(gate=P[9] + 2), -1), (dict(out=P[0] + 4), -1), (dict(out=P[0], out_stride=65), -1), (dict(out=P[6]), -1),
-    (dict(out=P[7]), -1), (dict(x=P[0] + 64), -1), (dict(x=P[5]), -1), (dict(codes=P[9]), -1), (dict(next=False), -1),
-    (dict(x=P[4]), -1), (dict(out=P[10]), -1), (dict(scales=P[8] + 5), -1),
+    (dict(rs=float("inf")), -1), (dict(bs=float("nan")), -1), (dict(gcol=2), -1), (dict(grow=-1), -1),
+    (dict(out=None), -1), (dict(y=None), -1), (dict(out=P[5] + 2), -1), (dict(y=P[6] + 1), -1),
+    (dict(slot=P[7] + 2), -1), (dict(p=P[8] + 2), -1), (dict(gate=P[9] + 2), -1), (dict(out=P[0] + 4), -1),
+    (dict(out=P[0], out_stride=65), -1), (dict(out=P[6]), -1), (dict(out=P[7]), -1), (dict(x=P[0] + 64), -1),
+    (dict(x=P[5]), -1), (dict(codes=P[9]), -1), (dict(next=False), -1), (dict(x=P[4]), -1), (dict(out=P[10]), -1),
+    (dict(scales=P[8] + 5), -1),
 ], ids=str)
 def test_after_refuses(qm, change, code):
-    a = dict(h=P[0], dtype=1, h_stride=64, T=8, H=64, x=P[1], codes=P[2], scales=P[3], weight=P[4], out=P[5], out_stride=64,
-             y=P[6], y_stride=64, y_rows=16, y_dtype=3, slot=P[7], p=P[8], K=2, gate=P[9], grow=64, gcol=1, next_weight=P[10],
-             rs=1.0, bs=1.0, branch=True, next=True)
+    a = dict(h=P[0], dtype=1, h_stride=64, T=8, H=64, x=P[1], codes=P[2], scales=P[3], weight=P[4], out=P[5],
+             out_stride=64, y=P[6], y_stride=64, y_rows=16, y_dtype=3, slot=P[7], p=P[8], K=2, gate=P[9], grow=64,
+             gcol=1, next_weight=P[10], rs=1.0, bs=1.0, branch=True, next=True)
     a.update(change)
     n, u = qm.NormStruct(a["weight"], 0.0, 1e-6), qm.NormStruct(a["next_weight"], 0.0, 1e-6)
     b = qm.BranchStruct(a["y"], a["y_stride"], a["y_rows"], a["y_dtype"], a["K"], a["slot"], a["p"], ctypes.pointer(n),
                         a["gate"], a["grow"], a["gcol"], a["rs"], a["bs"])
     _refused(qm, qm.library().strata_moe_norm_after(
-        a["h"], a["dtype"], a["h_stride"], a["T"], a["H"], ctypes.byref(b) if a["branch"] else None, a["out"], a["out_stride"],
-        ctypes.byref(u) if a["next"] else None, a["x"], a["codes"], a["scales"], None), code)
+        a["h"], a["dtype"], a["h_stride"], a["T"], a["H"], ctypes.byref(b) if a["branch"] else None, a["out"],
+        a["out_stride"], ctypes.byref(u) if a["next"] else None, a["x"], a["codes"], a["scales"], None), code)
 
 
 def test_no_tokens_is_a_no_op(qm):

@@ -15,8 +15,8 @@
 // What bounds it: with few tokens the latency of a chain of loads (slots, rows,
 // the norms' sums), with many the memory, as far as enough tokens are in flight
 // per CU to cover that chain.  So a token has few waves with few registers: 8192
-// tokens of 2560, K = 10 bf16 rows, with the next norm and codes, take 160 us (671
-// MB, 4.2 TB/s); runs of 4 columns (twice the waves) took 213, and 5 or 10 rows
+// tokens of 2560, K = 10 bf16 rows, with the next norm and codes, take 156 us (671
+// MB, 4.3 TB/s); runs of 4 columns (twice the waves) took 213, and 5 or 10 rows
 // loaded before the first is used, which costs registers, 183 and 280.
 //
 // All arithmetic is in 64 bits and an output is rounded to fp32, and from there
@@ -82,9 +82,11 @@ __device__ __forceinline__ void store_run(void* base, int dtype, int64_t at, int
     }
 }
 
-// v = sum_k p[t][k] y[slot[t][k]], k ascending.
+// v = sum_k p[t][k] y[slot[t][k]], k ascending.  Lane k holds slot and p of k, so
+// that their loads are one, begun with the kernel (in the loop they cost 32 tokens
+// 8.1 us against 7.5, and 8192 159 against 156).
 template <int NC, bool kSingle, typename T>
-__device__ __forceinline__ void gather(const NormArgs& a, int64_t t, double (*v)[kRun]) {
+__device__ __forceinline__ void gather(const NormArgs& a, int slot, int p_bits, double (*v)[kRun]) {
     const NormLaunch& l = a.l;
     constexpr int kBatch = 2;
     for (int k0 = 0; k0 < l.K; k0 += kBatch) {
@@ -92,8 +94,8 @@ __device__ __forceinline__ void gather(const NormArgs& a, int64_t t, double (*v)
         float p[kBatch], y[kBatch][NC][kRun];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            row[b] = k0 + b < l.K ? l.slot[t * l.K + k0 + b] : -1;
-            p[b] = k0 + b < l.K ? l.p[t * l.K + k0 + b] : 0.0f;
+            row[b] = __builtin_amdgcn_readlane(slot, k0 + b);  // -1 from K on
+            p[b] = __int_as_float(__builtin_amdgcn_readlane(p_bits, k0 + b));
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -169,6 +171,9 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
     const int H = l.H;
     const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (t >= l.T) return;
+    int slot = -1, p_bits = 0;
+    const int lane = threadIdx.x % 64;
+    if (l.slot && lane < l.K) slot = l.slot[t * l.K + lane], p_bits = __float_as_int(l.p[t * l.K + lane]);
     double v[NC][kRun], h[NC][kRun];
     float in[NC][kRun];
 #pragma unroll
@@ -179,9 +184,9 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
             for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int i = 0; i < kRun; ++i) v[c][i] = 0.0;
-            if (l.y_dtype == kF32) gather<NC, kSingle, float>(a, t, v);
-            else if (l.y_dtype == kF16) gather<NC, kSingle, _Float16>(a, t, v);
-            else gather<NC, kSingle, __bf16>(a, t, v);
+            if (l.y_dtype == kF32) gather<NC, kSingle, float>(a, slot, p_bits, v);
+            else if (l.y_dtype == kF16) gather<NC, kSingle, _Float16>(a, slot, p_bits, v);
+            else gather<NC, kSingle, __bf16>(a, slot, p_bits, v);
         } else {
             float y[NC][kRun];
 #pragma unroll

@@ -15,8 +15,8 @@
 // What bounds it: with few tokens the latency of a chain of loads (slots, rows,
 // the norms' sums), with many the memory, as far as enough tokens are in flight
 // per CU to cover that chain.  So a token has few waves with few registers: 8192
-// tokens of 2560, K = 10 bf16 rows, with the next norm and codes, take 156 us (671
-// MB, 4.3 TB/s); runs of 4 columns (twice the waves) took 213, and 5 or 10 rows
+// tokens of 2560, K = 10 bf16 rows, with the next norm and codes, take 153 us (671
+// MB, 4.4 TB/s); runs of 4 columns (twice the waves) took 213, and 5 or 10 rows
 // loaded before the first is used, which costs registers, 183 and 280.
 //
 // All arithmetic is in 64 bits and an output is rounded to fp32, and from there
@@ -115,12 +115,38 @@ __device__ __forceinline__ void gather(const NormArgs& a, int slot, int p_bits, 
     }
 }
 
+// The sum over the wave's 64 lanes, the same in each.  Lanes change places within
+// the registers; through the LDS path (__shfl_xor) 32 tokens took 7.6 us against
+// 7.0, one token's norm 2.7 against 2.5 and 8192 156 against 153.
+template <int kCtrl>
+__device__ __forceinline__ double moved(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)u, kCtrl, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), kCtrl, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double s) {
+    s += moved<0xb1>(s);   // quad_perm [1, 0, 3, 2]: lane ^ 1
+    s += moved<0x4e>(s);   // quad_perm [2, 3, 0, 1]: lane ^ 2
+    s += moved<0x141>(s);  // mirrored within 8 lanes: the other four's sum
+    s += moved<0x140>(s);  // mirrored within 16: the other eight's
+    // of two registers with the same rows of 16 lanes (halves of 32) a swap of one's odd
+    // rows with the other's even ones leaves a row and its neighbour side by side
+    auto both = [](double v, auto swap) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const auto lo = swap((uint32_t)u), hi = swap((uint32_t)(u >> 32));
+        return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) +
+               __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+    };
+    s = both(s, [](uint32_t w) { return __builtin_amdgcn_permlane16_swap(w, w, false, false); });
+    return both(s, [](uint32_t w) { return __builtin_amdgcn_permlane32_swap(w, w, false, false); });
+}
+
 // The sum over the workgroup, in a fixed order, in every thread.  red: one
 // double per possible wave, not used by an earlier sum of the same kernel.
 constexpr int kMaxWaves = kMaxThreads / 64;
 __device__ __forceinline__ double block_sum(double s, double* red) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    s = wave_sum(s);
     const int waves = blockDim.x / 64;
     if (waves == 1) return s;
     if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = s;

@@ -8,9 +8,9 @@
 //
 // One workgroup per token; its row stays in registers between the sums, so
 // every array is read or written once.  A thread holds runs of 8 neighbouring
-// columns, so 4 neighbouring threads hold the 32 columns of one 4-bit block; where
-// an array's rows do not take wide accesses (and no codes are written) it holds
-// single columns, neighbouring threads neighbouring ones.
+// columns, so 4 neighbouring threads hold the 32 columns of one 4-bit block; it
+// takes them in 16-byte accesses wherever the row begins, the last run of a row that
+// is no multiple of 8 one by one.
 //
 // What bounds it: with few tokens the latency of a chain of loads (slots, rows,
 // the norms' sums), with many the memory, as far as enough tokens are in flight
@@ -34,60 +34,37 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr int kRun = 8;  // columns of a thread's run
 
-struct NormArgs {
-    NormLaunch l;
-    int32_t vec_h, vec_y, vec_out, vec_x, vec_gate, vec_w, vec_u;  // rows of this array take 16-byte accesses
-};
-
-// Column i of a thread's run c.
-template <bool kSingle>
-__device__ __forceinline__ int column(int c, int i) {
-    const int n = blockDim.x, t = threadIdx.x;
-    return kSingle ? (c * kRun + i) * n + t : (c * n + t) * kRun + i;
-}
+// The first column of a thread's run c.
+__device__ __forceinline__ int column(int c) { return (c * (int)blockDim.x + (int)threadIdx.x) * kRun; }
 
 // A thread's run c of a row (columns at and past H: 0).
-template <bool kSingle, typename T>
-__device__ __forceinline__ void load_run(const T* row, int c, int H, bool vec, float* v) {
-    const int j = column<kSingle>(c, 0);
-    if (!kSingle && vec && j + kRun <= H) {
-        load8_vec(row + j, v);
+template <typename T>
+__device__ __forceinline__ void load_run(const T* row, int c, int H, float* v) {
+    const int j = column(c);
+    if (j + kRun <= H) {
+        load8(row + j, v);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) v[i] = column<kSingle>(c, i) < H ? widen(row[column<kSingle>(c, i)]) : 0.0f;
+    for (int i = 0; i < kRun; ++i) v[i] = j + i < H ? widen(row[j + i]) : 0.0f;
 }
-template <bool kSingle>
-__device__ __forceinline__ void load_run(const void* base, int dtype, int64_t at, int c, int H, bool vec, float* v) {
-    if (dtype == kF32) load_run<kSingle>((const float*)base + at, c, H, vec, v);
-    else if (dtype == kF16) load_run<kSingle>((const _Float16*)base + at, c, H, vec, v);
-    else load_run<kSingle>((const __bf16*)base + at, c, H, vec, v);
+__device__ __forceinline__ void load_run(const void* base, int dtype, int64_t at, int c, int H, float* v) {
+    if (dtype == kF32) load_run((const float*)base + at, c, H, v);
+    else if (dtype == kF16) load_run((const _Float16*)base + at, c, H, v);
+    else load_run((const __bf16*)base + at, c, H, v);
 }
-template <bool kSingle>
-__device__ __forceinline__ void store_run(void* base, int dtype, int64_t at, int c, int H, bool vec, const float* v) {
-    if (!kSingle) {
-        const int j = column<kSingle>(c, 0);
-        if (dtype == kF32) store8<float, v4f>((float*)base + at, j, H, vec, v);
-        else if (dtype == kF16) store8<_Float16, v8h>((_Float16*)base + at, j, H, vec, v);
-        else store8<__bf16, v8b>((__bf16*)base + at, j, H, vec, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-        const int j = column<kSingle>(c, i);
-        if (j >= H) continue;
-        if (dtype == kF32) ((float*)base)[at + j] = v[i];
-        else if (dtype == kF16) ((_Float16*)base)[at + j] = (_Float16)v[i];
-        else ((__bf16*)base)[at + j] = (__bf16)v[i];
-    }
+__device__ __forceinline__ void store_run(void* base, int dtype, int64_t at, int c, int H, const float* v) {
+    const int j = column(c);
+    if (dtype == kF32) store8<float, v4f_any>((float*)base + at, j, H, v);
+    else if (dtype == kF16) store8<_Float16, v8h_any>((_Float16*)base + at, j, H, v);
+    else store8<__bf16, v8b_any>((__bf16*)base + at, j, H, v);
 }
 
 // v = sum_k p[t][k] y[slot[t][k]], k ascending.  Lane k holds slot and p of k, so
 // that their loads are one, begun with the kernel (in the loop they cost 32 tokens
 // 8.1 us against 7.5, and 8192 159 against 156).
-template <int NC, bool kSingle, typename T>
-__device__ __forceinline__ void gather(const NormArgs& a, int slot, int p_bits, double (*v)[kRun]) {
-    const NormLaunch& l = a.l;
+template <int NC, typename T>
+__device__ __forceinline__ void gather(const NormLaunch& l, int slot, int p_bits, double (*v)[kRun]) {
     constexpr int kBatch = 2;
     for (int k0 = 0; k0 < l.K; k0 += kBatch) {
         int row[kBatch];
@@ -102,7 +79,7 @@ __device__ __forceinline__ void gather(const NormArgs& a, int slot, int p_bits, 
             // a row to read; used if it is the slot's
             const int64_t at = row[b] < 0 || row[b] >= l.y_rows ? 0 : row[b];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) load_run<kSingle>((const T*)l.y + at * l.y_stride, c, l.H, a.vec_y, y[b][c]);
+            for (int c = 0; c < NC; ++c) load_run((const T*)l.y + at * l.y_stride, c, l.H, y[b][c]);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -168,12 +145,12 @@ __device__ __forceinline__ double inverse_root(double v) {
     return __builtin_isfinite(r) ? r : e;
 }
 
-template <int NC, bool kSingle>
-__device__ __forceinline__ void apply_norm(double (*v)[kRun], const NormScale& n, bool vec, int H, double* red) {
+template <int NC>
+__device__ __forceinline__ void apply_norm(double (*v)[kRun], const NormScale& n, int H, double* red) {
     float w[NC][kRun];
     if (n.weight)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load_run<kSingle>(n.weight, c, H, vec, w[c]);
+        for (int c = 0; c < NC; ++c) load_run(n.weight, c, H, w[c]);
     double s = 0.0;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -190,10 +167,9 @@ __device__ __forceinline__ void apply_norm(double (*v)[kRun], const NormScale& n
         }
 }
 
-template <int NC, bool kSingle>
-__global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
+template <int NC>
+__global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormLaunch l) {
     __shared__ double red[2][kMaxWaves];
-    const NormLaunch& l = a.l;
     const int H = l.H;
     const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (t >= l.T) return;
@@ -203,20 +179,20 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
     double v[NC][kRun], h[NC][kRun];
     float in[NC][kRun];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) load_run<kSingle>(l.h, l.dtype, t * l.h_stride, c, H, a.vec_h, in[c]);
+    for (int c = 0; c < NC; ++c) load_run(l.h, l.dtype, t * l.h_stride, c, H, in[c]);
     if (l.y) {
         if (l.slot) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int i = 0; i < kRun; ++i) v[c][i] = 0.0;
-            if (l.y_dtype == kF32) gather<NC, kSingle, float>(a, slot, p_bits, v);
-            else if (l.y_dtype == kF16) gather<NC, kSingle, _Float16>(a, slot, p_bits, v);
-            else gather<NC, kSingle, __bf16>(a, slot, p_bits, v);
+            if (l.y_dtype == kF32) gather<NC, float>(l, slot, p_bits, v);
+            else if (l.y_dtype == kF16) gather<NC, _Float16>(l, slot, p_bits, v);
+            else gather<NC, __bf16>(l, slot, p_bits, v);
         } else {
             float y[NC][kRun];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) load_run<kSingle>(l.y, l.y_dtype, t * l.y_stride, c, H, a.vec_y, y[c]);
+            for (int c = 0; c < NC; ++c) load_run(l.y, l.y_dtype, t * l.y_stride, c, H, y[c]);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -228,7 +204,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < kRun; ++i) h[c][i] = in[c][i];
     if (l.y) {
-        if (l.after.on) apply_norm<NC, kSingle>(v, l.after, a.vec_w, H, red[0]);
+        if (l.after.on) apply_norm<NC>(v, l.after, H, red[0]);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float g[kRun], o[kRun];
@@ -236,7 +212,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
             for (int i = 0; i < kRun; ++i) g[i] = 1.0f;
             if (l.gate) {
                 const float* gr = l.gate + t * l.gate_row_stride;
-                if (l.gate_col_stride) load_run<kSingle>(gr, c, H, a.vec_gate, g);
+                if (l.gate_col_stride) load_run(gr, c, H, g);
                 else
 #pragma unroll
                     for (int i = 0; i < kRun; ++i) g[i] = *gr;
@@ -244,19 +220,19 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < kRun; ++i)
                 h[c][i] = round_to(fma(l.residual_scale, h[c][i], l.block_scale * (g[i] * v[c][i])), l.dtype, &o[i]);
-            store_run<kSingle>(l.out, l.dtype, t * l.out_stride, c, H, a.vec_out, o);
+            store_run(l.out, l.dtype, t * l.out_stride, c, H, o);
         }
     }
     if (!l.before.on) return;
-    apply_norm<NC, kSingle>(h, l.before, a.vec_u, H, red[1]);
+    apply_norm<NC>(h, l.before, H, red[1]);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         float o[kRun];
 #pragma unroll
         for (int i = 0; i < kRun; ++i) o[i] = (float)h[c][i];
-        if (l.x) store_run<kSingle>(l.x, kF32, t * H, c, H, a.vec_x, o);
-        if (!kSingle && l.codes) {  // H is a multiple of 32, so a block's 4 threads are all inside or all outside
-            const int j = column<kSingle>(c, 0);
+        if (l.x) store_run(l.x, kF32, t * H, c, H, o);
+        if (l.codes) {  // H is a multiple of 32, so a block's 4 threads are all inside or all outside
+            const int j = column(c);
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < kRun; ++i) top = max(top, __float_as_uint(o[i]) & 0x7fffffffu);
@@ -275,36 +251,18 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
     }
 }
 
-template <bool kSingle>
-hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
-    const int runs = (a.l.H + kRun - 1) / kRun;
-    const int threads = runs >= kMaxThreads ? kMaxThreads : (runs + 63) / 64 * 64;
-    // less than 2^32 threads along x
-    const int64_t most = (int64_t)1 << 21;
-    const dim3 grid((uint32_t)std::min(a.l.T, most), (uint32_t)((a.l.T + most - 1) / most)), block(threads);
-    if (runs <= threads) hipLaunchKernelGGL((norm_kernel<1, kSingle>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((norm_kernel<2, kSingle>), grid, block, 0, st, a);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_norm(const NormLaunch& l, hipStream_t st) {
-    NormArgs a{};
-    a.l = l;
-    auto vec = [](const void* p, int64_t stride, size_t el) {
-        return ((uintptr_t)p | (uintptr_t)(stride * (int64_t)el)) % 16 == 0 ? 1 : 0;
-    };
     static_assert(kNormMaxH <= 2 * kMaxThreads * kRun, "two runs a thread");
-    a.vec_h = vec(l.h, l.h_stride, dtype_bytes(l.dtype));
-    a.vec_out = vec(l.out, l.out_stride, dtype_bytes(l.dtype));
-    a.vec_y = vec(l.y, l.y_stride, dtype_bytes(l.y_dtype));
-    a.vec_x = vec(l.x, l.H, 4);
-    a.vec_gate = vec(l.gate, l.gate_row_stride, 4);
-    a.vec_w = vec(l.after.weight, 0, 4);
-    a.vec_u = vec(l.before.weight, 0, 4);
-    const bool wide = l.H % kRun == 0 && a.vec_h && a.vec_out && a.vec_y && a.vec_x && a.vec_gate && a.vec_w && a.vec_u;
-    return wide || l.codes ? launch_rows<false>(a, st) : launch_rows<true>(a, st);
+    const int runs = (l.H + kRun - 1) / kRun;
+    const int threads = runs >= kMaxThreads ? kMaxThreads : (runs + 63) / 64 * 64;
+    // less than 2^32 threads along x
+    const int64_t most = (int64_t)1 << 21;
+    const dim3 grid((uint32_t)std::min(l.T, most), (uint32_t)((l.T + most - 1) / most)), block(threads);
+    if (runs <= threads) hipLaunchKernelGGL(norm_kernel<1>, grid, block, 0, st, l);
+    else hipLaunchKernelGGL(norm_kernel<2>, grid, block, 0, st, l);
+    return hipGetLastError();
 }
 
 }  // namespace strata_moe

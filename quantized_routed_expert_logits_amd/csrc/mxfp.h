@@ -7,6 +7,7 @@
 namespace strata_moe {
 
 typedef float v2f __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef __bf16 v4b __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
@@ -31,19 +32,25 @@ __device__ __forceinline__ void load4_vec(const __bf16* p, float* v) {
     v[2] = __uint_as_float(f.y << 16), v[3] = __uint_as_float(f.y & 0xffff0000u);
 }
 
-// 8 values from a 16-byte aligned row.
-__device__ __forceinline__ void load8_vec(const float* p, float* v) {
-    load4_vec(p, v);
-    load4_vec(p + 4, v + 4);
+// 16 bytes at an element's address: the memory takes wide accesses at any of them.
+typedef v4f v4f_any __attribute__((aligned(4)));
+typedef v8h v8h_any __attribute__((aligned(2)));
+typedef v8b v8b_any __attribute__((aligned(2)));
+typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// 8 neighbouring values.
+__device__ __forceinline__ void load8(const float* p, float* v) {
+    const v4f a = *(const v4f_any*)p, b = *(const v4f_any*)(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
 }
-__device__ __forceinline__ void load8_vec(const _Float16* p, float* v) {
-    const v8h f = *(const v8h*)p;
+__device__ __forceinline__ void load8(const _Float16* p, float* v) {
+    const v8h f = *(const v8h_any*)p;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = (float)f[i];
 }
-__device__ __forceinline__ void load8_vec(const __bf16* p, float* v) {
-    const uint4 f = *(const uint4*)p;
-    const uint32_t u[4] = {f.x, f.y, f.z, f.w};
+__device__ __forceinline__ void load8(const __bf16* p, float* v) {
+    const v4u_any u = *(const v4u_any*)p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(u[i] << 16);
@@ -65,13 +72,11 @@ __device__ __forceinline__ void store4(T* row, int j, int H, bool vec, const flo
     for (int i = 0; i < 4; ++i)
         if (j + i < H) row[j + i] = (T)v[i];
 }
-typedef float v4f __attribute__((ext_vector_type(4)));
-
 // v (8 values) to columns j..j+7 of a row of H, 16 bytes a store.
 template <typename T, typename V>
-__device__ __forceinline__ void store8(T* row, int j, int H, bool vec, const float* v) {
+__device__ __forceinline__ void store8(T* row, int j, int H, const float* v) {
     constexpr int n = 16 / (int)sizeof(T);
-    if (vec && j + 8 <= H) {
+    if (j + 8 <= H) {
 #pragma unroll
         for (int k = 0; k < 8; k += n) {
             V o;

@@ -494,7 +494,8 @@ int strata_moe_mxfp_pack(const uint8_t* codes, const uint8_t* scales, int32_t e0
  *            `dtype`, out_stride elements apart; must not overlap an input
  * rows and x_rows are at most 2^24 and x_rows * cols below 2^33.  No workspace;
  * the call only enqueues one kernel, so calls may overlap and be captured, and
- * repeated calls give the same bits.  Errors: EINVAL for sizes, NULL pointers,
+ * repeated calls give the same bits; strata_moe_timing sees neither these calls
+ * nor those of the norms below.  Errors: EINVAL for sizes, NULL pointers,
  * alignment, strides or overlap, EUNSUPPORTED for an unknown dtype. */
 int strata_moe_mxfp_product(const uint8_t* codes, const uint8_t* scales, int64_t x_rows,
                             const strata_moe_mxfp_weights* weights, const int32_t* offsets, const int32_t* src,
@@ -517,7 +518,8 @@ typedef struct strata_moe_norm {
  *       32), or both NULL
  * 0 <= T <= 2^24, 1 <= H <= 16384.  The arithmetic is in fp64, each output is
  * rounded to fp32 (norm_after's out from there to its type).  Outputs overlap
- * neither each other nor an input.  Errors: EINVAL for sizes, NULL pointers,
+ * neither each other nor an input.  Each call enqueues one kernel, has no
+ * workspace and gives the same bits again.  Errors: EINVAL for sizes, NULL pointers,
  * alignment, strides or overlap, EUNSUPPORTED for an unknown dtype. */
 int strata_moe_norm_before(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H,
                            const strata_moe_norm* norm, float* x, uint8_t* codes, uint8_t* scales, void* stream);

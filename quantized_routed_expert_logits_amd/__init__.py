@@ -660,13 +660,16 @@ def strata_moe_decode(x: torch.Tensor, router_w: torch.Tensor, experts: Experts,
 # each tensor's properties once and go past torch's context managers.
 _Tensor = torch.Tensor
 _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_row_code = ROW_DTYPES.get
 
 
-def _float_rows(t, name: str, rows: int | None = None, width: int | None = None) -> int:
-    """A [rows][width] fp32, fp16 or bf16 tensor with contiguous rows that do not overlap -> its row stride."""
+def _float_rows(t, name: str, rows: int | None = None, width: int | None = None) -> tuple[int, int, int, int]:
+    """A [rows][width] fp32, fp16 or bf16 tensor with contiguous rows that do not overlap -> (rows, width, row
+    stride, type code)."""
     if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype not in ROW_DTYPES:
+    code = _row_code(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be one of {sorted(str(d) for d in ROW_DTYPES)}, got {t.dtype}")
     shape = t.shape
     if len(shape) != 2 or (rows is not None and shape[0] != rows) or (width is not None and shape[1] != width):
@@ -674,11 +677,11 @@ def _float_rows(t, name: str, rows: int | None = None, width: int | None = None)
         raise ValueError(f"{name} has shape {tuple(shape)}, expected {want}")
     n, w = shape
     if t.is_contiguous():
-        return w
+        return n, w, w, code
     stride, col = t.stride()
     if (w > 1 and n > 0 and col != 1) or (n > 1 and stride < w):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return stride if n > 1 else w
+    return n, w, stride if n > 1 else w, code
 
 
 def _array(t, name: str, shape: tuple, dt, dev: int):
@@ -703,10 +706,10 @@ def _same_device(t, name: str, dev: int):
         raise ValueError(f"{name} is on another device")
 
 
-def _run_on(dev: int, stream, what: str, fn, *args) -> None:
+def _run_on(dev: int, stream, fn, *args) -> None:
     """fn(*args, stream) with device `dev` current, on its current stream if none is given."""
     if dev < 0:
-        raise TypeError(f"{what} takes CUDA (HIP) tensors")
+        raise TypeError(f"{fn.__name__} takes CUDA (HIP) tensors")
     st = _raw_stream(dev) if stream is None else stream.cuda_stream
     if _get_device() == dev:
         rc = fn(*args, st)
@@ -714,7 +717,7 @@ def _run_on(dev: int, stream, what: str, fn, *args) -> None:
         with torch.cuda.device(dev):
             rc = fn(*args, st)
     if rc:
-        _check(rc, what)
+        _check(rc, fn.__name__)
 
 
 def _new_bytes(shape: tuple, like: torch.Tensor, stream) -> torch.Tensor:
@@ -727,8 +730,7 @@ def strata_moe_mxfp_quantize(x: torch.Tensor, codes: torch.Tensor | None = None,
                              stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """x [rows][cols] (fp32, fp16 or bf16; rows may be padded) -> codes uint8 [rows][cols/2], two 4-bit values a
     byte, and scales uint8 [rows][cols/32], powers of two."""
-    xs = _float_rows(x, "x")
-    rows, cols = x.shape
+    rows, cols, xs, code = _float_rows(x, "x")
     dev = x.get_device()
     if dev < 0:
         raise TypeError("x must be a CUDA (HIP) tensor")
@@ -736,8 +738,8 @@ def strata_moe_mxfp_quantize(x: torch.Tensor, codes: torch.Tensor | None = None,
         codes = _new_bytes((rows, cols // 2), x, stream)
     if scales is None:
         scales = _new_bytes((rows, cols // 32), x, stream)
-    _run_on(dev, stream, "strata_moe_mxfp_quantize", _lib.strata_moe_mxfp_quantize, x.data_ptr(), ROW_DTYPES[x.dtype],
-            xs, rows, cols, _array(codes, "codes", (rows, cols // 2), torch.uint8, dev),
+    _run_on(dev, stream, _lib.strata_moe_mxfp_quantize, x.data_ptr(), code, xs, rows, cols,
+            _array(codes, "codes", (rows, cols // 2), torch.uint8, dev),
             _array(scales, "scales", (rows, cols // 32), torch.uint8, dev))
     return codes, scales
 
@@ -745,15 +747,12 @@ def strata_moe_mxfp_quantize(x: torch.Tensor, codes: torch.Tensor | None = None,
 def strata_moe_mxfp_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor,
                                stream=None) -> torch.Tensor:
     """The values that codes and scales stand for, into out [rows][cols] (fp32, fp16 or bf16; rows may be padded)."""
-    os_ = _float_rows(out, "out")
-    rows, cols = out.shape
+    rows, cols, os_, code = _float_rows(out, "out")
     dev = out.get_device()
     if codes is None or scales is None:
         raise TypeError("codes and scales must be torch tensors")
-    _run_on(dev, stream, "strata_moe_mxfp_dequantize", _lib.strata_moe_mxfp_dequantize,
-            _array(codes, "codes", (rows, cols // 2), torch.uint8, dev),
-            _array(scales, "scales", (rows, cols // 32), torch.uint8, dev), rows, cols, out.data_ptr(),
-            ROW_DTYPES[out.dtype], os_)
+    _run_on(dev, stream, _lib.strata_moe_mxfp_dequantize, _array(codes, "codes", (rows, cols // 2), torch.uint8, dev),
+            _array(scales, "scales", (rows, cols // 32), torch.uint8, dev), rows, cols, out.data_ptr(), code, os_)
     return out
 
 
@@ -794,8 +793,8 @@ def strata_moe_mxfp_pack(codes: torch.Tensor, scales: torch.Tensor, e0: int, wei
     args = (_array(codes, "codes", (n, weights.rows, weights.cols // 2), torch.uint8, dev),
             _array(scales, "scales", (n, weights.rows, weights.cols // 32), torch.uint8, dev))
     _same_device(weights.packed, "weights", dev)
-    _run_on(dev, stream, "strata_moe_mxfp_pack", _lib.strata_moe_mxfp_pack, *args, e0, e0 + n, weights.rows,
-            weights.cols, int(weights.swiglu), weights.packed.data_ptr(), weights.stride)
+    _run_on(dev, stream, _lib.strata_moe_mxfp_pack, *args, e0, e0 + n, weights.rows, weights.cols, int(weights.swiglu),
+            weights.packed.data_ptr(), weights.stride)
 
 
 def strata_moe_mxfp_product(codes: torch.Tensor, scales: torch.Tensor, weights: MxfpWeights, out: torch.Tensor,
@@ -811,20 +810,20 @@ def strata_moe_mxfp_product(codes: torch.Tensor, scales: torch.Tensor, weights: 
     if scales is None:
         raise TypeError("scales must be a torch tensor")
     x_rows = codes.shape[0]
-    os_ = _float_rows(out, "out", None, weights.n_out)
-    rows, dev = out.shape[0], out.get_device()
+    rows, _, os_, code = _float_rows(out, "out", None, weights.n_out)
+    dev = out.get_device()
     args = (_array(codes, "codes", (x_rows, weights.cols // 2), torch.uint8, dev),
             _array(scales, "scales", (x_rows, weights.cols // 32), torch.uint8, dev), x_rows,
             ctypes.byref(weights.struct), _array(offsets, "offsets", (weights.n_expert + 1,), torch.int32, dev),
             _array(src, "src", (rows,), torch.int32, dev))
     _same_device(weights.packed, "weights", dev)
-    _run_on(dev, stream, "strata_moe_mxfp_product", _lib.strata_moe_mxfp_product, *args, rows, out.data_ptr(),
-            ROW_DTYPES[out.dtype], os_)
+    _run_on(dev, stream, _lib.strata_moe_mxfp_product, *args, rows, out.data_ptr(), code, os_)
     return out
 
 
 class Norm:
-    """A root mean square norm: v / sqrt(mean(v^2) + eps) * (weight_offset + weight); weight [H] float32 or None."""
+    """A root mean square norm: v / sqrt(mean(v^2) + eps) * (weight_offset + weight); weight [H] float32 or None.
+    The weight's memory is read by each call; eps, the offset and which memory it is are fixed here."""
 
     def __init__(self, weight: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0):
         self.width = self.device = None
@@ -869,11 +868,10 @@ def strata_moe_norm_before(h: torch.Tensor, norm: Norm, x: torch.Tensor | None =
     padded), and with codes and scales (uint8, as strata_moe_mxfp_quantize) x in 4 bits."""
     if norm is None:
         raise TypeError("norm must be a Norm object")
-    hs = _float_rows(h, "h")
-    T, H = h.shape
+    T, H, hs, code = _float_rows(h, "h")
     dev = h.get_device()
-    _run_on(dev, stream, "strata_moe_norm_before", _lib.strata_moe_norm_before, h.data_ptr(), ROW_DTYPES[h.dtype], hs,
-            T, H, _norm(norm, "norm", H, dev), *_norm_outputs(x, codes, scales, T, H, dev))
+    _run_on(dev, stream, _lib.strata_moe_norm_before, h.data_ptr(), code, hs, T, H,
+            _norm(norm, "norm", H, dev), *_norm_outputs(x, codes, scales, T, H, dev))
 
 
 def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, norm: Norm | None = None,
@@ -885,17 +883,16 @@ def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, n
     """out = residual_scale h + block_scale gate norm(v), v[t] = y[t], or with slot and p [T][K] the sum over k of
     p[t][k] y[slot[t][k]].  gate: float32 [H], [T][1] or [T][H].  out may be h.  next_norm: also the next block's
     input x = next_norm(out) (x, codes and scales as in strata_moe_norm_before)."""
-    hs = _float_rows(h, "h")
-    T, H = h.shape
+    T, H, hs, code = _float_rows(h, "h")
     dev = h.get_device()
     if out is h:
         os_ = hs
     else:
-        os_ = _float_rows(out, "out", T, H)
-        if out.dtype is not h.dtype:
+        _, _, os_, out_code = _float_rows(out, "out", T, H)
+        if out_code != code:
             raise TypeError(f"out must be {h.dtype}, got {out.dtype}")
         _same_device(out, "out", dev)
-    ys = _float_rows(y, "y", None, H)
+    y_rows, _, ys, y_code = _float_rows(y, "y", None, H)
     _same_device(y, "y", dev)
     K, slots, weights = 0, None, None
     if (slot is None) != (p is None):
@@ -905,8 +902,8 @@ def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, n
             raise ValueError("slot must be [T][K]")
         K = slot.shape[1]
         slots, weights = _array(slot, "slot", (T, K), torch.int32, dev), _array(p, "p", (T, K), torch.float32, dev)
-    elif y.shape[0] != T:
-        raise ValueError(f"y has {y.shape[0]} rows for {T} tokens")
+    elif y_rows != T:
+        raise ValueError(f"y has {y_rows} rows for {T} tokens")
     gates, grow, gcol = None, 0, 0
     if gate is not None:
         if not isinstance(gate, _Tensor):
@@ -923,11 +920,10 @@ def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, n
             raise ValueError("gate must have contiguous or broadcast rows")
         _same_device(gate, "gate", dev)
         gates = gate.data_ptr()
-    branch = BranchStruct(y.data_ptr(), ys, y.shape[0], ROW_DTYPES[y.dtype], K, slots, weights,
+    branch = BranchStruct(y.data_ptr(), ys, y_rows, y_code, K, slots, weights,
                           _norm(norm, "norm", H, dev), gates, grow, gcol, residual_scale, block_scale)
-    _run_on(dev, stream, "strata_moe_norm_after", _lib.strata_moe_norm_after, h.data_ptr(), ROW_DTYPES[h.dtype], hs, T,
-            H, ctypes.byref(branch), out.data_ptr(), os_, _norm(next_norm, "next_norm", H, dev),
-            *_norm_outputs(x, codes, scales, T, H, dev))
+    _run_on(dev, stream, _lib.strata_moe_norm_after, h.data_ptr(), code, hs, T, H, ctypes.byref(branch),
+            out.data_ptr(), os_, _norm(next_norm, "next_norm", H, dev), *_norm_outputs(x, codes, scales, T, H, dev))
     return out
 
 

@@ -20,7 +20,11 @@ typedef int v2i __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------ rounding and reading
-// A thread takes 8 consecutive values, 4 threads a block of 32.
+// A thread takes 8 consecutive values, 4 threads a block of 32: its largest magnitude
+// goes between them by two exchanges, and neighbouring threads read and write
+// neighbouring bytes.  The memory bounds both ways: 8192 rows of 2560 in fp32 take
+// 14.5 us to round and 16.7 to read back (6.6 and 5.7 TB/s, partly from the last
+// cache), 203 rows of 1056 in bf16 2.4 and 2.2, a launch.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const T* __restrict__ x, int64_t x_stride, uint32_t runs,
                                                             uint32_t row_runs, int vec, uint8_t* __restrict__ codes,
@@ -232,8 +236,9 @@ __device__ __forceinline__ void store_out(const ProductArgs& a, int32_t row, int
     store4_any(a.p.out, a.p.dtype, row * a.p.out_stride, n, a.n_out, a.vec_out4, f);
 }
 
-// Few rows: latency bounds it.  An item is up to 16 rows of an expert times kFewTiles
-// tiles of its weights.  A wave takes up to four steps at a time, so with a wave
+// Few rows: latency bounds it (one token's ten experts, 2560 -> 2 x 1024: 7.4 us, of
+// which the 28 MB of weights need 5.5; 406 rows of six experts, 544 -> 333: 5.8).  An
+// item is up to 16 rows of an expert times kFewTiles tiles of its weights.  A wave takes up to four steps at a time, so with a wave
 // for every four of them all loads of an item are in flight together; the waves'
 // sums are added in wave order through LDS.
 // kList: the items of the work list, shared out.  Otherwise a workgroup per row
@@ -366,10 +371,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(ProductArgs a) {
 // tiles come in pairs: an item of fewer rows leaves out the pairs it lacks.
 //
 // What bounds it: where an expert has a few hundred rows, the memory (8192 tokens,
-// ten of 512 experts, 2560 -> 2 x 1024 SwiGLU: 395 us; it moves 1.97 GB, 4.9 TB/s of a
+// ten of 512 experts, 2560 -> 2 x 1024 SwiGLU: 400 us; it moves 1.97 GB, 4.9 TB/s of a
 // copy's 5.1, of which 1.6 it cannot do without: the rest is rows read again past an
-// L2, 0.26 GB, and weights, 0.09; down 1024 -> 2560: 245 us, 1.18 GB).  With one
-// matrix, the matrix unit and what feeds it (8192 rows, 4096 -> 4096: 75 us, 3.7
+// L2, 0.26 GB, and weights, 0.09; down 1024 -> 2560: 255 to 263 us, 1.2 GB).  With one
+// matrix, the matrix unit and what feeds it (8192 rows, 4096 -> 4096: 77 us, 3.6
 // PFLOP/s; the unit alone reaches 6.7 to 7.3 on random values; without weight loads
 // 63, without rows' 74, without both and the stores 54).
 //

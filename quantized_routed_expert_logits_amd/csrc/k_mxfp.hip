@@ -236,11 +236,12 @@ __device__ __forceinline__ void store_out(const ProductArgs& a, int32_t row, int
     store4_any(a.p.out, a.p.dtype, row * a.p.out_stride, n, a.n_out, a.vec_out4, f);
 }
 
-// Few rows: latency bounds it (one token's ten experts, 2560 -> 2 x 1024: 7.4 us, of
-// which the 28 MB of weights need 5.5; 406 rows of six experts, 544 -> 333: 5.8).  An
-// item is up to 16 rows of an expert times kFewTiles tiles of its weights.  A wave takes up to four steps at a time, so with a wave
-// for every four of them all loads of an item are in flight together; the waves'
-// sums are added in wave order through LDS.
+// Few rows: latency bounds it (one token's ten experts, 2560 -> 2 x 1024: 7.4 us,
+// of which the 28 MB of weights need 5.5; 406 rows of six experts, 544 -> 333:
+// 5.8).  An item is up to 16 rows of an expert times kFewTiles tiles of its
+// weights.  A wave takes up to four steps at a time, so with a wave for every four
+// of them all loads of an item are in flight together; the waves' sums are added
+// in wave order through LDS.
 // kList: the items of the work list, shared out.  Otherwise a workgroup per row
 // and run, which looks the row's expert up and works if the row begins one of the
 // expert's tiles: no list, no scan, the offsets and the rows' sources in one

@@ -460,7 +460,8 @@ int strata_moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int6
  *   rows, cols: of one matrix (rows in [1, 65536]; the reduction is over cols)
  *   swiglu: 1 if a matrix is [gate; up] (rows even) and the product's output
  *           silu(gate x) (up x) of rows / 2 values, silu(v) = v / (1 + exp(-v))
- *           (0 from some v below -87 on, where it is under 2^-118)
+ *           (0 from some finite v below -87 on, where it is under 2^-118; NaN for
+ *           -inf, v itself for large v and +inf)
  *   stride: a multiple of 256, at least strata_moe_mxfp_packed_bytes(), at
  *           most 2^32 */
 typedef struct strata_moe_mxfp_weights {

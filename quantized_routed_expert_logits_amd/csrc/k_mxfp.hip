@@ -222,12 +222,14 @@ __device__ __forceinline__ Item find_item(const MxProduct& p, const List& L, int
 __device__ __forceinline__ v8i operand(v4i q) { return v8i{q[0], q[1], q[2], q[3], 0, 0, 0, 0}; }
 
 // silu(g) u, silu(g) = g / (1 + exp(-g)).  exp by 2^(-g log2 e), the product in
-// two parts: its rounding alone would cost |g| 2^-24 of the result.
+// two parts: its rounding alone would cost |g| 2^-24 of the result.  Where the power
+// is 0 or infinite (also g = +-inf, and g past 2.35e38, where the product is) the
+// second part is left out: it is infinite or NaN there itself.
 __device__ __forceinline__ float swiglu(float g, float u) {
     const float hi = -g * 1.44269502f;
     const float lo = fmaf(-g, 1.44269502f, -hi) + -g * 1.92596303e-8f;
     float e = __builtin_amdgcn_exp2f(hi);
-    if (e < __builtin_inff()) e = fmaf(e, lo * 0.693147182f, e);
+    if (e > 0.0f && e < __builtin_inff()) e = fmaf(e, lo * 0.693147182f, e);
     return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 

@@ -348,6 +348,52 @@ def test_a_row_s_result_does_not_depend_on_its_neighbours(qm, rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("rows", [64, 960, 2500])  # a workgroup per row and run, the list, the kernel of many rows
+def test_swiglu_over_the_whole_range(qm, rows, dtype):
+    """Gates to both ends of fp32 and past them, with ups of every size: the gate and
+    the up of an output are sums of two products that are exact in fp32."""
+    two = (0.0, 0)  # (magnitude, exponent) of a product
+    gates = [((1.0, 127), (1.5, 125)), ((1.0, 127), (1.5, 126)), ((1.5, 127), two), ((1.5, 127), (1.5, 125)),
+             ((6.0, 127), two), ((1.0, 6), (1.5, 4)), ((1.0, 0), two), (two, two), ((1.5, 100), two)]
+    ups = [((1.0, -33), two), ((1.5, -100), two), ((1.0, 0), two), ((1.5, 14), (1.0, 3)), ((1.0, 100), two),
+           ((6.0, 127), two), (two, two)]
+    pairs = [(g, u) for g in gates for u in ups]
+    n = 320
+    pairs = [pairs[j % len(pairs)] for j in range(n)]
+    code = {0.0: 0, 1.0: 2, 1.5: 3, 6.0: 7}
+    wc, ws = torch.zeros((1, 2 * n, 64), dtype=torch.uint8), torch.full((1, 2 * n, 4), 127, dtype=torch.uint8)
+    sums = np.zeros(2 * n)
+    for j, pair in enumerate(pairs):
+        for half in range(2):
+            for i, (m, e) in enumerate(pair[half]):  # x is 2^63 in the gates' blocks, 1 in the ups'
+                b, row = 2 * half + i, half * n + j
+                byte = e + 127 - (0 if half or m == 0.0 else 63)
+                assert 0 <= byte <= 254
+                wc[0, row, 16 * b], ws[0, row, b] = code[m], byte
+                sums[row] += m * 2.0 ** e
+    xc, xs = torch.zeros((rows, 64), dtype=torch.uint8), torch.full((rows, 4), 127, dtype=torch.uint8)
+    sign = np.where(np.arange(rows) % 3 == 1, -1.0, 1.0)
+    xc[:, ::16] = torch.from_numpy(np.where(sign < 0, 10, 2).astype(np.uint8))[:, None]
+    xs[:, :2] = 63 + 127
+    weights = qm.MxfpWeights(1, 2 * n, 128, swiglu=True).pack(0, wc.cuda(), ws.cuda())
+    out = _np(qm.strata_moe_mxfp_product(xc.cuda(), xs.cuda(), weights, torch.empty((rows, n), dtype=dtype).cuda()))
+    with np.errstate(all="ignore"):
+        y = (sign[:, None] * sums).astype(np.float32).astype(np.float64)  # infinite from 2^128 on
+        g, u = y[:, :n], y[:, n:]
+        want = g / (1.0 + np.exp(-g)) * u
+        # the output's rounding, and the arithmetic as ref.product has it: 12 roundings, 0 below -87
+        fi = torch.finfo(dtype)
+        tol = ref.rounding(fi.eps, fi.smallest_normal * fi.eps, want) + 12 * 2.0 ** -23 * np.abs(want)
+        tol = np.where(g < -87, tol + 2.0 ** -118 * np.abs(u), tol)
+        border = fi.max * (1.0 + fi.eps / 2 / (2.0 - fi.eps))  # from here on the nearest is infinity
+        over = np.isinf(out) & (np.abs(want) + tol >= border) & (np.sign(out) == np.sign(want))
+        ok = (np.abs(out - want) <= tol) | over | (np.isnan(out) & np.isnan(want))
+    ok |= (g < -87) & (g > -100) & np.isinf(u)  # 0 times infinity there: 0 is what the gate may be
+    assert ok.all(), [(g[i], u[i], out[i], want[i]) for i in map(tuple, np.argwhere(~ok)[:5])]
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,n_e", [(3, 1), (50, 8), (3000, 8)])
 def test_repeated_calls_give_the_same_bits(qm, rows, n_e):
     xc, xs, wc, ws = _operands(rows, 640, 200, n_e, seed=6)

@@ -490,7 +490,7 @@ int strata_moe_mxfp_pack(const uint8_t* codes, const uint8_t* scales, int32_t e0
  *            rows are its.  Read on the device, within [0, rows]; rows that no
  *            expert has are left as they were.
  *   src:     [rows] int32 on the device, or NULL: row r of x (x_rows >= rows).
- *            A row whose src is outside [0, x_rows) counts as zeros.
+ *            A row whose src is outside [0, x_rows) is 0, whatever the weights.
  *   out:     [rows] rows of weights->rows values (rows / 2 with swiglu) of
  *            `dtype`, out_stride elements apart; must not overlap an input
  * rows and x_rows are at most 2^24 and x_rows * cols below 2^33.  No workspace;

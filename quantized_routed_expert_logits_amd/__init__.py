@@ -802,7 +802,7 @@ def strata_moe_mxfp_product(codes: torch.Tensor, scales: torch.Tensor, weights: 
                             stream=None) -> torch.Tensor:
     """out[r] = W_e x[src[r]] for the rows r of expert e, [offsets[e], offsets[e+1]).  codes, scales: x in 4 bits;
     out [rows][n_out] fp32, fp16 or bf16 (rows may be padded).  One expert needs no offsets; without src row r is
-    x's row r."""
+    x's row r; a row whose src is outside x is 0."""
     if not isinstance(weights, MxfpWeights):
         raise TypeError("weights must be an MxfpWeights object")
     if not isinstance(codes, _Tensor) or codes.dim() != 2:

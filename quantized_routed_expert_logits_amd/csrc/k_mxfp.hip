@@ -309,6 +309,7 @@ __device__ __forceinline__ void few_item(const ProductArgs& a, int e, int run, i
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], up[i]);
         }
+        if (src < 0) v = v4f{0, 0, 0, 0};  // zeros times a weight of NaN are not 0
         const int n = (run * kFewTiles + f) / per * kMxTileRows + 4 * g;
         if (r16 < rows && n < a.n_out) store_out(a, row + r16, n, v);
     }

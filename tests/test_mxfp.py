@@ -394,6 +394,30 @@ def test_swiglu_over_the_whole_range(qm, rows, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("rows,n", [(30, 50), (700, 50), (4000, 400)])  # one in each of the three kernels
+def test_src_outside_x_gives_zeros_whatever_the_weights(qm, rows, n, swiglu):
+    """Weights that hold NaN blocks: a row with a source is NaN at their outputs, a row without one 0 everywhere."""
+    xc, xs, wc, ws = _operands(9, 160, n, 3, seed=20)
+    for e in range(3):
+        ws[e, e::7, e] = 255
+    src = torch.randint(-3, 12, (rows,), generator=torch.Generator().manual_seed(21)).int()
+    src[0], src[1] = -2 ** 31, 2 ** 31 - 1
+    off = _offsets(3, rows, 22)
+    n_out = n // 2 if swiglu else n
+    out = torch.full((rows, n_out), 7.0, device="cuda")
+    qm.strata_moe_mxfp_product(xc, xs, qm.MxfpWeights(3, n, 160, swiglu=swiglu).pack(0, wc, ws), out, offsets=off,
+                               src=src.cuda())
+    nan = (ws == 255).any(-1).cpu()
+    nan = nan[:, :n_out] | nan[:, -n_out:]
+    expert = torch.bucketize(torch.arange(rows, dtype=torch.int32), off.cpu()[1:], right=True)
+    outside = (src < 0) | (src >= 9)
+    out = out.cpu()
+    assert torch.all(out[outside] == 0)
+    assert torch.equal(torch.isnan(out[~outside]), nan[expert[~outside]])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,n_e", [(3, 1), (50, 8), (3000, 8)])
 def test_repeated_calls_give_the_same_bits(qm, rows, n_e):
     xc, xs, wc, ws = _operands(rows, 640, 200, n_e, seed=6)

@@ -901,6 +901,8 @@ def strata_moe_norm_after(h: torch.Tensor, y: torch.Tensor, out: torch.Tensor, n
         if not isinstance(slot, _Tensor) or slot.dim() != 2:
             raise ValueError("slot must be [T][K]")
         K = slot.shape[1]
+        if K == 0:  # without memory the tensors would pass for None
+            raise ValueError("slot must have at least one row of y a token")
         slots, weights = _array(slot, "slot", (T, K), torch.int32, dev), _array(p, "p", (T, K), torch.float32, dev)
     elif y_rows != T:
         raise ValueError(f"y has {y_rows} rows for {T} tokens")

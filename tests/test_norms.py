@@ -381,6 +381,15 @@ def test_no_tokens_is_a_no_op(qm):
     assert lib.strata_moe_norm_after(None, 1, 64, 0, 64, ctypes.byref(b), None, 64, None, None, None, None, None) == 0
 
 
+def test_no_choices_are_not_no_combine(qm):
+    """slot and p of [T][0]: their memory is a null pointer, which to the library says that there are none."""
+    h = torch.zeros((4, 64))
+    none = dict(slot=torch.zeros((4, 0), dtype=torch.int32), p=torch.zeros((4, 0)))
+    for rows in (4, 9):
+        with pytest.raises(ValueError):
+            qm.strata_moe_norm_after(h, torch.zeros((rows, 64)), h.clone(), **none)
+
+
 def test_the_binding_checks_its_tensors(qm):
     h, x = torch.zeros((4, 64)), torch.zeros((4, 64))
     n = qm.Norm(None)

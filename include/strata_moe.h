@@ -517,11 +517,12 @@ typedef struct strata_moe_norm {
  *   x:  [T][H] fp32 (what strata_moe_prefill and strata_moe_decode take), or NULL
  *   codes, scales: x rounded as strata_moe_mxfp_quantize does (H a multiple of
  *       32), or both NULL
- * 0 <= T <= 2^24, 1 <= H <= 16384.  The arithmetic is in fp64, each output is
- * rounded to fp32 (norm_after's out from there to its type).  Outputs overlap
- * neither each other nor an input.  Each call enqueues one kernel, has no
- * workspace and gives the same bits again.  Errors: EINVAL for sizes, NULL pointers,
- * alignment, strides or overlap, EUNSUPPORTED for an unknown dtype. */
+ * 0 <= T <= 2^24, 1 <= H <= 16384; with T = 0 the arrays of rows may be NULL.  The
+ * arithmetic is in fp64, each output is rounded to fp32 (norm_after's out from
+ * there to its type).  Outputs overlap neither each other nor an input.  Each call
+ * enqueues one kernel, has no workspace and gives the same bits again.  Errors:
+ * EINVAL for sizes, NULL pointers, alignment, strides or overlap, EUNSUPPORTED for
+ * an unknown dtype. */
 int strata_moe_norm_before(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H,
                            const strata_moe_norm* norm, float* x, uint8_t* codes, uint8_t* scales, void* stream);
 

@@ -836,7 +836,7 @@ NormScale norm_scale(const strata_moe_norm* n) {
 }
 
 // The checks both norm calls share: the stream's rows, and what the norm that
-// follows writes.
+// follows writes.  Arrays of no tokens may be null.
 int check_norm_rows(const void* h, int32_t dtype, int64_t h_stride, int64_t T, int32_t H, const strata_moe_norm* n,
                     const float* x, const uint8_t* codes, const uint8_t* scales) {
     TRY(check_dtype(dtype));
@@ -845,7 +845,7 @@ int check_norm_rows(const void* h, int32_t dtype, int64_t h_stride, int64_t T, i
     TRY(check_stride("h_stride", h_stride, H));
     if (n) {
         TRY(check_norm("norm", n));
-        if (!x && !codes) return fail(STRATA_MOE_EINVAL, "a norm needs x, or codes and scales, to write");
+        if (T && !x && !codes) return fail(STRATA_MOE_EINVAL, "a norm needs x, or codes and scales, to write");
     } else if (x || codes || scales) {
         return fail(STRATA_MOE_EINVAL, "x, codes and scales need a norm");
     }
@@ -1606,7 +1606,8 @@ int strata_moe_norm_after(const void* h, int32_t dtype, int64_t h_stride, int64_
     TRY(check_stride("out_stride", out_stride, H));
     TRY(check_rows("y_rows", b.y_rows));
     if ((b.slot == nullptr) != (b.p == nullptr)) return fail(STRATA_MOE_EINVAL, "slot and p come together");
-    if (b.slot ? (b.K < 1 || b.K > kMaxTopK) : b.K != 0)
+    // slot and p of no tokens may be null at any K
+    if (b.slot ? (b.K < 1 || b.K > kMaxTopK) : (T ? b.K != 0 : b.K < 0 || b.K > kMaxTopK))
         return fail(STRATA_MOE_EINVAL, "K = %d outside [1, %d] with slot, or not 0 without", b.K, kMaxTopK);
     if (!b.slot && b.y_rows < T)
         return fail(STRATA_MOE_EINVAL, "%lld rows of y for %lld tokens", (long long)b.y_rows, (long long)T);

@@ -381,6 +381,48 @@ def test_no_tokens_is_a_no_op(qm):
     assert lib.strata_moe_norm_after(None, 1, 64, 0, 64, ctypes.byref(b), None, 64, None, None, None, None, None) == 0
 
 
+@pytest.mark.parametrize("x,codes", [(None, None), (P[0], None), (None, P[1])])
+def test_no_tokens_with_empty_arrays(qm, x, codes):
+    """Arrays of no rows may be null: an allocation of no bytes is."""
+    lib, n = qm.library(), qm.NormStruct(None, 0.0, 1e-6)
+    scales = codes and P[2]
+    assert lib.strata_moe_norm_before(None, 1, 64, 0, 64, ctypes.byref(n), x, codes, scales, None) == 0
+    for K in (0, 1, 16):
+        b = qm.BranchStruct(None, 64, 0, 1, K, None, None, None, None, 0, 0, 1.0, 1.0)
+        for following in (None, ctypes.byref(n)):
+            o = (x, codes, scales) if following else (None, None, None)
+            assert lib.strata_moe_norm_after(None, 1, 64, 0, 64, ctypes.byref(b), None, 64, following, *o, None) == 0
+    b = qm.BranchStruct(None, 64, 0, 1, 17, None, None, None, None, 0, 0, 1.0, 1.0)
+    rc = lib.strata_moe_norm_after(None, 1, 64, 0, 64, ctypes.byref(b), None, 64, None, None, None, None, None)
+    _refused(qm, rc, -1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [0, 4])
+def test_no_tokens_through_the_binding(qm, K):
+    T, H, I, E = 0, 64, 96, 3
+    f = lambda *a: torch.empty(a, device="cuda")  # noqa: E731
+    u8 = lambda *a: torch.empty(a, dtype=torch.uint8, device="cuda")  # noqa: E731
+    i32 = lambda *a: torch.empty(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    n = qm.Norm(torch.ones(H, device="cuda"))
+    c, s = u8(T, H // 2), u8(T, H // 32)
+    for x, codes, scales in ((f(T, H), None, None), (None, c, s), (f(T, H), c, s)):
+        qm.strata_moe_norm_before(f(T, H), n, x, codes, scales)
+        choice = dict(slot=i32(T, K), p=f(T, K)) if K else {}
+        for gate in (None, f(H), f(T, 1), f(T, H)):
+            for y in (f(T, H), f(5, H)) if K else (f(T, H),):
+                qm.strata_moe_norm_after(f(T, H), y, f(T, H), norm=n, gate=gate, next_norm=n, x=x, codes=codes,
+                                         scales=scales, **choice)
+    codes, scales = qm.strata_moe_mxfp_quantize(f(T, H))
+    assert qm.strata_moe_mxfp_dequantize(codes, scales, f(T, H)).shape == (T, H)
+    w = qm.MxfpWeights(E, I, H).pack(0, u8(0, I, H // 2), u8(0, I, H // 32))
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    for x_rows in (0, 5):
+        out = qm.strata_moe_mxfp_product(u8(x_rows, H // 2), u8(x_rows, H // 32), w, f(0, I), offsets=off, src=i32(0))
+        assert out.shape == (0, I)
+    torch.cuda.synchronize()
+
+
 def test_no_choices_are_not_no_combine(qm):
     """slot and p of [T][0]: their memory is a null pointer, which to the library says that there are none."""
     h = torch.zeros((4, 64))

@@ -449,9 +449,11 @@ int strata_moe_decode(const float* x, const float* router_w, const strata_moe_ex
 int strata_moe_mxfp_quantize(const void* x, int32_t dtype, int64_t x_stride, int64_t rows, int32_t cols,
                              uint8_t* codes, uint8_t* scales, void* stream);
 
-/* The values that codes and scales stand for, into rows of `dtype` (rounded to
- * it; bf16 and fp32 hold them exactly, bf16 except below 2^-133).  Errors:
- * those of strata_moe_mxfp_quantize. */
+/* The values that codes and scales stand for, into rows of `dtype`, rounded to
+ * it.  bf16 and fp32 hold them exactly, but for magnitudes from 4 on at scale byte
+ * 253 and from 2 on at 254: these are past both types, and infinite (rounding
+ * gives no finite value a byte above 252).  Errors: those of
+ * strata_moe_mxfp_quantize. */
 int strata_moe_mxfp_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* out,
                                int32_t dtype, int64_t out_stride, void* stream);
 

@@ -85,6 +85,24 @@ def test_quantize_infinities_and_nan_stay_in_their_block(qm, dtype):
     assert nan.sum() == 96 and nan[0, :32].all() and nan[1, 32:64].all() and nan[2, 96:].all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_every_code_at_every_scale_is_read_back(qm, dtype):
+    """Rounded to the type: infinite past it, subnormal and zero below, NaN at byte 255."""
+    codes = np.broadcast_to(np.arange(32, dtype=np.uint8) % 16, (256, 32))
+    byte = np.arange(256, dtype=np.uint8)[:, None]
+    out = qm.strata_moe_mxfp_dequantize(torch.from_numpy(ref.pack(codes)).cuda(), torch.from_numpy(byte).cuda(),
+                                        torch.empty((256, 32), dtype=dtype).cuda())
+    v = ref.values(codes, byte)
+    want = torch.from_numpy(v).to(dtype)
+    assert torch.equal(torch.isnan(out.cpu()), torch.isnan(want))
+    assert torch.equal(out[:255].cpu(), want[:255])
+    if dtype != torch.float16:  # exact, but for magnitudes 4 and 6 at byte 253 and 2 to 6 at 254
+        past = (byte == 253) & (codes % 8 >= 6) | (byte == 254) & (codes % 8 >= 4)
+        exact = want.double().numpy() == v
+        assert exact[:255][~past[:255]].all() and torch.isinf(want[torch.from_numpy(past)]).all()
+
+
 # ------------------------------------------------------------------- product
 def _operands(rows, cols, n, E, seed, spread=6):
     g = torch.Generator().manual_seed(seed)

@@ -435,6 +435,55 @@ def test_src_outside_x_gives_zeros_whatever_the_weights(qm, rows, n, swiglu):
     assert torch.equal(torch.isnan(out[~outside]), nan[expert[~outside]])
 
 
+# The next three with sizes for the list and for the kernel of many rows: rows, cols, n.
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,n", [(9000, 256, 48), (3000, 256, 600), (3000, 544, 600), (10000, 32, 1000)])
+def test_nan_stays_in_its_row_and_output_of_many(qm, rows, cols, n):
+    xc, xs, wc, ws = _operands(rows, cols, n, 1, seed=23)
+    xs[3, -1], xs[rows - 1, 0], ws[0, 20, 0], ws[0, n - 1, -1] = 255, 255, 255, 255
+    out = torch.empty((rows, n), device="cuda")
+    qm.strata_moe_mxfp_product(xc, xs, qm.MxfpWeights(1, n, cols).pack(0, wc, ws), out)
+    want = torch.zeros((rows, n), dtype=torch.bool, device="cuda")
+    want[3], want[rows - 1], want[:, 20], want[:, n - 1] = True, True, True, True
+    assert torch.equal(torch.isnan(out), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,n", [(9000, 544, 70), (3000, 544, 600), (10000, 32, 1000), (5000, 96, 1000),
+                                         (3000, 608, 600), (3000, 672, 600), (3000, 992, 600), (3001, 1056, 600)])
+def test_many_rows_do_not_depend_on_their_neighbours(qm, rows, cols, n):
+    """Every other row NaN, where a group of 512 ends after 1, 2, 3, 5 and 15 blocks: behind a row's
+    last scale the next row's are read, and left out."""
+    xc, xs, wc, ws = _operands(rows, cols, n, 1, seed=24)
+    w = qm.MxfpWeights(1, n, cols).pack(0, wc, ws)
+    alone = torch.empty((rows, n), device="cuda")
+    _check_product(qm, xc, xs, wc, ws, alone, weights=w)
+    for odd in (1, 0):
+        xs2 = xs.clone()
+        xs2[odd::2] = 255
+        out = qm.strata_moe_mxfp_product(xc, xs2, w, torch.empty((rows, n), device="cuda"))
+        assert torch.equal(out[1 - odd::2], alone[1 - odd::2]) and torch.isnan(out[odd::2]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,n", [(900, 64, 24), (8000, 64, 700), (8000, 544, 700)])
+def test_offsets_of_any_value_with_many_rows(qm, rows, cols, n):
+    """Offsets that fall, are negative or lie past the rows, and offsets with gaps, also with NaN
+    rows and weights beside the rows that have an expert."""
+    xc, xs, wc, ws = _operands(rows, cols, n, 5, seed=25)
+    w = qm.MxfpWeights(5, n, cols).pack(0, wc, ws)
+    buf = torch.full((rows + 64, n), 7.0, device="cuda")
+    off = torch.tensor([-2 ** 31, 4, 2, 2 ** 31 - 1, -7, 3], dtype=torch.int32, device="cuda")
+    qm.strata_moe_mxfp_product(xc, xs, w, buf[:rows], offsets=off)
+    assert torch.all(buf[rows:] == 7.0)
+    x = ref.values(ref.unpack(_np(xc)), _np(xs))[4:]  # rows 4.. are expert 2's alone
+    want, tol = ref.product(x, ref.values(ref.unpack(_np(wc[2])), _np(ws[2])), False)
+    assert np.all(np.abs(_np(buf[4:rows]) - want) <= tol + 2.0 ** -24 * (np.abs(want) + tol))
+    off = torch.tensor([7, 7, 19, 19, rows // 2, rows - 5], dtype=torch.int32, device="cuda")
+    xs[:7], xs[rows - 5:], ws[0], ws[2] = 255, 255, 255, 255
+    _check_product(qm, xc, xs, wc, ws, torch.full((rows, n), 7.0, device="cuda"), offsets=off)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows,n_e", [(3, 1), (50, 8), (3000, 8)])
 def test_repeated_calls_give_the_same_bits(qm, rows, n_e):

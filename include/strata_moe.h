@@ -431,9 +431,10 @@ int strata_moe_decode(const float* x, const float* router_w, const strata_moe_ex
 #define STRATA_MOE_F16 2
 #define STRATA_MOE_BF16 3
 
-/* The format: 32 consecutive values of a row share a power of two; a value is
- * a sign and a magnitude of 0, 0.5, 1, 1.5, 2, 3, 4 or 6 (code bit 3 the sign,
- * bits 2..1 the exponent, bit 0 the mantissa).  Arrays:
+/* The format, MXFP4 of the OCP Microscaling Formats specification (not NVFP4, whose
+ * scales are of 16 values): 32 consecutive values of a row share a power of two; a
+ * value is a sign and a magnitude of 0, 0.5, 1, 1.5, 2, 3, 4 or 6 (code bit 3 the
+ * sign, bits 2..1 the exponent, bit 0 the mantissa).  Arrays:
  *   codes  [rows][cols / 2] bytes, value 2 j in the low half of byte j
  *   scales [rows][cols / 32] bytes, 2^(byte - 127); 255 is NaN
  * cols is a multiple of 32 in [32, 65536], rows in [0, 2^24], codes 16-byte

@@ -23,8 +23,9 @@ constexpr int kThreads = 256;
 // A thread takes 8 consecutive values, 4 threads a block of 32: its largest magnitude
 // goes between them by two exchanges, and neighbouring threads read and write
 // neighbouring bytes.  The memory bounds both ways: 8192 rows of 2560 in fp32 take
-// 14.5 us to round and 16.7 to read back (6.6 and 5.7 TB/s, partly from the last
-// cache), 203 rows of 1056 in bf16 2.4 and 2.2, a launch.
+// 23.7 us to round (4.0 TB/s; 14.5 where the rows are still in the last cache) and
+// 16.7 to read back (5.7 TB/s, the codes from that cache), 203 rows of 1056 in bf16
+// 2.6 and 2.4, a launch.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const T* __restrict__ x, int64_t x_stride, uint32_t runs,
                                                             uint32_t row_runs, int vec, uint8_t* __restrict__ codes,
@@ -90,7 +91,9 @@ __device__ __forceinline__ int tile_row(int tile, int r, int rows, int paired) {
 // One wave per (expert, tile, group of 16 blocks).  A group is four steps: in step
 // s lane l holds row l % 16 and block 4 (l / 16) + s of the group, what the matrix
 // unit reads, so a lane's blocks are neighbours and its scale dword is theirs, byte
-// s for step s.  The last group keeps only the blocks there are (mx_step_at).
+// s for step s.  The last group keeps only the blocks there are (mx_step_at).  The
+// memory bounds it: 512 matrices of 2048 x 2560 take 690 us, 1.43 GB in and out, 4.1
+// TB/s; of 2560 x 1024 322 us, 4.4.
 __global__ __launch_bounds__(64) void pack_kernel(const uint8_t* __restrict__ codes,
                                                   const uint8_t* __restrict__ scales, int rows, int cols, int paired,
                                                   uint8_t* __restrict__ packed, int64_t stride, int64_t tile_bytes) {
@@ -224,7 +227,10 @@ __device__ __forceinline__ v8i operand(v4i q) { return v8i{q[0], q[1], q[2], q[3
 // silu(g) u, silu(g) = g / (1 + exp(-g)).  exp by 2^(-g log2 e), the product in
 // two parts: its rounding alone would cost |g| 2^-24 of the result.  Where the power
 // is 0 or infinite (also g = +-inf, and g past 2.35e38, where the product is) the
-// second part is left out: it is infinite or NaN there itself.
+// second part is left out: it is infinite or NaN there itself.  Rounded in fp32 at
+// each step, with the unit's power and reciprocal (1 ulp each), for speed: fp32
+// outputs of one token's gate/up are 5.0e-8 off in relative terms, 4.6e-8 with
+// PyTorch's exp and a division; rounding to 16 bits hides both.
 __device__ __forceinline__ float swiglu(float g, float u) {
     const float hi = -g * 1.44269502f;
     const float lo = fmaf(-g, 1.44269502f, -hi) + -g * 1.92596303e-8f;
@@ -238,12 +244,12 @@ __device__ __forceinline__ void store_out(const ProductArgs& a, int32_t row, int
     store4_any(a.p.out, a.p.dtype, row * a.p.out_stride, n, a.n_out, a.vec_out4, f);
 }
 
-// Few rows: latency bounds it (one token's ten experts, 2560 -> 2 x 1024: 7.4 us,
-// of which the 28 MB of weights need 5.5; 406 rows of six experts, 544 -> 333:
-// 5.8).  An item is up to 16 rows of an expert times kFewTiles tiles of its
-// weights.  A wave takes up to four steps at a time, so with a wave for every four
-// of them all loads of an item are in flight together; the waves' sums are added
-// in wave order through LDS.
+// Few rows: latency bounds it (one token's ten experts, 2560 -> 2 x 1024: 8.7 us,
+// of which the 28 MB of weights need 5.5, or 7.5 where they are still in the last
+// cache; 406 rows of six experts, 544 -> 333: 5.9).  An item is up to 16 rows of an
+// expert times kFewTiles tiles of its weights.  A wave takes up to four steps at a
+// time, so with a wave for every four of them all loads of an item are in flight
+// together; the waves' sums are added in wave order through LDS.
 // kList: the items of the work list, shared out.  Otherwise a workgroup per row
 // and run, which looks the row's expert up and works if the row begins one of the
 // expert's tiles: no list, no scan, the offsets and the rows' sources in one
@@ -375,12 +381,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(ProductArgs a) {
 // tiles come in pairs: an item of fewer rows leaves out the pairs it lacks.
 //
 // What bounds it: where an expert has a few hundred rows, the memory (8192 tokens,
-// ten of 512 experts, 2560 -> 2 x 1024 SwiGLU: 400 us; it moves 1.97 GB, 4.9 TB/s of a
+// ten of 512 experts, 2560 -> 2 x 1024 SwiGLU: 405 us; it moves 1.97 GB, 4.9 TB/s of a
 // copy's 5.1, of which 1.6 it cannot do without: the rest is rows read again past an
-// L2, 0.26 GB, and weights, 0.09; down 1024 -> 2560: 255 to 263 us, 1.2 GB).  With one
-// matrix, the matrix unit and what feeds it (8192 rows, 4096 -> 4096: 77 us, 3.6
+// L2, 0.26 GB, and weights, 0.09; down 1024 -> 2560: 262 us, 1.2 GB).  With one
+// matrix, the matrix unit and what feeds it (8192 rows, 4096 -> 4096: 78 us, 3.5
 // PFLOP/s; the unit alone reaches 6.7 to 7.3 on random values; without weight loads
-// 63, without rows' 74, without both and the stores 54).
+// 63, without rows' 74, without both and the stores 54): in a step of 128 a CU's two
+// workgroups load 45 KB, some 700 cycles, for 768 of products.
+//
+// All 256 registers are in use: 2 to 4 values, which each item needs once, wait in
+// scratch memory; nothing in the loop over the groups does.
 //
 // What was measured against it (us, the three calls above, 405 / 258 / 77): items of
 // 128 rows with weights two steps ahead 411 / 278 / 77; weights through the compiler's
@@ -840,7 +850,9 @@ hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
     a.vec_out = align % 16 == 0;
     a.vec_out4 = align % (4 * el) == 0;
     // The kernel by the number of its items, at most (us, MI355X; few: a workgroup
-    // per row and run / the list / the tiles of many rows):
+    // per row and run / the list / the tiles of many rows).  The first border lies
+    // between 320 lookups and 640, where the first and the last are level; the
+    // second between the list's 3930 steps and 11520, with none measured nearer.
     //   one token, ten experts, 2560 -> 2 x 1024 (320 lookups)   7.8 / 12.9 / 11.0
     //   two tokens (640)                                        14.8 / 21.1 / 15.3
     //   128 rows, 2560 -> 2560, one matrix (320)                 6.9 /  9.9 /  8.9

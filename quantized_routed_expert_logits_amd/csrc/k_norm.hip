@@ -15,8 +15,8 @@
 // What bounds it: with few tokens the latency of a chain of loads (slots, rows,
 // the norms' sums), with many the memory, as far as enough tokens are in flight
 // per CU to cover that chain.  So a token has few waves with few registers: 8192
-// tokens of 2560, K = 10 bf16 rows, with the next norm and codes, take 153 us (671
-// MB, 4.4 TB/s); runs of 4 columns (twice the waves) took 213, and 5 or 10 rows
+// tokens of 2560, K = 10 bf16 rows, with the next norm and codes, take 152 us (599
+// MB, 3.9 TB/s); runs of 4 columns (twice the waves) took 213, and 5 or 10 rows
 // loaded before the first is used, which costs registers, 183 and 280.
 //
 // All arithmetic is in 64 bits and an output is rounded to fp32, and from there
